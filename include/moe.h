@@ -10,6 +10,12 @@
  *   moe_layer_dbo  all of the above on two micro-batches ("ubatches") overlapped on a
  *                  compute stream and a comm stream (Dual-Batch Overlap)
  *
+ * and, for the rest of a serving step around that layer,
+ *
+ *   moe_kv_write, moe_kv_read  a paged key/value cache (bf16, or e4m3 quantised as written)
+ *   moe_attn_paged             attention of new tokens (one, a draft, a prompt chunk) over it
+ *   moe_draft_verify           drafted tokens against the target's probabilities
+ *
  * The operations follow the problem statement of the vLLM Dual-Batch Overlap pages:
  *   [A] "[Core/DBO][1/N] Add Dual-Batch Overlap mechanism to VLLM", Purpose
  *   [B] "[Core/DBO][2/N] Dual-Batch Overlap add DeepEP High Throughput support and
@@ -66,7 +72,7 @@ typedef enum {
     MOE_ERR_WORKSPACE = 4,   /* workspace missing or smaller than the *_workspace_size query */
     MOE_ERR_CUDA = 5,        /* a CUDA call or launch failed */
     MOE_ERR_CAPACITY = 6,    /* device flag: an expert received more rows than `capacity` */
-    MOE_ERR_BAD_INDEX = 7,   /* device flag: an expert id outside [0, num_experts) */
+    MOE_ERR_BAD_INDEX = 7,   /* device flag: an id (expert, page, slot, token) or length out of range */
     MOE_ERR_TIMEOUT = 8      /* device flag: a bounded device-side wait gave up */
 } moe_status;
 
@@ -390,6 +396,138 @@ MOE_API int32_t moe_stack_schedule(int32_t layers, int32_t two_ubatches, int32_t
                                    int32_t* ops, int32_t max_ops);
 
 MOE_API const char* moe_status_string(moe_status s);
+
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache.  The pages named above run the layer inside a serving step
+ * whose attention keeps such a cache; they give no layout, so this is the library's own.
+ * A pool of num_pages pages; a page holds page_size consecutive tokens of one request for
+ * every key/value head; a request's pages are listed in order in its row of a block table.
+ *   k, v     device, element (page, head, token, d) at
+ *            page*stride_page + head*stride_head + token*stride_token + d (in elements;
+ *            the same strides for both).  Any order of the three is allowed; each stride
+ *            and each pool must be a multiple of 16 bytes (MOE_ERR_ALIGNMENT).
+ *   dtype    MOE_BF16; or MOE_FP8_E4M3: every (token, head) row of head_dim values is
+ *            e4m3 codes under one power-of-two scale 2^s.
+ *   k_scale, v_scale  MOE_FP8_E4M3 only, else NULL: device uint8
+ *            [num_pages][num_heads][page_size], packed, 16-byte aligned.  A byte b stands
+ *            for 2^(b - 127); 255 stands for NaN (the whole row is NaN).
+ * head_dim is 64 or 128; page_size a power of two >= 16; else MOE_ERR_UNSUPPORTED. */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int32_t dtype; /* moe_dtype */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t num_heads; /* key/value heads */
+    int32_t head_dim;
+    int64_t stride_page;
+    int64_t stride_head;
+    int64_t stride_token;
+} moe_kv_cache;
+
+/* ---------------------------------------------------------------------------
+ * moe_kv_write -- stores T tokens' keys and values into their slots, quantising them for an
+ * e4m3 cache: s = the smallest integer with amax <= 448 * 2^s over the row's head_dim
+ * values, kept within [-100, 119] (amax = 0: s = 0), code = x / 2^s rounded to nearest even
+ * and saturated to +-448.  So every code times its scale is an exact bf16 value.  A row with
+ * a NaN gets the scale byte 255.
+ * k, v     device bf16: head h of token t at t*ld + h*head_stride (elements; ld_k for k,
+ *          ld_v for v, head_stride for both), so both may be parts of one projection's
+ *          output.  16-byte aligned rows.
+ * slots    device int64 [T]: page*page_size + offset of each token, all different.  A
+ *          negative slot is skipped (padding); one past the pool sets MOE_ERR_BAD_INDEX.
+ * err_flag device int32 or NULL. */
+MOE_API moe_status moe_kv_write(const moe_kv_cache* cache, int32_t T, const void* k, const void* v, int64_t ld_k,
+                                int64_t ld_v, int64_t head_stride, const int64_t* slots, int32_t* err_flag,
+                                int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_kv_read -- cached tokens back to packed bf16 rows (a prefix taken out of the cache, or
+ * handed to a dense consumer): for request b, tokens [start[b], start[b] + n) with
+ * n = cu_len[b+1] - cu_len[b] go to rows [cu_len[b], cu_len[b+1]) of k_out and v_out.
+ * Exact: an e4m3 code times its scale is a bf16 value.
+ * T        rows of k_out / v_out; rows at or past cu_len[B] are not written.
+ * block_table device int32 [B][table_ld]; a token past the table's width, a page outside
+ *          the pool or a negative start sets MOE_ERR_BAD_INDEX and leaves its row unwritten.
+ * start    device int32 [B];  cu_len device int32 [B+1], not decreasing, cu_len[0] = 0.
+ * k_out, v_out device bf16 [T][num_heads][head_dim]. */
+MOE_API moe_status moe_kv_read(const moe_kv_cache* cache, int32_t B, int32_t T, const int32_t* block_table,
+                               int32_t table_ld, const int32_t* start, const int32_t* cu_len, void* k_out,
+                               void* v_out, int32_t* err_flag, int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_attn_paged -- attention of each request's newest tokens over its cached tokens, the
+ * new ones among them (moe_kv_write comes first).  Request b has the n = cu_q[b+1] - cu_q[b]
+ * query rows cu_q[b] .. and kv_len[b] cached tokens; its row i stands at position
+ * p = kv_len[b] - n + i.  Head h reads key/value head h / (num_q_heads / num_heads).
+ *   s_j = scale * q . k_j  for the tokens j that the row sees:
+ *         0 <= j < kv_len[b], and j <= p if causal, and j > p - window if window > 0
+ *   o   = sum_j softmax(s)_j v_j,   lse = ln sum_j e^(s_j)
+ * A row that sees no token (kv_len[b] = 0, or p < 0 under the causal mask) gets o = 0 and
+ * lse = -inf.  What lies in tokens that no row sees -- the rest of the last page, pages
+ * before the window -- never reaches a result, whatever it holds.  Scores, the softmax's
+ * maximum and sum, and o are held in fp32; the probabilities are rounded to bf16 for the
+ * second product (the sum takes them before that), o once at the end.
+ * Requests may be mixed freely: one new token, a draft, a prompt chunk. */
+typedef struct {
+    const void* q;              /* device bf16: head h of row t at t*q_ld + h*q_head_stride */
+    void* o;                    /* device bf16 (out), likewise */
+    float* lse;                 /* device fp32 [T][num_q_heads] (out) or NULL */
+    int64_t q_ld, q_head_stride, o_ld, o_head_stride; /* elements; rows 16-byte aligned */
+    const int32_t* cu_q;        /* device int32 [B+1], not decreasing, cu_q[0] = 0, cu_q[B] <= T */
+    const int32_t* kv_len;      /* device int32 [B] */
+    const int32_t* block_table; /* device int32 [B][table_ld]: pages in order */
+    int32_t table_ld;
+    int32_t T;                  /* rows of q and o */
+    int32_t B;                  /* requests, at most 8192 */
+    int32_t max_q;              /* upper bounds of the requests' query rows and kv_len; they size */
+    int32_t max_kv;             /* the launch, and a request above one sets MOE_ERR_BAD_INDEX */
+    int32_t num_q_heads;        /* a multiple of the cache's num_heads, at most 64 times it */
+    float scale;
+    int32_t causal;             /* 0 or 1 */
+    int32_t window;             /* 0 = none */
+    int32_t* err_flag;          /* device int32 or NULL */
+    void* workspace;            /* moe_attn_workspace_size bytes, 256-byte aligned.  Zero it once */
+    size_t workspace_bytes;     /* before its first use; every call leaves it ready for the next */
+} moe_attn_args;
+
+/* err_flag: MOE_ERR_BAD_INDEX for a page outside the pool (its tokens read as zeros), a
+ * request above max_q / max_kv or with more tokens than its table row has pages for (its
+ * rows are not written), or rows outside [0, T) (likewise); MOE_ERR_TIMEOUT.  Two calls that
+ * may overlap on the GPU need a workspace each. */
+MOE_API size_t moe_attn_workspace_size(const moe_kv_cache* cache, int32_t num_q_heads);
+MOE_API moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* args, int32_t max_ctas,
+                                  moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_draft_verify -- speculative decoding's acceptance test.  Request b drafted
+ * n = cu_draft[b+1] - cu_draft[b] tokens x_i from the draft's distributions q_i; the target's
+ * distributions at these places and at the one after them are p_0 .. p_n.
+ *   x_i is kept while u_i * q_i(x_i) < p_i(x_i) (products compared exactly); c = how many;
+ *   then one more token is drawn: for c < n from max(p_c - q_c, 0), for c = n from p_n.
+ * The draw is by its cumulative sum in whole numbers, so it does not depend on any order of
+ * summation: w_v = floor(2^40 * min(max(p - q, 0), 1)) with the difference in binary32, the
+ * token is the lowest v with w_0 + .. + w_v > floor(floor(2^24 * u) * W / 2^24), W the sum
+ * over all v (at most 2^64 - 1 for vocab <= 2^23).  If W is 0 (p and q equal, or not finite)
+ * the token is drawn from p_c; if that has no mass either, it is -1 and MOE_ERR_BAD_INDEX
+ * is set.  The result is distributed as the target's own tokens for uniform u in [0, 1).
+ * target   device [cu_draft[B] + B][target_ld]: rows cu_draft[b] + b + i, i = 0 .. n; fp32 or
+ *          bf16 by `dtype`.
+ * draft    device [cu_draft[B]][draft_ld], the same type; or NULL: the draft was
+ *          deterministic (q_i is 1 at x_i, 0 elsewhere).
+ * cu_draft device int32 [B+1], not decreasing, cu_draft[0] = 0.
+ * ids      device int32 [cu_draft[B]]: the x_i (NULL, with u: no request drafted any).  One outside [0, vocab) is refused and sets
+ *          MOE_ERR_BAD_INDEX, and so does a request with n > max_draft (out_len 0).
+ * u, u_draw device fp32 [cu_draft[B]], [B], in [0, 1) (outside it is taken as the nearest).
+ * out_ids  device int32 [B][max_draft + 1] (out): kept tokens, the drawn one, then -1.
+ * out_len  device int32 [B] (out): c + 1.   max_draft <= 255. */
+MOE_API moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t dtype, const void* target,
+                                    int64_t target_ld, const void* draft, int64_t draft_ld,
+                                    const int32_t* cu_draft, const int32_t* ids, const float* u,
+                                    const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err_flag,
+                                    int32_t max_ctas, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_debug_inject_wait -- test hook for the failure path of the bounded device

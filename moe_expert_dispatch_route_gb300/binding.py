@@ -54,6 +54,24 @@ class MoeLayerArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("stride_page", ctypes.c_int64), ("stride_head", ctypes.c_int64), ("stride_token", ctypes.c_int64)]
+
+
+class MoeAttnArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_ld", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("o_ld", ctypes.c_int64),
+                ("o_head_stride", ctypes.c_int64), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_ld", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("err_flag", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 def config(hidden, inter, num_experts, num_shared, top_k, gate=GATE_SOFTMAX, renormalize=1,
            n_group=1, topk_group=1, routed_scale=1.0, dtype=BF16) -> MoeConfig:
     return MoeConfig(hidden, inter, num_experts, num_shared, top_k, gate, int(renormalize), n_group,
@@ -70,6 +88,7 @@ def config_of(wl) -> MoeConfig:
 
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CFG = ctypes.POINTER(MoeConfig)
+_CACHE = ctypes.POINTER(MoeKvCache)
 _SIGS = {
     "moe_route": (_I32, [_CFG, _I32, _P, _P, _P, _P, _I32, _P]),
     "moe_route_hash": (_I32, [_CFG, _I32, _P, _P, _P, _I32, _P, _P, _I32, _P]),
@@ -97,6 +116,11 @@ _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I32]),
     "moe_debug_inject_wait": (_I32, [_I32, _I64]),
     "moe_comm_error": (_I32, [_P, _I32]),
+    "moe_kv_write": (_I32, [_CACHE, _I32, _P, _P, _I64, _I64, _I64, _P, _P, _I32, _P]),
+    "moe_kv_read": (_I32, [_CACHE, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P]),
+    "moe_attn_workspace_size": (_SZ, [_CACHE, _I32]),
+    "moe_attn_paged": (_I32, [_CACHE, ctypes.POINTER(MoeAttnArgs), _I32, _P]),
+    "moe_draft_verify": (_I32, [_I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -308,3 +332,128 @@ def moe_stack_schedule(layers: int, two_ubatches: bool = True, event_before_yiel
     buf = (ctypes.c_int32 * (4 * n))()
     lib().moe_stack_schedule(layers, int(two_ubatches), int(event_before_yield), buf, n)
     return [tuple(buf[4 * i:4 * i + 4]) for i in range(n)]
+
+
+# ---------------------------------------------------------------- serving around the layer
+def _same(what, *pairs):
+    """Raises ValueError unless every (got, want) pair agrees: shapes and types that the C call,
+    which sees pointers only, cannot check."""
+    for got, want in pairs:
+        if got != want:
+            raise ValueError(f"{what}: got {got}, expected {want}")
+
+
+def _vector(what, t, dtype, n):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what}: a packed {dtype} vector of {n} is expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None) -> MoeKvCache:
+    """The cache in pools k and v [pages][heads][page_size][head_dim] (any strides, head_dim
+    contiguous: a pool kept as [pages][page_size][heads][head_dim] is passed transposed).  bf16,
+    or float8_e4m3fn / uint8 codes with packed uint8 scale exponents [pages][heads][page_size].
+    The tensors must outlive the cache."""
+    fp8 = k.dtype in (torch.float8_e4m3fn, torch.uint8)
+    if not fp8 and k.dtype != torch.bfloat16:
+        raise ValueError(f"kv_cache: bf16 or e4m3 pools are expected, got {k.dtype}")
+    if k.dim() != 4 or k.stride(3) != 1:
+        raise ValueError("kv_cache: pools are [pages][heads][page_size][head_dim] with head_dim contiguous")
+    _same("kv_cache: v", (v.dtype, k.dtype), (v.shape, k.shape), (v.stride(), k.stride()))
+    if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+        raise ValueError("kv_cache: e4m3 pools come with scales, bf16 pools without")
+    for s in (k_scale, v_scale):
+        if s is not None:
+            _same("kv_cache: scales", (s.dtype, torch.uint8), (s.shape, k.shape[:3]), (s.is_contiguous(), True))
+    return MoeKvCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), FP8_E4M3 if fp8 else BF16, k.shape[0],
+                      k.shape[2], k.shape[1], k.shape[3], k.stride(0), k.stride(1), k.stride(2))
+
+
+def moe_kv_write(cache: MoeKvCache, k, v, slots, err_flag=None, max_ctas=0, stream=None):
+    """Stores k, v [T][heads][head_dim] (bf16, any token and head strides) at slots int64 [T]."""
+    T = k.shape[0]
+    rows = (T, cache.num_heads, cache.head_dim)
+    if k.shape != rows or v.shape != rows or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise ValueError(f"moe_kv_write: k and v are bf16 {rows}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1 or ks[1] != vs[1]:
+        raise ValueError("moe_kv_write: head_dim is contiguous and the head stride the same for k and v")
+    _vector("moe_kv_write: slots", slots, torch.int64, T)
+    _check(lib().moe_kv_write(ctypes.byref(cache), T, k.data_ptr(), v.data_ptr(), ks[0], vs[0], ks[1],
+                              slots.data_ptr(), _ptr(err_flag), max_ctas, _stream(stream)), "moe_kv_write")
+
+
+def moe_kv_read(cache: MoeKvCache, block_table, start, cu_len, k_out, v_out, err_flag=None, max_ctas=0, stream=None):
+    """Cached tokens [start[b], start[b] + n_b) of every request to rows of k_out, v_out (bf16)."""
+    B, T = start.shape[0], k_out.shape[0]
+    rows = (T, cache.num_heads, cache.head_dim)
+    for t in (k_out, v_out):
+        if t.shape != rows or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"moe_kv_read: outputs are packed bf16 {rows}, got {t.dtype} {tuple(t.shape)}")
+    _table_ok("moe_kv_read", block_table, B)
+    _vector("moe_kv_read: start", start, torch.int32, B)
+    _vector("moe_kv_read: cu_len", cu_len, torch.int32, B + 1)
+    _check(lib().moe_kv_read(ctypes.byref(cache), B, T, _ptr(block_table), block_table.shape[1], _ptr(start),
+                             _ptr(cu_len), _ptr(k_out), _ptr(v_out), _ptr(err_flag), max_ctas, _stream(stream)),
+           "moe_kv_read")
+
+
+def _table_ok(where, t, B):
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous():
+        raise ValueError(f"{where}: the block table is packed int32 [{B}][pages], got {t.dtype} {tuple(t.shape)}")
+
+
+def moe_attn_workspace_size(cache: MoeKvCache, num_q_heads: int) -> int:
+    return int(lib().moe_attn_workspace_size(ctypes.byref(cache), num_q_heads))
+
+
+def attn_args(q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal=True, window=0, lse=None,
+              workspace=None, err_flag=None) -> MoeAttnArgs:
+    """MoeAttnArgs from tensors: q, o bf16 [T][heads][head_dim] (any token and head strides), lse
+    fp32 [T][heads]; workspace: moe_attn_workspace_size bytes, zeroed once before its first use."""
+    T, H, _ = q.shape
+    B = kv_len.shape[0]
+    _same("attn_args: o", (o.shape, q.shape), (o.dtype, torch.bfloat16), (q.dtype, torch.bfloat16))
+    if q.stride(2) != 1 or o.stride(2) != 1:
+        raise ValueError("attn_args: head_dim is contiguous in q and o")
+    _vector("attn_args: cu_q", cu_q, torch.int32, B + 1)
+    _vector("attn_args: kv_len", kv_len, torch.int32, B)
+    _table_ok("attn_args", block_table, B)
+    if lse is not None:
+        _same("attn_args: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
+    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return MoeAttnArgs(_ptr(q), _ptr(o), _ptr(lse), q.stride(0), q.stride(1), o.stride(0), o.stride(1), _ptr(cu_q),
+                       _ptr(kv_len), _ptr(block_table), block_table.shape[1], T, B, max_q, max_kv, H, float(scale),
+                       int(causal), window, _ptr(err_flag), _ptr(workspace), size)
+
+
+def moe_attn_paged(cache: MoeKvCache, args: MoeAttnArgs, max_ctas=0, stream=None):
+    _check(lib().moe_attn_paged(ctypes.byref(cache), ctypes.byref(args), max_ctas, _stream(stream)),
+           "moe_attn_paged")
+
+
+def moe_draft_verify(target, draft, cu_draft, ids, u, u_draw, out_ids, out_len, err_flag=None, max_ctas=0,
+                     stream=None):
+    """Drafted tokens ids against target [N + B][vocab] and draft [N][vocab] (or None) probabilities
+    (fp32 or bf16, rows at any stride) from uniform numbers u [N], u_draw [B]; see moe.h."""
+    B, V = out_len.shape[0], target.shape[1]
+    N = ids.shape[0] if ids is not None else 0
+    if target.dtype not in (torch.float32, torch.bfloat16) or target.stride(1) != 1 or target.shape[0] != N + B:
+        raise ValueError(f"moe_draft_verify: target is fp32 or bf16 [{N + B}][vocab], got {target.dtype} "
+                         f"{tuple(target.shape)}")
+    if draft is not None and (draft.dtype != target.dtype or draft.shape != (N, V) or draft.stride(1) != 1):
+        raise ValueError(f"moe_draft_verify: draft is {target.dtype} [{N}][{V}], got {draft.dtype} "
+                         f"{tuple(draft.shape)}")
+    _vector("moe_draft_verify: cu_draft", cu_draft, torch.int32, B + 1)
+    _vector("moe_draft_verify: u_draw", u_draw, torch.float32, B)
+    _vector("moe_draft_verify: out_len", out_len, torch.int32, B)
+    if N:
+        _vector("moe_draft_verify: ids", ids, torch.int32, N)
+        _vector("moe_draft_verify: u", u, torch.float32, N)
+    if out_ids.dtype != torch.int32 or out_ids.dim() != 2 or out_ids.shape[0] != B or not out_ids.is_contiguous():
+        raise ValueError(f"moe_draft_verify: out_ids is packed int32 [{B}][max_draft + 1]")
+    _check(lib().moe_draft_verify(B, V, out_ids.shape[1] - 1, F32 if target.dtype == torch.float32 else BF16,
+                                  target.data_ptr(), target.stride(0) if target.shape[0] > 1 else V,
+                                  draft.data_ptr() if draft is not None and N else None,
+                                  0 if draft is None else draft.stride(0) if N > 1 else V, cu_draft.data_ptr(),
+                                  _ptr(ids), _ptr(u), u_draw.data_ptr(), out_ids.data_ptr(), out_len.data_ptr(),
+                                  _ptr(err_flag), max_ctas, _stream(stream)), "moe_draft_verify")

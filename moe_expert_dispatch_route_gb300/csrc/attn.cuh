@@ -1,0 +1,369 @@
+// What the paged attention's kernels share: how the work is cut and handed out, and how a
+// query tile whose keys were shared out over several CTAs is put together.
+//
+// Rows.  For one key/value head, a request's queries are (token, group) rows, group fastest:
+// the query heads that read the same keys sit in one tile, so the keys are read once for
+// all of them.  A query tile holds tokens_per_tile tokens of one request.
+//
+// Units.  A unit is one query tile against one tile of kKeyTile keys; masked-out key tiles
+// (after the causal diagonal, before the window) are no units, and a query tile that sees
+// no key at all counts as one.  Units are numbered request by request, head by head, query
+// tile by query tile, key tile by key tile, and CTA c of N = min(grid, U) takes units [c*U/N, (c+1)*U/N): ragged
+// lengths cost no balance, and few rows over a long context are split over the whole GPU by
+// the same rule that gives a CTA many short requests.  Every CTA derives U and its first unit
+// from the lengths on the device, so nothing is read back to the host.
+//
+// Joining.  A query tile whose units span CTAs c0 < .. < c1 is finished by the last of them
+// to arrive: each stores its part (unnormalised o, running maximum, sum) in its own slot of
+// the workspace, then counts itself in counter c0; the last sums the parts in CTA order, so
+// the result does not depend on who came last.  It also clears the counter for the next call.
+#pragma once
+
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace attn {
+
+constexpr int kKeyTile = 128;
+constexpr int kMaxCtas = 1024;     // counters at the front of the workspace
+constexpr int kMaxRows = 256;      // rows of the largest query tile
+
+// One part of a split tile: [rows][head_dim] o, then [rows] (max, sum).
+constexpr size_t kPartBytes = (size_t)kMaxRows * 128 * 4 + (size_t)kMaxRows * 8;
+
+struct Params {
+    const uint16_t* q;
+    uint16_t* o;
+    float* lse;
+    int64_t q_ld, q_head, o_ld, o_head;
+    const int32_t* cu_q;
+    const int32_t* kv_len;
+    const int32_t* table;
+    int table_ld;
+    int T, B, max_q, max_kv;
+    int heads, group;         // key/value heads; query heads per key/value head
+    int tokens_per_tile;
+    int num_pages, page_shift, page_size;
+    float scale_log2;         // scale * log2(e): scores in powers of two
+    int causal, window;
+    int32_t* err;
+    uint32_t* counters;       // [kMaxCtas], all zero between calls
+    uint8_t* parts;           // [grid][2] parts: slot 0 the tile begun last, slot 1 the tile continued
+    int64_t inject_ns;
+};
+
+// A request's lengths; n = 0 for one that is refused (its rows are not written).
+struct Request {
+    int row0, n, kv;
+};
+
+__device__ __forceinline__ Request request(const Params& p, int b, bool report) {
+    Request r;
+    r.row0 = p.cu_q[b];
+    r.n = p.cu_q[b + 1] - r.row0;
+    r.kv = p.kv_len[b];
+    const int64_t room = (int64_t)p.table_ld << p.page_shift;
+    if (r.row0 < 0 || r.n < 0 || r.n > p.max_q || r.row0 > p.T - r.n || r.kv < 0 || r.kv > p.max_kv || r.kv > room) {
+        if (report) set_err(p.err, MOE_ERR_BAD_INDEX);
+        r.n = 0;
+    }
+    return r;
+}
+
+// Key tiles [k0, k1) that query tile i of a request sees, and the keys [lo, hi) among them.
+struct Span {
+    int lo, hi, k0, units;
+};
+__device__ __forceinline__ Span span(const Params& p, const Request& r, int i) {
+    Span s;
+    const int t0 = i * p.tokens_per_tile, t1 = min(t0 + p.tokens_per_tile, r.n);
+    s.hi = p.causal ? min(r.kv, max(r.kv - r.n + t1, 0)) : r.kv;
+    s.lo = p.window > 0 ? max(0, r.kv - r.n + t0 - p.window + 1) : 0;
+    s.k0 = s.lo / kKeyTile;
+    s.units = s.hi > s.lo ? (s.hi + kKeyTile - 1) / kKeyTile - s.k0 : 0;
+    return s;
+}
+__device__ __forceinline__ int tiles_of(const Params& p, const Request& r) {
+    return (r.n + p.tokens_per_tile - 1) / p.tokens_per_tile;
+}
+
+// Where a CTA stands: a query tile and how many of its units lie before and inside the
+// CTA's range.
+struct Cursor {
+    int b, head, tile;
+    int64_t unit;       // number of the tile's unit that comes first in this CTA's range
+    int64_t end;        // of the CTA's range
+    int skip;           // units of the tile before `unit`
+    Request r;
+};
+
+struct Start {  // in shared memory, filled by locate()
+    int b, head, tile, skip;
+    int64_t unit, end, total;
+};
+
+__device__ __forceinline__ int64_t range_begin(int64_t total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int cta_of(int64_t total, int n, int64_t unit) {
+    return (int)(((unit + 1) * n - 1) / total);
+}
+
+__device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+
+// Whole CTA (kThreads threads): the CTA's range of units and the query tile it begins in.
+// scratch: shared, p.B + 32 uint32.  Ends with a barrier; st->unit == st->end: nothing to do.
+template <int kThreads>
+__device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
+    constexpr int kWarps = kThreads / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t* per = scratch + 32;  // units of one head of request b
+    if (p.max_q <= p.tokens_per_tile) {
+        for (int b = tid; b < p.B; b += kThreads) {
+            const Request r = request(p, b, blockIdx.x == 0);
+            per[b] = r.n > 0 ? (uint32_t)max(1, span(p, r, 0).units) : 0u;
+        }
+    } else {
+        for (int b = warp; b < p.B; b += kWarps) {
+            const Request r = request(p, b, blockIdx.x == 0 && lane == 0);
+            const int n = tiles_of(p, r);
+            uint32_t s = 0;
+            for (int i = lane; i < n; i += 32) s += (uint32_t)max(1, span(p, r, i).units);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) per[b] = s;
+        }
+    }
+    __syncthreads();
+    // sums over a run of requests per thread, then over warps
+    const int run = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
+    uint32_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += per[b];
+    const uint32_t incl = warp_incl(mine);
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scratch[w];
+        all += scratch[w];
+    }
+    const int64_t total = (int64_t)all * p.heads;
+    // no CTA's range is empty but those of surplus CTAs: the CTAs of a split tile are consecutive
+    const int n = (int)min((int64_t)gridDim.x, total), me = (int)blockIdx.x;
+    const int64_t u0 = me < n ? range_begin(total, n, me) : total, u1 = me < n ? range_begin(total, n, me + 1) : total;
+    if (tid == 0) {
+        st->unit = u0;
+        st->end = u1;
+        st->total = total;
+    }
+    int64_t at = (int64_t)(before + incl - mine) * p.heads;
+    if (u0 < u1 && u0 >= at && u0 < at + (int64_t)mine * p.heads) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t n = (int64_t)per[b] * p.heads;
+            if (u0 < at + n) {
+                st->b = b;
+                st->head = (int)((u0 - at) / per[b]);
+                st->skip = (int)((u0 - at) % per[b]);  // units of this head's tiles before u0
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    if (u0 < u1 && warp == 0) {
+        const Request r = request(p, st->b, false);
+        const int n = tiles_of(p, r);
+        uint32_t left = (uint32_t)st->skip;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const uint32_t u = i0 + lane < n ? (uint32_t)max(1, span(p, r, i0 + lane).units) : 0u;
+            const uint32_t in = warp_incl(u);
+            const uint32_t over = __ballot_sync(0xffffffffu, in > left);
+            if (over) {
+                const int l = __ffs(over) - 1;
+                const uint32_t ex = __shfl_sync(0xffffffffu, in - u, l);
+                if (lane == 0) {
+                    st->tile = i0 + l;
+                    st->skip = (int)(left - ex);
+                }
+                break;
+            }
+            left -= __shfl_sync(0xffffffffu, in, 31);
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ Cursor cursor(const Params& p, const Start& st) {
+    Cursor c;
+    c.b = st.b;
+    c.head = st.head;
+    c.tile = st.tile;
+    c.unit = st.unit;
+    c.end = st.end;
+    c.skip = st.skip;
+    if (c.unit < c.end) c.r = request(p, c.b, false);
+    return c;
+}
+
+// One stretch of work: a query tile and this CTA's units of it.
+struct Item {
+    int b, head, tile;
+    Request r;
+    Span s;
+    int k0, n;          // first key tile and number of key tiles (0: the tile sees no key)
+    int tokens;         // tokens of the query tile
+    bool whole;         // no other CTA has units of this tile
+    bool first;         // this CTA has the tile's first unit
+    int64_t tile_unit;  // number of the tile's first unit
+    int units;          // the tile's units
+};
+
+__device__ __forceinline__ bool more(const Cursor& c) { return c.unit < c.end; }
+
+// The item at the cursor; the cursor moves behind it.
+__device__ __forceinline__ Item take(const Params& p, Cursor& c) {
+    Item it;
+    it.b = c.b;
+    it.head = c.head;
+    it.tile = c.tile;
+    it.r = c.r;
+    it.s = span(p, c.r, c.tile);
+    it.units = max(1, it.s.units);
+    it.tile_unit = c.unit - c.skip;
+    const int n = (int)min((int64_t)(it.units - c.skip), c.end - c.unit);
+    it.k0 = it.s.k0 + c.skip;
+    it.n = it.s.units ? n : 0;
+    it.first = c.skip == 0;
+    it.whole = n == it.units;
+    it.tokens = min(p.tokens_per_tile, c.r.n - c.tile * p.tokens_per_tile);
+    c.unit += n;
+    c.skip = 0;
+    if (more(c)) {
+        if (++c.tile >= tiles_of(p, c.r)) {
+            c.tile = 0;
+            if (++c.head >= p.heads) {
+                c.head = 0;
+                do {  // the range ends before the requests do
+                    c.r = request(p, ++c.b, false);
+                } while (c.r.n == 0);
+            }
+        }
+    }
+    return it;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The value of a UE8M0 scale byte (255: NaN).
+__device__ __forceinline__ float scale_of(uint8_t b) {
+    return b == 255 ? CUDART_NAN_F : __uint_as_float((uint32_t)b << 23);
+}
+
+// Four e4m3 codes -> the bf16 pairs of bytes (a, b) and (c, d), times 2^-120.
+template <int kSelLo, int kSelHi>
+__device__ __forceinline__ void e4m3_spread(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    // a code's sign, exponent and significand moved to bf16's places: its value times 2^-120
+    // (subnormal codes included), which one exact product undoes
+    const uint32_t x = __byte_perm(w, 0, kSelLo), y = __byte_perm(w, 0, kSelHi);
+    lo = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+    hi = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+constexpr uint32_t kTwo120 = 0x7b807b80u;  // 2^120 twice
+
+__device__ __forceinline__ float* part_o(const Params& p, int cta, int slot) {
+    return reinterpret_cast<float*>(p.parts + ((size_t)cta * 2 + slot) * kPartBytes);
+}
+__device__ __forceinline__ float2* part_ml(const Params& p, int cta, int slot) {
+    return reinterpret_cast<float2*>(p.parts + ((size_t)cta * 2 + slot) * kPartBytes + (size_t)kMaxRows * 128 * 4);
+}
+
+// Row r of a query tile -> its row of q / o and its query head.
+struct RowAt {
+    int token, head;
+};
+__device__ __forceinline__ RowAt row_at(const Params& p, const Item& it, int r) {
+    const int t = r / p.group;
+    return {it.r.row0 + it.tile * p.tokens_per_tile + t, it.head * p.group + (r - t * p.group)};
+}
+
+// kThreads threads (ids 0 .. kThreads-1, each with its barrier): counts this CTA's stored
+// part, and, as the tile's last, forms the output rows from all parts.  `sync` is a barrier
+// over those threads, `last` a shared int.
+template <int kD, int kThreads, typename Sync, typename RowMap>
+__device__ void join(const Params& p, const Item& it, int64_t total, int tid, int* last, Sync sync, int rows,
+                     RowMap row_map) {
+    const int n = (int)min((int64_t)gridDim.x, total);
+    const int c0 = cta_of(total, n, it.tile_unit), c1 = cta_of(total, n, it.tile_unit + it.units - 1);
+    __threadfence();
+    sync();
+    if (tid == 0) {
+        const uint32_t seen = atomicAdd(&p.counters[c0], 1u);
+        *last = seen == (uint32_t)(c1 - c0);
+        if (*last) p.counters[c0] = 0;
+    }
+    sync();
+    const bool mine = *last;
+    if (mine) {
+        __threadfence();
+        constexpr int kPer = kD / 4;  // threads a row: four columns each
+        for (int r = tid / kPer; r < rows; r += kThreads / kPer) {
+            const int d = (tid % kPer) * 4;
+            float m = -CUDART_INF_F, l = 0.0f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = c0; c <= c1; ++c) {
+                const int slot = c == c0 ? 0 : 1;
+                const float2 ml = __ldcg(part_ml(p, c, slot) + r);
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o(p, c, slot) + (size_t)r * kD + d));
+                const float mn = fmaxf(m, ml.x);
+                const float base = mn == -CUDART_INF_F ? 0.0f : mn;
+                const float fa = exp2_fast(m - base), fb = exp2_fast(ml.x - base);
+                l = l * fa + ml.y * fb;
+                o.x = o.x * fa + x.x * fb;
+                o.y = o.y * fa + x.y * fb;
+                o.z = o.z * fa + x.z * fb;
+                o.w = o.w * fa + x.w * fb;
+                m = mn;
+            }
+            const int q = row_map(r);
+            if (q < 0) continue;
+            const RowAt at = row_at(p, it, q);
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+            *reinterpret_cast<uint2*>(p.o + at.token * p.o_ld + at.head * p.o_head + d) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (p.lse && d == 0)
+                p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
+                    l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+        }
+    }
+    sync();
+}
+
+// Tensor map of a pool for boxes of up to kKeyTile tokens of one head: (d, token, head, page).
+bool make_pool_map(CUtensorMap* m, const moe_kv_cache& c, const void* base);
+
+// attn_rows.cu: query tiles of up to 64 rows on mma.sync, the keys of a tile shared by warps
+cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int row_warps, int grid_cap, cudaStream_t st);
+
+}  // namespace attn
+}  // namespace moe

@@ -143,6 +143,24 @@ bool standin_tc_supported(const moe_config& c);
 cudaError_t launch_standin(const moe_config& c, int rows, const void* x, const void* wa, void* out, int grid_cap,
                            cudaStream_t st);
 
+// kv_cache.cu
+cudaError_t launch_kv_write(const moe_kv_cache& c, int T, const void* k, const void* v, int64_t ld_k, int64_t ld_v,
+                            int64_t head_stride, const int64_t* slots, int32_t* err, int grid_cap, cudaStream_t st);
+cudaError_t launch_kv_read(const moe_kv_cache& c, int B, int T, const int32_t* table, int table_ld,
+                           const int32_t* start, const int32_t* cu, void* k_out, void* v_out, int32_t* err,
+                           int grid_cap, cudaStream_t st);
+
+// attn.cu: paged attention (the kernels are in attn_rows.cu and attn_tile.cu)
+constexpr int kMaxRequests = 8192;
+size_t attn_workspace_bytes();
+cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_cap, cudaStream_t st);
+
+// draft_verify.cu
+cudaError_t launch_draft_verify(int B, int V, int max_draft, bool f32, const void* target, int64_t target_ld,
+                                const void* draft, int64_t draft_ld, const int32_t* cu, const int32_t* ids,
+                                const float* u, const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err,
+                                int grid_cap, cudaStream_t st);
+
 // Launches `kern` with programmatic stream serialisation: it may be scheduled while
 // the previous kernel on the stream finishes; the kernel calls pdl_begin() before it
 // touches that kernel's outputs.
