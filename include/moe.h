@@ -466,8 +466,9 @@ MOE_API moe_status moe_kv_read(const moe_kv_cache* cache, int32_t B, int32_t T, 
  *         0 <= j < kv_len[b], and j <= p if causal, and j > p - window if window > 0
  *   o   = sum_j softmax(s)_j v_j,   lse = ln sum_j e^(s_j)
  * A row that sees no token (kv_len[b] = 0, or p < 0 under the causal mask) gets o = 0 and
- * lse = -inf.  What lies in tokens that no row sees -- the rest of the last page, pages
- * before the window -- never reaches a result, whatever it holds.  Scores, the softmax's
+ * lse = -inf.  What lies in tokens that no row of the request sees -- the rest of the last
+ * page, pages before the window -- never reaches a result, whatever it holds.  (A NaN or an
+ * infinity in a value that some of its rows see may make others of its rows NaN.)  Scores, the softmax's
  * maximum and sum, and o are held in fp32; the probabilities are rounded to bf16 for the
  * second product (the sum takes them before that), o once at the end.
  * Requests may be mixed freely: one new token, a draft, a prompt chunk. */
@@ -485,7 +486,7 @@ typedef struct {
     int32_t max_q;              /* upper bounds of the requests' query rows and kv_len; they size */
     int32_t max_kv;             /* the launch, and a request above one sets MOE_ERR_BAD_INDEX */
     int32_t num_q_heads;        /* a multiple of the cache's num_heads, at most 64 times it */
-    float scale;
+    float scale;                /* > 0 */
     int32_t causal;             /* 0 or 1 */
     int32_t window;             /* 0 = none */
     int32_t* err_flag;          /* device int32 or NULL */

@@ -83,7 +83,8 @@ moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, int
     if (s != MOE_OK) return s;
     if (!a || a->T < 0 || a->B < 0 || a->max_q < 0 || a->max_kv < 0 || a->table_ld < 0 || a->window < 0)
         return MOE_ERR_INVALID_ARG;
-    if (a->num_q_heads <= 0 || a->num_q_heads % cache->num_heads || !isfinite(a->scale)) return MOE_ERR_INVALID_ARG;
+    if (a->num_q_heads <= 0 || a->num_q_heads % cache->num_heads || !isfinite(a->scale) || a->scale <= 0.0f)
+        return MOE_ERR_INVALID_ARG;
     if (a->causal != 0 && a->causal != 1) return MOE_ERR_INVALID_ARG;
     if (a->num_q_heads / cache->num_heads > 64 || a->B > kMaxRequests) return MOE_ERR_UNSUPPORTED;
     if (a->T == 0 || a->B == 0 || a->max_q == 0) return MOE_OK;

@@ -64,7 +64,8 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_
     p.inject_ns = wait_injection_ns();
     if (grid_cap > kMaxCtas) grid_cap = kMaxCtas;
     int row_warps = 1;
-    while (row_warps < 8 && (int64_t)a.max_q * p.group > row_warps * 16) row_warps *= 2;
+    while (row_warps < 4 && (int64_t)a.max_q * p.group > row_warps * 16) row_warps *= 2;
+    if ((int64_t)a.max_q * p.group > 64) return launch_tiles(c, p, grid_cap, st);
     return launch_rows(c, p, row_warps, grid_cap, st);
 }
 

@@ -364,6 +364,16 @@ bool make_pool_map(CUtensorMap* m, const moe_kv_cache& c, const void* base);
 
 // attn_rows.cu: query tiles of up to 64 rows on mma.sync, the keys of a tile shared by warps
 cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int row_warps, int grid_cap, cudaStream_t st);
+// attn_tile.cu: query tiles of up to 256 rows on tcgen05
+cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);
+
+// One CTA per SM, and no more CTAs than there can be units.
+inline int grid_for(const Params& p, int grid_cap) {
+    int grid = device_info().num_sms;
+    if (grid > grid_cap) grid = grid_cap;
+    const int64_t units = ((int64_t)p.T / p.tokens_per_tile + p.B) * p.heads * (p.max_kv / kKeyTile + 2);
+    return units < grid ? (int)units : grid;
+}
 
 }  // namespace attn
 }  // namespace moe

@@ -483,12 +483,7 @@ cudaError_t launch_rows_as(const moe_kv_cache& c, const Params& p, int row_warps
 
 cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int row_warps, int grid_cap, cudaStream_t st) {
     p.tokens_per_tile = row_warps * 16 / p.group;
-    int grid = device_info().num_sms;
-    if (grid > grid_cap) grid = grid_cap;
-    // no more CTAs than units there can be
-    const int64_t tiles = (int64_t)p.T / p.tokens_per_tile + p.B;
-    const int64_t units = tiles * p.heads * (p.max_kv / kKeyTile + 2);
-    if (units < grid) grid = (int)units;
+    const int grid = grid_for(p, grid_cap);
     const bool fp8 = c.dtype == MOE_FP8_E4M3;
     if (c.head_dim == 128)
         return fp8 ? launch_rows_as<128, true>(c, p, row_warps, grid, st)

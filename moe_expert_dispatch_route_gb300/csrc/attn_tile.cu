@@ -1,0 +1,690 @@
+// Paged attention for query tiles of up to 256 rows (prompt chunks): bound by the tensor cores,
+// so both products run on tcgen05 with scores, probabilities and output in tensor memory.
+//
+// A query tile is two halves of up to 128 rows over the same key tiles; while the softmax of
+// one half runs, the tensor cores work on the other.  Per half and 128-key tile:
+//   S = Q K^T    A = Q (shared memory), B = K tile (d contiguous), 128 columns of fp32
+//   P = 2^(s - m) in bf16, written over S's first 64 columns: the A operand of
+//   O += P V     A = P (tensor memory), B = V tile with the columns contiguous
+// which fills the 512 columns of tensor memory: S0 | S1 | O0 | O1.  The MMA thread issues
+// PV(j), S(j+1) for each half in turn; tcgen05.mma instructions of one thread execute in
+// order, so S(j+1) may overwrite P(j) without a wait.
+//
+// The running maximum is followed loosely: o and the sum stay relative to an older maximum
+// until a row's new one is 2^8 times as large (in the probabilities), and only then are they
+// rescaled.  The quotient o / sum does not depend on the reference point, fp32 holds both
+// with the same relative precision, and bf16 probabilities up to 256 round like those up to 1.
+// So the rescaling, a round trip of o through registers, happens a few times a row.
+//
+//   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row)
+//   warps 8-11       e4m3 only: turn raw K and V tiles into bf16 tiles
+//   last four warps  one issues the MMAs, one the copies
+#include <cudaTypedefs.h>
+
+#include "attn.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kHalfRows = 128;
+constexpr float kLoose = 8.0f;  // log2 of how far the maximum may run ahead
+
+template <int kD, bool kFp8>
+struct Cfg {
+    static constexpr int kThreads = kFp8 ? 512 : 384;
+    static constexpr int kCols = kD / 64;                             // 128-byte column blocks of a bf16 tile
+    static constexpr int kBlockBytes = kKeyTile * 128;                // one of them
+    static constexpr int kQBytes = 2 * kCols * kHalfRows * 128;       // both halves of Q
+    static constexpr int kEntryBytes = kCols * kBlockBytes;           // a bf16 K or V tile
+    static constexpr int kRawBytes = kKeyTile * kD;                   // an e4m3 one
+    static constexpr int kEntries = kD == 64 ? 8 : kFp8 ? 4 : 5;
+    static constexpr int kRaw = kFp8 ? (kD == 64 ? 4 : 2) : 0;
+    static constexpr int kSmem = 1024 + kQBytes + kEntries * kEntryBytes + kRaw * (kRawBytes + kKeyTile) + 512;
+    static_assert(kSmem <= 232448 - 256, "");
+    static_assert(kEntries * kEntryBytes >= (kMaxRequests + 32) * 4, "locate()'s scratch");
+    // registers per thread after the redistribution: softmax, converters, the rest; their sum
+    // over the block is what it was launched with
+    static constexpr int kRegsSoft = kFp8 ? 192 : 224;
+    static constexpr int kRegsConv = 80;
+    static constexpr int kRegsRest = kFp8 ? 48 : 56;
+};
+
+// ---------------------------------------------------------------- PTX not shared with the FFN
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], A's row i in lane i, two bf16 of K per column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an operand whose M/N index is contiguous (here V: columns contiguous, keys the
+// K index), 128-byte swizzle: blocks of 64 columns kBlock bytes apart (the leading byte
+// offset), groups of 8 keys 1024 bytes apart (the stride byte offset).
+__device__ __forceinline__ uint64_t desc_sw128_mnmajor(uint32_t saddr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(block_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+constexpr uint32_t kIdescBMn = 1u << 16;  // B with its N index contiguous
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+          "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The halves of a query tile: rows, and the key tiles each sees within an item's.
+struct Halves {
+    int rows;     // rows of a full half: tokens_per_tile / 2 * group
+    int count;    // 1 or 2
+    int k0[2], k1[2];
+};
+__device__ __forceinline__ Halves halves(const Params& p, const Item& it) {
+    Halves v;
+    const int half = p.tokens_per_tile / 2;
+    v.rows = half * p.group;
+    v.count = it.tokens > half ? 2 : 1;
+    const int pos0 = it.r.kv - it.r.n + it.tile * p.tokens_per_tile;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int t0 = h * half, t1 = min(t0 + half, it.tokens);
+        const int hi = p.causal ? min(it.r.kv, max(pos0 + t1, 0)) : it.r.kv;
+        const int lo = p.window > 0 ? max(0, pos0 + t0 - p.window + 1) : 0;
+        v.k0[h] = max(lo / kKeyTile, it.k0);
+        v.k1[h] = h < v.count && hi > lo ? min((hi + kKeyTile - 1) / kKeyTile, it.k0 + it.n) : 0;
+    }
+    return v;
+}
+__device__ __forceinline__ bool active(const Halves& v, int h, int kt) { return kt >= v.k0[h] && kt < v.k1[h]; }
+
+template <int kD, bool kFp8>
+__global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
+    attn_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale) {
+    using C = Cfg<kD, kFp8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* ring = qs + C::kQBytes;                          // bf16 tiles, as the MMAs read them
+    uint8_t* raw = ring + C::kEntries * C::kEntryBytes;       // e4m3 tiles
+    uint8_t* scales = raw + C::kRaw * C::kRawBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::kRaw * kKeyTile);
+    uint64_t* empty = full + C::kEntries;
+    uint64_t* raw_full = empty + C::kEntries;
+    uint64_t* raw_empty = raw_full + C::kRaw;
+    uint64_t* q_full = raw_empty + C::kRaw;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;   // [2] scores of a half are in tensor memory
+    uint64_t* p_full = s_full + 2;    // [2] its probabilities are
+    uint64_t* pv_done = p_full + 2;   // [2] they have been multiplied into o
+    uint64_t* done = pv_done + 2;
+    uint64_t* never = done + 1;
+    __shared__ Start start;
+    __shared__ Cursor cursors[2];  // where the two softmax groups stand: not held in registers
+    __shared__ int abort_s, last_s;
+    __shared__ uint32_t tmem_s;
+    volatile int* abort = &abort_s;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kMmaWarp = C::kThreads / 32 - 4, kCopyWarp = kMmaWarp + 1;
+    if (threadIdx.x == 0) {
+        abort_s = 0;
+        for (int i = 0; i < C::kEntries; ++i) {
+            tc::mbar_init(&full[i], kFp8 ? 4 : 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::kRaw; ++i) {
+            tc::mbar_init(&raw_full[i], 1);
+            tc::mbar_init(&raw_empty[i], 4);
+        }
+        tc::mbar_init(q_full, 1);
+        tc::mbar_init(q_empty, 1);
+        for (int h = 0; h < 2; ++h) {
+            tc::mbar_init(&s_full[h], 1);
+            tc::mbar_init(&p_full[h], 4);
+            tc::mbar_init(&pv_done[h], 1);
+        }
+        tc::mbar_init(done, 1);
+        tc::mbar_init(never, 1);
+        tc::fence_barrier_init();
+        tc::prefetch_tmap(&qmap);
+        tc::prefetch_tmap(&kmap);
+        tc::prefetch_tmap(&vmap);
+    }
+    __syncthreads();
+    pdl_begin();
+    if (p.inject_ns > 0) {  // test hook: the failure path of a bounded wait
+        if (threadIdx.x == 0) {
+            tc::wait_on_nothing(never, (uint64_t)p.inject_ns);
+            set_err(p.err, MOE_ERR_TIMEOUT);
+        }
+        return;
+    }
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&tmem_s, 512);
+        tc::tmem_relinquish();
+        tc::tc_fence_before();
+    }
+    locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
+    tc::fence_proxy_async_smem();  // the scratch becomes the copies' destination
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_s;
+    Cursor cur = cursor(p, start);
+    if (threadIdx.x == 0 || threadIdx.x == 128) cursors[threadIdx.x >> 7] = cur;
+    __syncthreads();
+    // a wait that runs out is reported and then passed, here and in every later wait, so that
+    // each barrier is still met; the results are void
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!tc::mbar_wait(bar, parity, abort)) {
+            set_err(p.err, MOE_ERR_TIMEOUT);
+            *abort = 1;
+        }
+    };
+
+    if (warp >= kMmaWarp) {
+        regs_dec<C::kRegsRest>();
+        if (warp == kCopyWarp) {
+            // -------------------------------------------------------- copies
+            int e = 0;
+            uint32_t turn = 0, items = 0;
+            const int box_keys = min(p.page_size, kKeyTile), npg = kKeyTile / box_keys;
+            constexpr int kBoxes = kFp8 ? 1 : C::kCols;  // column blocks of a K or V tile as copied
+            constexpr int kRing = kFp8 ? C::kRaw : C::kEntries;
+            constexpr int kRowBytes = kFp8 ? kD : 128;
+            uint64_t* to_full = kFp8 ? raw_full : full;
+            uint64_t* to_empty = kFp8 ? raw_empty : empty;
+            const int half_tokens = p.tokens_per_tile / 2;
+            while (more(cur)) {
+                const Item it = take(p, cur);
+                if (it.n == 0) continue;
+                const int32_t* table = p.table + (int64_t)it.b * p.table_ld;
+                if (items > 0) wait(q_empty, (items - 1) & 1);
+                if (!*abort && lane == 0) {
+                    const int count = it.tokens > half_tokens ? 2 : 1;
+                    tc::mbar_arrive_expect_tx(q_full, count * C::kCols * half_tokens * p.group * 128);
+                    for (int h = 0; h < count; ++h)
+                        for (int b = 0; b < C::kCols; ++b)
+                            tc::tma_load_3d(qs + (h * C::kCols + b) * kHalfRows * 128, &qmap, q_full, b * 64,
+                                            it.head * p.group,
+                                            it.r.row0 + it.tile * p.tokens_per_tile + h * half_tokens);
+                }
+                ++items;
+                for (int k = 0; k < it.n; ++k) {
+                    const int key0 = (it.k0 + k) * kKeyTile;
+                    // lane i: box i of the tile (page i / kBoxes of it, column block i % kBoxes)
+                    const int pg = lane / kBoxes, blk = lane % kBoxes;
+                    const int key = key0 + pg * box_keys;
+                    const bool want = pg < npg && key < it.s.hi && key + box_keys > it.s.lo;
+                    int page = 0;
+                    if (want) {
+                        page = table[key >> p.page_shift];
+                        if (page < 0 || page >= p.num_pages) {
+                            set_err(p.err, MOE_ERR_BAD_INDEX);
+                            page = p.num_pages;  // past the pool: the copy fills zeros
+                        }
+                    }
+                    const bool scaled = kFp8 && want && page < p.num_pages;
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * kRowBytes) +
+                                           __popc(__ballot_sync(0xffffffffu, scaled)) * box_keys;
+                    const int off = key & (p.page_size - 1);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (turn > 0) wait(&to_empty[e], (turn - 1) & 1);
+                        if (!*abort) {
+                            if (lane == 0) tc::mbar_arrive_expect_tx(&to_full[e], bytes);
+                            __syncwarp();
+                            uint8_t* dst = kFp8 ? raw + e * C::kRawBytes + pg * box_keys * kD
+                                                : ring + e * C::kEntryBytes + blk * C::kBlockBytes + pg * box_keys * 128;
+                            if (want)
+                                tc::tma_load_4d(dst, kv ? &vmap : &kmap, &to_full[e], blk * 64, off, it.head, page);
+                            if (scaled)
+                                tc::bulk_load(scales + e * kKeyTile + pg * box_keys,
+                                              (kv ? v_scale : k_scale) +
+                                                  ((int64_t)page * p.heads + it.head) * p.page_size + off,
+                                              box_keys, &to_full[e]);
+                        }
+                        if (++e == kRing) e = 0, ++turn;
+                    }
+                }
+            }
+            if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
+                for (int i = 0; i < kRing; ++i) {
+                    const uint32_t issued = turn + (i < e ? 1 : 0);
+                    if (issued > 0) tc::mbar_wait_bounded(&to_full[i], (issued - 1) & 1);
+                }
+                if (items > 0) tc::mbar_wait_bounded(q_full, (items - 1) & 1);
+            }
+        } else if (warp == kMmaWarp) {
+            // -------------------------------------------------------- MMAs
+            constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, kKeyTile);
+            constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, kD) | kIdescBMn;
+            int e = 0;
+            uint32_t turn = 0, items = 0;
+            uint32_t np[2] = {0, 0};  // probabilities of half h taken so far
+            auto next = [&] {
+                if (++e == C::kEntries) e = 0, ++turn;
+            };
+            auto scores = [&](int h) {  // S_h = Q_h K^T from the ring entry at e
+                if (lane == 0) {
+                    // a step along K moves a descriptor's start address, its low bits (in 16 bytes)
+                    const uint64_t a = tc::desc_sw128_kmajor(tc::smem_u32(qs + h * C::kCols * kHalfRows * 128));
+                    const uint64_t b = tc::desc_sw128_kmajor(tc::smem_u32(ring + e * C::kEntryBytes));
+#pragma unroll
+                    for (int s = 0; s < kD / 16; ++s) {
+                        const uint32_t off = ((s / 4) * C::kBlockBytes + (s % 4) * 32) >> 4;
+                        tc::mma_bf16(tmem + h * 128, a + off, b + off, kIdescS, s > 0);
+                    }
+                    tc::mma_commit(&s_full[h]);
+                }
+                __syncwarp();
+            };
+            while (more(cur)) {
+                const Item it = take(p, cur);
+                if (it.n == 0) continue;
+                const Halves v = halves(p, it);
+                wait(q_full, items & 1);
+                ++items;
+                wait(&full[e], turn & 1);
+                tc::tc_fence_after();
+                for (int h = 0; h < 2; ++h)
+                    if (active(v, h, it.k0)) scores(h);
+                if (lane == 0) tc::mma_commit(&empty[e]);
+                next();
+                for (int k = 0; k < it.n; ++k) {
+                    const int kt = it.k0 + k;
+                    const int ve = e;
+                    wait(&full[ve], turn & 1);
+                    const int key0 = kt * kKeyTile;
+                    if (!kFp8 && (key0 < it.s.lo || key0 + kKeyTile > it.s.hi)) {
+                        // keys that no row sees hold anything, NaN among it: 0 * NaN would reach o
+                        const int z0 = min(max(it.s.lo - key0, 0), kKeyTile);  // zero [0, z0) and [z1, end)
+                        const int z1 = min(it.s.hi - key0, kKeyTile);
+                        uint4* row = reinterpret_cast<uint4*>(ring + ve * C::kEntryBytes);
+                        for (int i = lane; i < kKeyTile * 8; i += 32)
+                            if (i / 8 < z0 || i / 8 >= z1)
+#pragma unroll
+                                for (int b = 0; b < C::kCols; ++b)
+                                    row[b * (C::kBlockBytes / 16) + i] = make_uint4(0, 0, 0, 0);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    next();
+                    const bool ahead = k + 1 < it.n;
+                    bool waited = false;
+                    for (int h = 0; h < 2; ++h) {
+                        if (active(v, h, kt)) {
+                            wait(&p_full[h], np[h]++ & 1);
+                            tc::tc_fence_after();
+                            if (lane == 0) {
+                                const uint64_t b = desc_sw128_mnmajor(tc::smem_u32(ring + ve * C::kEntryBytes),
+                                                                      C::kBlockBytes);
+#pragma unroll
+                                for (int s = 0; s < kKeyTile / 16; ++s)
+                                    mma_bf16_ta(tmem + 256 + h * 128, tmem + h * 128 + s * 8, b + s * (2048 >> 4),
+                                                kIdescO, s > 0 || kt > v.k0[h]);
+                                tc::mma_commit(&pv_done[h]);
+                            }
+                            __syncwarp();
+                        }
+                        if (ahead && active(v, h, kt + 1)) {
+                            if (!waited) {
+                                wait(&full[e], turn & 1);
+                                tc::tc_fence_after();
+                                waited = true;
+                            }
+                            scores(h);
+                        }
+                    }
+                    if (lane == 0) tc::mma_commit(&empty[ve]);
+                    if (ahead) {
+                        if (lane == 0) tc::mma_commit(&empty[e]);
+                        next();
+                    }
+                }
+                if (lane == 0) tc::mma_commit(q_empty);
+            }
+            if (lane == 0) tc::mma_commit(done);
+            __syncwarp();
+            tc::mbar_wait_bounded(done, 0);
+        }
+    } else if (kFp8 && warp >= 8) {
+        // ------------------------------------------------------------ e4m3 tiles to bf16
+        regs_dec<C::kRegsConv>();
+        int re = 0, e = 0;
+        uint32_t rturn = 0, turn = 0;
+        // A warp turns 32 keys, 8 at a time.  Eight lanes read four chunks of rows r and r ^ 5:
+        // under the 128-byte swizzle both the 16-byte reads and the two 16-byte writes of each
+        // lane fall into different banks.
+        const int quad = lane >> 2, c4 = lane & 3;
+        const int row8 = (quad >> 1) ^ ((quad & 1) * 5);
+        while (more(cur)) {
+            const Item it = take(p, cur);
+            for (int i = 0; i < 2 * it.n; ++i) {  // K, V, K, V, ...
+                const int key0 = (it.k0 + i / 2) * kKeyTile;
+                wait(&raw_full[re], rturn & 1);
+                if (turn > 0) wait(&empty[e], (turn - 1) & 1);
+                const uint8_t* src = raw + re * C::kRawBytes;
+                uint8_t* dst = ring + e * C::kEntryBytes;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int r = (warp - 8) * 32 + g * 8 + row8;
+                    const bool seen = key0 + r >= it.s.lo && key0 + r < it.s.hi;
+                    const int b = seen ? scales[re * kKeyTile + r] : 0;
+                    // code * 2^-120 -> code * 2^(b - 127): in one exact product while 2^(b - 7) is finite
+                    const uint32_t f1 = (uint32_t)(b == 255 ? 0x7fc0 : b > 134 ? 0x7b80 : (b + 120) << 7) * 0x10001u;
+                    const uint32_t f2 = (uint32_t)(b > 134 && b < 255 ? b << 7 : 0x3f80) * 0x10001u;
+#pragma unroll
+                    for (int hf = 0; hf < C::kCols; ++hf) {
+                        uint4 w = *reinterpret_cast<const uint4*>(
+                            src + (kD == 128 ? r * 128 + (((hf * 4 + c4) ^ (r & 7)) << 4)
+                                             : r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)));
+                        uint32_t o[8];
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            e4m3_spread<0x1404, 0x3424>(x[j], o[2 * j], o[2 * j + 1]);
+                            o[2 * j] = mul_bf16x2(o[2 * j], f1);
+                            o[2 * j + 1] = mul_bf16x2(o[2 * j + 1], f1);
+                        }
+                        if (b > 134) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = mul_bf16x2(o[j], f2);
+                        }
+                        if (!seen) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = 0;
+                        }
+                        uint8_t* to = dst + hf * C::kBlockBytes + r * 128;
+                        *reinterpret_cast<uint4*>(to + (((2 * c4) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(to + (((2 * c4 + 1) ^ (r & 7)) << 4)) =
+                            make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&full[e]);
+                    tc::mbar_arrive(&raw_empty[re]);
+                }
+                if (++re == C::kRaw) re = 0, ++rturn;
+                if (++e == C::kEntries) e = 0, ++turn;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax and epilogue
+        regs_inc<C::kRegsSoft>();
+        const int h = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the lanes
+        const uint32_t ts = tmem + h * 128 + lanes, to = tmem + 256 + h * 128 + lanes;
+        auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        uint32_t n = 0;  // key tiles of this half so far
+        for (;;) {
+            Cursor c = cursors[h];
+            if (!more(c)) break;
+            Item it = take(p, c);
+            Halves v = halves(p, it);
+            const int q = h * v.rows + row;  // row of the query tile
+            const bool valid = row < v.rows && q < it.tokens * p.group;
+            int lo = 0, hi = 0;
+            RowAt at = {0, 0};
+            if (valid) {
+                at = row_at(p, it, q);
+                const int pos = it.r.kv - it.r.n + (at.token - it.r.row0);
+                hi = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
+                lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            }
+            // every row of the half sees keys [lo_all, hi_all): no mask there
+            const int half = p.tokens_per_tile / 2;
+            const int pos0 = it.r.kv - it.r.n + it.tile * p.tokens_per_tile + h * half;
+            const int pos1 = pos0 + min(half, it.tokens - h * half) - 1;
+            const int hi_all = p.causal ? min(it.r.kv, pos0 + 1) : it.r.kv;
+            const int lo_all = p.window > 0 ? max(0, pos1 - p.window + 1) : 0;
+            float m = -CUDART_INF_F, l = 0.0f;
+            const int k1 = v.k1[h];
+            for (int kt = v.k0[h]; kt < k1; ++kt, ++n) {
+                const int key0 = kt * kKeyTile;
+                wait(&s_full[h], n & 1);
+                tc::tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc::tmem_ld32(ts + i * 32, s[i]);
+                tc::tmem_wait_ld();
+                if (key0 < lo_all || key0 + kKeyTile > hi_all) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int key = key0 + i * 32 + j;
+                            if (key < lo || key >= hi) s[i][j] = 0xff800000u;
+                        }
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][j]));
+                }
+                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const bool first = kt == v.k0[h];
+                const bool move = (mn - m) * p.scale_log2 > kLoose;  // also from -inf
+                if (first) {
+                    m = mn;
+                } else if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? exp2_fast((m - mn) * p.scale_log2) : 1.0f;
+                    if (move) m = mn;
+                    l *= f;
+                    wait(&pv_done[h], (n - 1) & 1);
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < kD / 16; ++i) {
+                        uint32_t o[16];
+                        tmem_ld16(to + i * 16, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st16(to + i * 16, o);
+                    }
+                }
+                const float base = m == -CUDART_INF_F ? 0.0f : m * p.scale_log2;
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t out[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int a = 2 * i + j / 16, b = (j % 16) * 2;
+                        float2 x = make_float2(__uint_as_float(s[a][b]), __uint_as_float(s[a][b + 1]));
+                        x = fma2(x, sc2, nb2);
+                        x.x = exp2_fast(x.x);
+                        x.y = exp2_fast(x.y);
+                        sum[j & 1] = add2(sum[j & 1], x);
+                        out[j] = cvt_bf16x2(x.x, x.y);
+                    }
+                    tmem_st32(ts + i * 32, out);
+                }
+                tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&p_full[h]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+            }
+            // the item again, from the cursor: its fields would cost registers throughout the loop above
+            __syncwarp();
+            asm volatile("" ::: "memory");
+            c = cursors[h];
+            it = take(p, c);
+            v = halves(p, it);
+            const bool any = v.k0[h] < v.k1[h];
+            if (any) {
+                wait(&pv_done[h], (n - 1) & 1);
+                tc::tc_fence_after();
+            }
+            const float m2 = m * p.scale_log2;  // parts and lse are in powers of two
+            if (it.whole) {
+                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+                uint16_t* out = p.o + at.token * p.o_ld + at.head * p.o_head;
+#pragma unroll
+                for (int i = 0; i < kD / 32; ++i) {
+                    uint32_t o[32];
+                    if (any) {
+                        tc::tmem_ld32(to + i * 32, o);
+                        tc::tmem_wait_ld();
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                w[x] = l == 0.0f ? 0u
+                                                 : cvt_bf16x2(__uint_as_float(o[8 * j + 2 * x]) * inv,
+                                                              __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + i * 32 + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (valid && p.lse)
+                    p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
+                        l == 0.0f ? -CUDART_INF_F : (m2 + log2f(l)) * 0.6931471805599453f;
+            } else {
+                const int slot = it.first ? 0 : 1;
+                float* out = part_o(p, blockIdx.x, slot) + (size_t)(h * kHalfRows + row) * kD;
+#pragma unroll
+                for (int i = 0; i < kD / 32; ++i) {
+                    uint32_t o[32];
+                    if (any) {
+                        tc::tmem_ld32(to + i * 32, o);
+                        tc::tmem_wait_ld();
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(out + i * 32 + j * 4) =
+                                any ? make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3])
+                                    : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (valid) part_ml(p, blockIdx.x, slot)[h * kHalfRows + row] = make_float2(m2, l);
+                const int all = it.tokens * p.group, half_rows = v.rows;
+                join<kD, 256>(p, it, start.total, threadIdx.x, &last_s, sync, v.count * kHalfRows, [=](int r) {
+                    const int in_half = r & (kHalfRows - 1), t = (r / kHalfRows) * half_rows + in_half;
+                    return in_half < half_rows && t < all ? t : -1;
+                });
+            }
+            tc::tc_fence_before();  // o has been read: the next item's first arrival on p_full says so
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
+            if ((threadIdx.x & 127) == 0) cursors[h] = c;
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
+        }
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// q as (d, head, token): a box holds the rows of half a query tile in (token, group) order.
+bool make_q_map(CUtensorMap* m, const Params& p, int head_dim, int half_tokens) {
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encode_fn());
+    if (!enc) return false;
+    const cuuint64_t heads = (cuuint64_t)p.heads * p.group;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, heads, (cuuint64_t)p.T};
+    cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? p.q_head * 2 : head_dim * 2),
+                             (cuuint64_t)(p.T > 1 ? p.q_ld * 2 : head_dim * 2)};
+    cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)half_tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kD, bool kFp8>
+cudaError_t launch_as(const moe_kv_cache& c, const Params& p, int grid, cudaStream_t st) {
+    CUtensorMap qm, km, vm;
+    if (!make_q_map(&qm, p, kD, p.tokens_per_tile / 2) || !make_pool_map(&km, c, c.k) || !make_pool_map(&vm, c, c.v))
+        return cudaErrorInvalidValue;
+    auto kern = attn_tile_kernel<kD, kFp8>;
+    constexpr int smem = Cfg<kD, kFp8>::kSmem;
+    cudaError_t e = ensure_max_dynamic_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, Cfg<kD, kFp8>::kThreads, smem, st, p, qm, km, vm, c.k_scale, c.v_scale);
+}
+
+}  // namespace
+
+cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st) {
+    p.tokens_per_tile = 2 * (kHalfRows / p.group);
+    const int grid = grid_for(p, grid_cap);
+    const bool fp8 = c.dtype == MOE_FP8_E4M3;
+    if (c.head_dim == 128)
+        return fp8 ? launch_as<128, true>(c, p, grid, st) : launch_as<128, false>(c, p, grid, st);
+    return fp8 ? launch_as<64, true>(c, p, grid, st) : launch_as<64, false>(c, p, grid, st);
+}
+
+}  // namespace attn
+}  // namespace moe
