@@ -264,6 +264,36 @@ __device__ __forceinline__ Item take(const Params& p, Cursor& c) {
     return it;
 }
 
+// The copying warp's view of an item's pages: lane i holds table entry first + i of 32, the
+// next 32 are on their way, and so are the next item's first ones, so that no tile waits for
+// its table entries (a load from the table takes longer than a tile's copies may).
+struct Pages {
+    int first, now, then;
+};
+__device__ __forceinline__ int page_entry(const Params& p, const Item& it, int i) {
+    const bool in = it.n > 0 && i >= it.s.lo >> p.page_shift && ((int64_t)i << p.page_shift) < it.s.hi;
+    return in ? __ldg(p.table + (int64_t)it.b * p.table_ld + i) : 0;
+}
+__device__ __forceinline__ Pages pages_of(const Params& p, const Item& it) {
+    Pages g;
+    const int lane = threadIdx.x & 31;
+    g.first = (it.k0 * kKeyTile >> p.page_shift) & ~31;
+    g.now = page_entry(p, it, g.first + lane);
+    g.then = page_entry(p, it, g.first + 32 + lane);
+    return g;
+}
+// The pages of a tile's boxes: lane i gets that of box row `pg` of the tile at key0 (the whole
+// warp calls this; a tile's pages lie in one run of 32).
+__device__ __forceinline__ int page_of(const Params& p, const Item& it, Pages& g, int key0, int pg) {
+    const int i0 = key0 >> p.page_shift;
+    if (i0 >= g.first + 32) {
+        g.first += 32;
+        g.now = g.then;
+        g.then = page_entry(p, it, g.first + 32 + (threadIdx.x & 31));
+    }
+    return __shfl_sync(0xffffffffu, g.now, (i0 - g.first + pg) & 31);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -258,10 +258,20 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             uint64_t* to_full = kFp8 ? raw_full : full;
             uint64_t* to_empty = kFp8 ? raw_empty : empty;
             const int half_tokens = p.tokens_per_tile / 2;
-            while (more(cur)) {
-                const Item it = take(p, cur);
+            bool more_now = more(cur);
+            Item it, after;
+            Pages pages, pages_after;
+            if (more_now) {
+                it = take(p, cur);
+                pages = pages_of(p, it);
+            }
+            for (; more_now; it = after, pages = pages_after) {
+                more_now = more(cur);
+                if (more_now) {
+                    after = take(p, cur);
+                    pages_after = pages_of(p, after);
+                }
                 if (it.n == 0) continue;
-                const int32_t* table = p.table + (int64_t)it.b * p.table_ld;
                 if (items > 0) wait(q_empty, (items - 1) & 1);
                 if (!*abort && lane == 0) {
                     const int count = it.tokens > half_tokens ? 2 : 1;
@@ -279,13 +289,10 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     const int pg = lane / kBoxes, blk = lane % kBoxes;
                     const int key = key0 + pg * box_keys;
                     const bool want = pg < npg && key < it.s.hi && key + box_keys > it.s.lo;
-                    int page = 0;
-                    if (want) {
-                        page = table[key >> p.page_shift];
-                        if (page < 0 || page >= p.num_pages) {
-                            set_err(p.err, MOE_ERR_BAD_INDEX);
-                            page = p.num_pages;  // past the pool: the copy fills zeros
-                        }
+                    int page = page_of(p, it, pages, key0, pg);
+                    if (want && (page < 0 || page >= p.num_pages)) {
+                        set_err(p.err, MOE_ERR_BAD_INDEX);
+                        page = p.num_pages;  // past the pool: the copy fills zeros
                     }
                     const bool scaled = kFp8 && want && page < p.num_pages;
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * kRowBytes) +
