@@ -63,10 +63,8 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_
     p.parts = static_cast<uint8_t*>(a.workspace) + kMaxCtas * sizeof(uint32_t);
     p.inject_ns = wait_injection_ns();
     if (grid_cap > kMaxCtas) grid_cap = kMaxCtas;
-    int row_warps = 1;
-    while (row_warps < 4 && (int64_t)a.max_q * p.group > row_warps * 16) row_warps *= 2;
-    if ((int64_t)a.max_q * p.group > 64) return launch_tiles(c, p, grid_cap, st);
-    return launch_rows(c, p, row_warps, grid_cap, st);
+    const int64_t rows = (int64_t)a.max_q * p.group;
+    return rows <= 64 ? launch_rows(c, p, (int)rows, grid_cap, st) : launch_tiles(c, p, grid_cap, st);
 }
 
 }  // namespace moe

@@ -392,8 +392,8 @@ __device__ void join(const Params& p, const Item& it, int64_t total, int tid, in
 // Tensor map of a pool for boxes of up to kKeyTile tokens of one head: (d, token, head, page).
 bool make_pool_map(CUtensorMap* m, const moe_kv_cache& c, const void* base);
 
-// attn_rows.cu: query tiles of up to 64 rows on mma.sync, the keys of a tile shared by warps
-cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int row_warps, int grid_cap, cudaStream_t st);
+// attn_rows.cu: requests of up to 64 rows a key/value head, on mma.sync, a tile's keys shared by warps
+cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st);
 // attn_tile.cu: query tiles of up to 256 rows on tcgen05
 cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);
 

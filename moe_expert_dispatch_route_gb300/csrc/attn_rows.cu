@@ -1,17 +1,22 @@
-// Paged attention for query tiles of up to 64 rows (a decode step, a draft): the keys and
-// values of a request are read once and HBM bounds the kernel, so the products run on
-// mma.sync, whose fragments keep scores, probabilities and output in registers, and the
-// warps of a CTA share out the keys of a tile instead of padding the rows to 128.
+// Paged attention for query tiles of up to 64 rows (a decode step, a draft).  The keys and
+// values of a request are read once and HBM bounds the work; the products run on mma.sync,
+// whose fragments keep scores, probabilities and output in registers, transposed:
+//   S^T = K Q^T    m = 16 keys, n = 8 rows      O^T += V^T P^T    m = 16 columns, n = 8 rows
+// so that a decode step's 4 to 8 rows fill an instruction's n instead of half of its m, and o
+// takes head_dim / 4 registers for every 8 rows.  Warps share out a tile's keys, each with its
+// own running maximum and sum; they are put together once per query tile.
 //
-//   warps 8-    TMA copies of 128-key K and V tiles, page by page, into a ring
-//   warps 0-7   row group = warp % kRowWarps (16 rows each), key group = warp / kRowWarps;
-//               each keeps a running maximum and sum over its own keys; the key groups are
-//               merged in shared memory once per query tile
+//   12 (or 8) consumer warps   row group x key group x tile group: kRW groups of 8 * kNT rows,
+//                              kKW warps sharing a tile's keys, kTG groups taking tiles in turn
+//   4 warps beside them        copies of K tiles; of V tiles; of their scales (e4m3); query rows
+//                              and what else the consumers need to know of the next query tile
+// A copying warp issues a copy about every 100 cycles and a tile in 16-token pages takes 8 or 16
+// of them, so K and V have a warp each.
 //
-// An e4m3 cache is multiplied in fp16, which holds every e4m3 code exactly, so a conversion
-// instruction turns two codes into an operand; bf16 operands took five (shifts and masks), and
-// the ALU pipe, not HBM, bounded the kernel (48 % busy at 47 % of the copy rate; 64 / 8 heads
-// of 128, 96 requests: 643 us).  What else the products need is put in fp16's range exactly:
+// An e4m3 cache is multiplied in fp16, which holds every e4m3 code exactly: one conversion
+// instruction makes two codes an operand, where bf16 takes five (shifts and masks), and the
+// conversions, not HBM, would bound the kernel.  What else the products need is put into fp16's
+// range exactly:
 //   q   a row is multiplied by a power of two that brings its largest element into [2^14, 2^15);
 //       an element 2^29 below that becomes subnormal, an absolute error of 2^-40 of the largest
 //   p   2^14 p 2^(s - r), s the value's scale exponent, r the largest s so far: at most 2^14, and
@@ -22,28 +27,55 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kConsumers = 256;
-constexpr int kXchgBytes = 4 * 16 * 128 * 4;  // o of four warps
-
-template <int kD, bool kFp8>
-struct Cfg {
-    static constexpr int kElt = kFp8 ? 1 : 2;
-    static constexpr int kEntryBytes = kKeyTile * kD * kElt;
-    static constexpr int kRowBytes = kD * kElt < 128 ? kD * kElt : 128;  // of one swizzled row
-    static constexpr int kHalves = kD * kElt / kRowBytes;
-    static constexpr int kEntries = kD == 64 ? 12 : kFp8 ? 8 : 6;
-    // Copying warps: a warp issues a copy about every 100 cycles, and small pages make many of
-    // them.  Entry i of the stream belongs to warp i % kCopyWarps, and a ring slot always to
-    // the same warp, so that no warp's wait can miss a phase.
-    static constexpr int kCopyWarps = kEntries % 4 == 0 ? 4 : 2;
-    static constexpr int kThreads = kConsumers + 32 * kCopyWarps;
-    static constexpr int kScratchBytes = (kMaxRequests + 32) * 4;  // locate(); the exchange area later
-    static_assert(kScratchBytes >= kXchgBytes, "");
-    static constexpr int kScaleBytes = kFp8 ? kEntries * kKeyTile : 0;
-    static constexpr int kSmem = 1024 + kEntries * kEntryBytes + kScratchBytes + kScaleBytes + 4 * 16 * 8 + 512;
-    static_assert(kSmem <= 232448, "");
+// What the consumers know of a query tile, in shared memory.
+template <int kRows>
+struct TileInfo {
+    Item it;
+    int stop;              // no more tiles
+    int lo_all, hi_all;    // keys that every row sees: no mask there
+    int2 range[kRows];     // the keys a row sees
+    float row_scale[kRows];
 };
 
+template <int kD, bool kFp8, int kNT, int kRW>
+struct Cfg {
+    static constexpr int kElt = kFp8 ? 1 : 2;
+    static constexpr int kRows = 8 * kNT * kRW;
+    // 64 rows: o of a key group takes as much shared memory as a key tile, so there are two
+    static constexpr int kTG = kRW == 4 ? 2 : 3;
+    static constexpr int kKW = kRW == 4 ? 1 : 4 / kRW;
+    static constexpr int kMerged = kKW * kTG;  // key groups to be put together
+    static constexpr int kWarps = kRW * kMerged;
+    static constexpr int kConsumers = 32 * kWarps;
+    static constexpr int kThreads = kConsumers + 128;
+    static constexpr int kWarpKeys = kKeyTile / kKW;
+    static constexpr int kStrips = 2;  // of 16 keys, at a time
+    static constexpr int kChunks = kWarpKeys / (16 * kStrips);
+    static constexpr int kTileBytes = kKeyTile * kD * kElt;  // of K or V
+    static constexpr int kRowBytes = kD * kElt < 128 ? kD * kElt : 128;
+    static constexpr int kHalves = kD * kElt / kRowBytes;  // 128-byte column blocks
+    // stages of K and V: a multiple of kTG, so that a stage always serves the same tile group and
+    // no warp's wait can miss a phase.  192 KB in flight (128 KB for 64 rows) cover HBM's latency.
+    static constexpr int kStages = kRW == 4 ? (kTileBytes == 32768 ? 2 : kTileBytes == 16384 ? 4 : 8)
+                                            : (kTileBytes == 32768 ? 3 : kTileBytes == 16384 ? 6 : 9);
+    static constexpr int kRing = 2 * kStages * kTileBytes;
+    static constexpr int kQStride = 2 * kD + 16;  // bytes; rows fall into different banks
+    static constexpr int kOStride = kD + 4;       // floats; likewise
+    static constexpr int kGroupBytes = kRows * kOStride * 4;  // o of one key group
+    static constexpr int kFixed = 1024 + kRing + (kFp8 ? 2 * kStages * kKeyTile : 0) + kMerged * kRows * 8 + kRows * 8 +
+                                  (4 * kStages + 8) * 8;
+    static constexpr int kInfoBytes = ((int)sizeof(TileInfo<kRows>) + 15) / 16 * 16 + kRows * kQStride;
+    static constexpr int kBudget = 232448 - 256;  // less the static shared memory
+    // the next tile's rows are fetched ahead where there is room for them
+    static constexpr int kInfos = kBudget - kFixed - 2 * kInfoBytes >= kGroupBytes ? 2 : 1;
+    static constexpr int kRoom = (kBudget - kFixed - kInfos * kInfoBytes) / kGroupBytes;
+    static constexpr int kSlots = kRoom < kMerged ? kRoom : kMerged;
+    static constexpr int kSmem = kFixed + kInfos * kInfoBytes + kSlots * kGroupBytes;
+    static_assert(kSlots >= 1 && kStages % kTG == 0, "");
+    static_assert(kRing >= (kMaxRequests + 32) * 4, "locate()'s scratch");
+};
+
+// ---------------------------------------------------------------- fragments
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -56,20 +88,26 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-        "%2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// An 8x8 matrix of 16-bit elements, two of a row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
 }
-
-__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-        "%2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool kF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (kF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+            "%1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+            "%1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Four e4m3 codes as two fp16 pairs.
 __device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -95,31 +133,97 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int kD, bool kFp8, int kRowWarps>
-__global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
+// ---------------------------------------------------------------- query rows
+// One warp: the rows of item `it` into `qs` (bf16 as they are; for an e4m3 cache fp16, scaled,
+// and in the order in which the keys' fragments hold their columns), and the rows' ranges.
+template <int kD, bool kFp8, int kRows>
+__device__ void stage_rows(const Params& p, const Item& it, TileInfo<kRows>* info, uint8_t* qs, int stride) {
+    const int lane = threadIdx.x & 31;
+    const int rows = it.tokens * p.group;
+    constexpr int kPieces = kD / 8;  // 16-byte pieces of a row
+    constexpr int kBatch = 4;
+    if (lane == 0) {
+        info->it = it;
+        info->stop = 0;
+        const int pos0 = it.r.kv - it.r.n + it.tile * p.tokens_per_tile;
+        info->hi_all = p.causal ? min(it.r.kv, pos0 + 1) : it.r.kv;
+        info->lo_all = p.window > 0 ? max(0, pos0 + it.tokens - p.window) : 0;
+    }
+    for (int r = lane; r < kRows; r += 32) {
+        int2 v = make_int2(0, 0);
+        if (r < rows) {
+            const int pos = it.r.kv - it.r.n + it.tile * p.tokens_per_tile + r / p.group;
+            v.y = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
+            v.x = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+        }
+        info->range[r] = v;
+        if (!kFp8) info->row_scale[r] = p.scale_log2;
+    }
+    static_assert(kRows * kPieces % 32 == 0, "");
+    for (int i0 = 0; i0 < kRows * kPieces / 32; i0 += kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = (i0 + b) * 32 + lane, r = i / kPieces;
+            x[b] = make_uint4(0, 0, 0, 0);
+            if (i0 + b < kRows * kPieces / 32 && r < rows) {
+                const RowAt at = row_at(p, it, r);
+                x[b] = __ldg(reinterpret_cast<const uint4*>(p.q + at.token * p.q_ld + at.head * p.q_head) + i % kPieces);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (i0 + b >= kRows * kPieces / 32) break;
+            const int i = (i0 + b) * 32 + lane, r = i / kPieces, piece = i % kPieces;
+            uint8_t* row = qs + r * stride;
+            if (!kFp8) {
+                *reinterpret_cast<uint4*>(row + piece * 16) = x[b];
+                continue;
+            }
+            const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+            uint32_t mx = 0;  // largest magnitude as bf16 bits
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7fff7fffu);
+            mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+            for (int o = kPieces / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // largest element's exponent -> 14, by at most 2^100 (a row of zeros, or of numbers so small
+            // that its scores are 0); in two factors, each a float
+            const int up = min(14 - ((int)(mx >> 7) - 127), 100), u1 = up / 2, u2 = up - u1;
+            uint32_t f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[j] = pack_f16x2(__uint_as_float(w[j] << 16) * pow2(u1) * pow2(u2),
+                                  __uint_as_float(w[j] & 0xffff0000u) * pow2(u1) * pow2(u2));
+            // of 16 columns, 4c and 4c + 1 stand at 2c, 4c + 2 and 4c + 3 at 8 + 2c
+            uint8_t* at = row + (piece >> 1) * 32 + (piece & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = make_uint2(f[0], f[2]);
+            *reinterpret_cast<uint2*>(at + 16) = make_uint2(f[1], f[3]);
+            if (piece == 0) info->row_scale[r] = p.scale_log2 * pow2(-u1) * pow2(-u2);
+        }
+    }
+}
+
+template <int kD, bool kFp8, int kNT, int kRW>
+__global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
     attn_rows_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const uint8_t* __restrict__ k_scale,
                      const uint8_t* __restrict__ v_scale) {
-    using C = Cfg<kD, kFp8>;
-    // With one row warp, two groups of four warps take alternate key tiles: 32 keys a warp at a
-    // time instead of 16 halve what a step costs beside its products.  A ring entry always goes
-    // to the same group (whole tiles in the ring: an even number), so that no warp's wait can
-    // miss a phase; the bf16 ring of head_dim 128 holds three tiles and stays with one group.
-    constexpr int kTileGroups = kRowWarps == 1 && C::kEntries / 2 % 2 == 0 ? 2 : 1;
-    constexpr int kKeyWarps = 8 / kRowWarps / kTileGroups;  // warps sharing a tile's keys
-    constexpr int kMerged = kKeyWarps * kTileGroups;        // key groups of a query row
-    constexpr int kWarpKeys = kKeyTile / kKeyWarps;
-    constexpr int kStrips = kWarpKeys >= 32 ? 2 : 1;        // 16 keys each, at a time
-    constexpr int kChunks = kWarpKeys / (16 * kStrips);
-    constexpr int kSteps = kD / 16;  // k-steps of the first product, column pairs of the second
+    using C = Cfg<kD, kFp8, kNT, kRW>;
+    using Info = TileInfo<C::kRows>;
+    constexpr int kSteps = kD / 16;  // k-steps of the first product, column tiles of the second
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* xchg = ring + C::kEntries * C::kEntryBytes;
-    uint8_t* scales = xchg + C::kScratchBytes;
-    float2* xml = reinterpret_cast<float2*>(scales + C::kScaleBytes);
-    uint64_t* full = reinterpret_cast<uint64_t*>(xml + 4 * 16);
-    uint64_t* empty = full + C::kEntries;
-    uint64_t* never = empty + C::kEntries;
+    float* xchg = reinterpret_cast<float*>(ring + C::kRing);  // o of kSlots key groups
+    uint8_t* infos = reinterpret_cast<uint8_t*>(xchg) + C::kSlots * C::kGroupBytes;
+    uint8_t* scales = infos + C::kInfos * C::kInfoBytes;
+    float2* group_ml = reinterpret_cast<float2*>(scales + (kFp8 ? 2 * C::kStages * kKeyTile : 0));
+    float2* row_ml = group_ml + C::kMerged * C::kRows;
+    uint64_t* full = reinterpret_cast<uint64_t*>(row_ml + C::kRows);  // [stage][K, V]
+    uint64_t* empty = full + 2 * C::kStages;
+    uint64_t* info_full = empty + 2 * C::kStages;
+    uint64_t* info_empty = info_full + 2;
+    uint64_t* never = info_empty + 2;
     __shared__ Start start;
     __shared__ int abort_s, last_s;
     volatile int* abort = &abort_s;
@@ -127,9 +231,13 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         abort_s = 0;
-        for (int i = 0; i < C::kEntries; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 8 / kTileGroups);
+        for (int i = 0; i < 2 * C::kStages; ++i) {
+            tc::mbar_init(&full[i], kFp8 ? 2 : 1);
+            tc::mbar_init(&empty[i], kRW * C::kKW);
+        }
+        for (int i = 0; i < C::kInfos; ++i) {
+            tc::mbar_init(&info_full[i], 32);
+            tc::mbar_init(&info_empty[i], 1);
         }
         tc::mbar_init(never, 1);
         tc::fence_barrier_init();
@@ -145,467 +253,474 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
         }
         return;
     }
-    locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(xchg), &start);
-    Cursor cur = cursor(p, start);
-    if (!more(cur)) return;
+    locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
+    tc::fence_proxy_async_smem();  // the scratch becomes the copies' destination
+    __syncthreads();
+    // a wait that runs out is reported and then passed, here and in every later wait, so that
+    // each barrier is still met; the results are void
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!tc::mbar_wait(bar, parity, abort)) {
+            set_err(p.err, MOE_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        __syncwarp();
+    };
 
-    if (warp >= 8) {
-        // ------------------------------------------------------------ copies
-        int e = 0;
-        uint32_t turn = 0, entry = 0;  // of the stream K, V, K, V, ...
+    if (warp >= C::kWarps) {
+        Cursor cur = cursor(p, start);
+        const int role = warp - C::kWarps;  // 0: K, 1: V, 2: scales, 3: query rows
+        if (role == 3) {
+            uint32_t n = 0;
+            for (bool stop = false; !stop; ++n) {
+                const int buf = n % C::kInfos;
+                uint8_t* at = infos + buf * C::kInfoBytes;
+                Info* info = reinterpret_cast<Info*>(at);
+                stop = !more(cur);
+                Item it;
+                if (!stop) it = take(p, cur);
+                // not cut short by an abort: the consumers meet for every query tile
+                if (n >= C::kInfos && !tc::mbar_wait_bounded(&info_empty[buf], (n / C::kInfos - 1) & 1)) break;
+                __syncwarp();
+                if (stop) {
+                    if (lane == 0) info->stop = 1;
+                } else {
+                    stage_rows<kD, kFp8, C::kRows>(p, it, info, at + C::kInfoBytes - C::kRows * C::kQStride,
+                                                   C::kQStride);
+                }
+                tc::mbar_arrive(&info_full[buf]);
+            }
+            return;
+        }
+        if (role == 2 && !kFp8) return;
         const int box_keys = min(p.page_size, kKeyTile), npg = kKeyTile / box_keys;
-        auto next = [&] {
-            if (++e == C::kEntries) e = 0, ++turn;
-        };
-        bool more_now = true;
-        Item it = take(p, cur);
-        Pages pages = pages_of(p, it);
-        while (more_now) {
-            const bool more_then = more(cur);
-            Item after;
-            Pages pages_after;
-            if (more_then) {
+        int stage = 0;
+        uint32_t turn = 0;
+        bool more_now = more(cur);
+        Item it, after;
+        Pages pages, pages_after;
+        if (more_now) {
+            it = take(p, cur);
+            pages = pages_of(p, it);
+        }
+        for (; more_now; it = after, pages = pages_after) {
+            more_now = more(cur);
+            if (more_now) {
                 after = take(p, cur);
                 pages_after = pages_of(p, after);
             }
             for (int k = 0; k < it.n; ++k) {
                 const int key0 = (it.k0 + k) * kKeyTile;
-                // lane i: box i of the tile (page i / kHalves of it, column half i % kHalves)
-                const int pg = lane / C::kHalves, half = lane % C::kHalves;
-                const int key = key0 + pg * box_keys;
+                // roles 0 and 1: lane i copies box i of the tile (page i / kHalves of it, column block
+                // i % kHalves); role 2: the scales of page i / 2 of it for K (i even) or V
+                const int per = role == 2 ? 2 : C::kHalves;
+                const int pg = lane / per, part = lane % per;
+                const int key = key0 + pg * box_keys, off = key & (p.page_size - 1);
                 const bool want = pg < npg && key < it.s.hi && key + box_keys > it.s.lo;
                 int page = page_of(p, it, pages, key0, pg);
-                if (want && (page < 0 || page >= p.num_pages)) {
-                    set_err(p.err, MOE_ERR_BAD_INDEX);
-                    page = p.num_pages;  // past the pool: the copy fills zeros
-                }
-                const bool scaled = kFp8 && want && half == 0 && page < p.num_pages;
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * C::kRowBytes) +
-                                       __popc(__ballot_sync(0xffffffffu, scaled)) * box_keys;
-                const int off = key & (p.page_size - 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, next()) {
-                    if ((int)(entry++ % C::kCopyWarps) != warp - 8) continue;
-                    if (turn > 0 && !tc::mbar_wait(&empty[e], (turn - 1) & 1, abort)) {
-                        if (lane == 0) set_err(p.err, MOE_ERR_TIMEOUT);
-                        *abort = 1;
+                const bool bad = page < 0 || page >= p.num_pages;
+                if (want && bad) set_err(p.err, MOE_ERR_BAD_INDEX);
+                if (role < 2) {
+                    if (bad) page = p.num_pages;  // past the pool: the copy fills zeros
+                    uint64_t* bar = &full[2 * stage + role];
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * C::kRowBytes);
+                    if (turn > 0) wait(&empty[2 * stage + role], (turn - 1) & 1);
+                    if (!*abort) {
+                        if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (want)
+                            tc::tma_load_4d(ring + (2 * stage + role) * C::kTileBytes +
+                                                (part * kKeyTile + pg * box_keys) * C::kRowBytes,
+                                            role ? &vmap : &kmap, bar, part * (C::kRowBytes / C::kElt), off, it.head,
+                                            page);
+                    }
+                } else {
+                    const uint32_t copied = __ballot_sync(0xffffffffu, want && !bad);
+                    if (turn > 0) {
+                        wait(&empty[2 * stage], (turn - 1) & 1);
+                        wait(&empty[2 * stage + 1], (turn - 1) & 1);
                     }
                     if (!*abort) {
-                        if (lane == 0) tc::mbar_arrive_expect_tx(&full[e], bytes);
+                        if (lane < 2)  // as many pages for K as for V
+                            tc::mbar_arrive_expect_tx(&full[2 * stage + lane], __popc(copied) / 2 * box_keys);
                         __syncwarp();
-                        uint8_t* dst = ring + e * C::kEntryBytes + half * kKeyTile * C::kRowBytes +
-                                       pg * box_keys * C::kRowBytes;
-                        if (want)
-                            tc::tma_load_4d(dst, kv ? &vmap : &kmap, &full[e], half * (C::kRowBytes / C::kElt), off, it.head,
-                                        page);
-                        if (scaled)
-                            tc::bulk_load(scales + e * kKeyTile + pg * box_keys,
-                                          (kv ? v_scale : k_scale) + ((int64_t)page * p.heads + it.head) * p.page_size +
-                                              off,
-                                          box_keys, &full[e]);
+                        if (want && !bad)
+                            tc::bulk_load(scales + (2 * stage + part) * kKeyTile + pg * box_keys,
+                                          (part ? v_scale : k_scale) +
+                                              ((int64_t)page * p.heads + it.head) * p.page_size + off,
+                                          box_keys, &full[2 * stage + part]);
                     }
                 }
+                if (++stage == C::kStages) stage = 0, ++turn;
             }
-            it = after;
-            pages = pages_after;
-            more_now = more_then;
         }
         if (*abort)  // copies still in flight land (or a bounded wait gives up) before the CTA ends
-            for (int i = warp - 8; i < C::kEntries; i += C::kCopyWarps) {
-                const uint32_t issued = turn + (i < e ? 1 : 0);
-                if (issued > 0) tc::mbar_wait_bounded(&full[i], (issued - 1) & 1);
+            for (int i = 0; i < 2 * C::kStages; ++i) {
+                const uint32_t issued = turn + (i / 2 < stage ? 1 : 0);
+                if (issued > 0 && (role == 2 || i % 2 == role)) tc::mbar_wait_bounded(&full[i], (issued - 1) & 1);
             }
         return;
     }
 
     // ---------------------------------------------------------------- consumers
-    const int rg = warp % kRowWarps, kg = warp / kRowWarps % kKeyWarps, tg = warp / kRowWarps / kKeyWarps;
-    const int mg = warp / kRowWarps;  // key group among those that are merged
-    uint32_t tiles = 0;               // key tiles so far
-    const int g = lane >> 2, c = lane & 3;  // fragment row and column
-    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); };
-    int e = 0;
-    uint32_t turn = 0;
-    auto next = [&] {
-        if (++e == C::kEntries) e = 0, ++turn;
-    };
-    auto wait_full = [&] {
-        if (!tc::mbar_wait(&full[e], turn & 1, abort)) {  // goes on without data: every barrier is still met
-            if (lane == 0) set_err(p.err, MOE_ERR_TIMEOUT);
+    const int rg = warp % kRW, mg = warp / kRW, kg = mg % C::kKW, tg = mg / C::kKW;
+    const int g = lane >> 2, c = lane & 3;
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(C::kConsumers) : "memory"); };
+    uint32_t tiles = 0;  // key tiles of the query tiles so far
+    for (uint32_t n = 0;; ++n) {
+        const int buf = n % C::kInfos;
+        const Info* info = reinterpret_cast<const Info*>(infos + buf * C::kInfoBytes);
+        const uint32_t q_addr = tc::smem_u32(info) + C::kInfoBytes - C::kRows * C::kQStride + rg * 8 * kNT * C::kQStride;
+        if (!tc::mbar_wait_bounded(&info_full[buf], (n / C::kInfos) & 1)) {
+            set_err(p.err, MOE_ERR_TIMEOUT);
             *abort = 1;
+            return;  // every consumer waits here, and none past it
         }
-    };
-    while (more(cur)) {
-        const Item it = take(p, cur);
-        const int rows = it.tokens * p.group;
-        // this thread's two rows: what they see, and their query fragments
-        int lo[2], hi[2];
-        uint32_t qf[kSteps][4];
+        __syncwarp();
+        if (info->stop) return;
+        float o[kSteps][kNT][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = rg * 16 + g + 8 * h;
-            lo[h] = hi[h] = 0;
-            const uint16_t* q = nullptr;
-            if (r < rows) {
-                const RowAt at = row_at(p, it, r);
-                const int pos = it.r.kv - it.r.n + (at.token - it.r.row0);
-                hi[h] = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
-                lo[h] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-                q = p.q + at.token * p.q_ld + at.head * p.q_head;
+        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[j][t][i] = 0.0f;
+        // this thread's rows are 8 t + 2 c + x of the row group; m is before row_scale (> 0)
+        float m[kNT][2], l[kNT][2], base[kNT][2], row_scale[kNT][2];
+        int2 range[kNT][2];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = rg * 8 * kNT + t * 8 + c * 2 + x;
+                m[t][x] = -CUDART_INF_F;
+                l[t][x] = base[t][x] = 0.0f;
+                row_scale[t][x] = info->row_scale[r];
+                range[t][x] = info->range[r];
             }
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                // an e4m3 row's fragments hold four neighbouring columns: k order within a step
-                // is the keys' and free otherwise
-                if (kFp8) {
-                    const uint2 w = q ? *reinterpret_cast<const uint2*>(q + s * 16 + c * 4) : make_uint2(0, 0);
-                    qf[s][h] = w.x;
-                    qf[s][2 + h] = w.y;
-                } else {
-                    qf[s][h] = q ? *reinterpret_cast<const uint32_t*>(q + s * 16 + c * 2) : 0u;
-                    qf[s][2 + h] = q ? *reinterpret_cast<const uint32_t*>(q + s * 16 + 8 + c * 2) : 0u;
-                }
-            }
-        }
-        float row_scale[2] = {p.scale_log2, p.scale_log2};
-        if (kFp8) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t mx = 0;  // largest magnitude as bf16 bits
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    mx = __vmaxu2(mx, __vmaxu2(qf[s][h] & 0x7fff7fffu, qf[s][2 + h] & 0x7fff7fffu));
-                mx = max(mx & 0xffffu, mx >> 16);
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // largest element's exponent -> 14; in two factors, each a float
-                const int up = 14 - ((int)(mx >> 7) - 127), u1 = up / 2, u2 = up - u1;
-                row_scale[h] = p.scale_log2 * pow2(-u1) * pow2(-u2);
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int x = 0; x < 4; x += 2) {
-                        const uint32_t w = qf[s][x + h];
-                        qf[s][x + h] = pack_f16x2(__uint_as_float(w << 16) * pow2(u1) * pow2(u2),
-                                                  __uint_as_float(w & 0xffff0000u) * pow2(u1) * pow2(u2));
-                    }
-            }
-        }
+        const int lo_all = info->lo_all, hi_all = info->hi_all, lo_any = info->it.s.lo, hi_any = info->it.s.hi;
+        const int tile0 = info->it.k0, count = info->it.n;
         uint32_t vref = 0;  // e4m3: the largest value scale byte so far
-        float o[kD / 8][4];
-#pragma unroll
-        for (int j = 0; j < kD / 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f}, base[2] = {0.0f, 0.0f};
-        // keys [lo_all, hi_all) are seen by every row of the tile that sees any: no mask there
-        const int pos0 = it.r.kv - it.r.n + it.tile * p.tokens_per_tile;
-        const int hi_all = p.causal ? min(it.r.kv, pos0 + 1) : it.r.kv;
-        const int lo_all = p.window > 0 ? max(0, pos0 + it.tokens - p.window) : 0;
-
-        for (int kt = 0; kt < it.n; ++kt, ++tiles) {
-            if (kTileGroups > 1 && (int)(tiles & 1) != tg) {
-                next();
-                next();
-                continue;
-            }
-            const int ke = e;  // the ring entry of the keys; the values' is the next one
-            wait_full();
-            next();
-            const uint32_t k_addr = tc::smem_u32(ring + ke * C::kEntryBytes);
-            const uint32_t v_addr = tc::smem_u32(ring + e * C::kEntryBytes);
+        for (int kt = (tg + C::kTG - (int)(tiles % C::kTG)) % C::kTG; kt < count; kt += C::kTG) {
+            const uint32_t at = tiles + kt, stage = at % C::kStages, parity = (at / C::kStages) & 1;
+            const uint32_t k_addr = tc::smem_u32(ring + 2 * stage * C::kTileBytes), v_addr = k_addr + C::kTileBytes;
+            const uint8_t* sc_at = scales + 2 * stage * kKeyTile;
+            wait(&full[2 * stage], parity);
 #pragma unroll 1
-            for (int ch = 0; ch < kChunks; ++ch) {
-                const int in0 = kg * kWarpKeys + ch * 16 * kStrips;  // first key within the tile
-                const int key0 = (it.k0 + kt) * kKeyTile + in0;
-                const bool edge = key0 < lo_all || key0 + 16 * kStrips > hi_all;
-                // ---- scores
-                float sc[kStrips][2][4];
+            for (int ch = 0; ch < C::kChunks; ++ch) {
+                const int in0 = kg * C::kWarpKeys + ch * 16 * C::kStrips;  // first key within the tile
+                const int key0 = (tile0 + kt) * kKeyTile + in0;
+                const bool edge = key0 < lo_all || key0 + 16 * C::kStrips > hi_all;
+                // ---- scores: element (key g + 8 (i / 2), row 2 c + i % 2)
+                float s[C::kStrips][kNT][4];
 #pragma unroll
-                for (int st = 0; st < kStrips; ++st)
+                for (int st = 0; st < C::kStrips; ++st)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[st][0][i] = sc[st][1][i] = 0.0f;
-                if (kFp8) {
+                    for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                    for (int s = 0; s < kSteps; s += 2)
+                        for (int i = 0; i < 4; ++i) s[st][t][i] = 0.0f;
 #pragma unroll
-                        for (int st = 0; st < kStrips; ++st) {
-                            uint32_t w[4];  // keys 0-7 and 8-15 of chunk s, then of chunk s + 1
-                            ldsm_x4(w, k_addr + swizzled<C::kRowBytes>(
-                                                    in0 + st * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), s + (lane >> 4)));
+                for (int ks = 0; ks < kSteps; ks += 2) {
+                    uint32_t q[kNT][4];  // two k-steps
 #pragma unroll
-                            for (int u = 0; u < 2; ++u)
+                    for (int t = 0; t < kNT; ++t)
+                        ldsm_x4(q[t], q_addr + (t * 8 + (lane & 7)) * C::kQStride + (2 * ks + (lane >> 3)) * 16);
 #pragma unroll
-                                for (int t = 0; t < 2; ++t) {
-                                    uint32_t b0, b1;
-                                    e4m3x4_f16(w[2 * u + t], b0, b1);
-                                    mma16816_f16(sc[st][t], qf[s + u], b0, b1);
-                                }
+                    for (int st = 0; st < C::kStrips; ++st) {
+                        const int row0 = in0 + st * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+                        uint32_t a[2][4];
+                        if (kFp8) {
+                            uint32_t w[4];  // keys 0-7 and 8-15 of chunk ks, then of chunk ks + 1
+                            ldsm_x4(w, k_addr + swizzled<C::kRowBytes>(row0, ks + (lane >> 4)));
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                e4m3x4_f16(w[2 * u], a[u][0], a[u][2]);
+                                e4m3x4_f16(w[2 * u + 1], a[u][1], a[u][3]);
+                            }
+                        } else {
+                            ldsm_x4(a[0], k_addr + swizzled<C::kRowBytes>(row0, 2 * ks + (lane >> 4)));
+                            ldsm_x4(a[1], k_addr + swizzled<C::kRowBytes>(row0, 2 * ks + 2 + (lane >> 4)));
                         }
-                } else {
 #pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int st = 0; st < kStrips; ++st) {
-                            uint32_t b[4];
-                            ldsm_x4(b, k_addr + swizzled<C::kRowBytes>(in0 + st * 16 + (lane >> 4) * 8 + (lane & 7),
-                                                                       2 * s + ((lane >> 3) & 1)));
-                            mma16816(sc[st][0], qf[s], b[0], b[1]);
-                            mma16816(sc[st][1], qf[s], b[2], b[3]);
-                        }
+                            for (int t = 0; t < kNT; ++t) mma16816<kFp8>(s[st][t], a[u], q[t][2 * u], q[t][2 * u + 1]);
+                    }
                 }
-                // ---- the keys' scales, the mask, the running maximum (before row_scale, which is > 0)
-                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
-                const int mine = in0 + (lane & (16 * kStrips - 1));  // e4m3: the key whose scales this lane looks up
-                const float kscale = kFp8 ? scale_of(scales[ke * kKeyTile + mine]) : 1.0f;
+                // ---- the keys' scales, the mask, the running maximum
+                const float kscale = kFp8 ? scale_of(sc_at[in0 + lane]) : 1.0f;  // lane i: key i's
+                float mx[kNT][2];
 #pragma unroll
-                for (int st = 0; st < kStrips; ++st)
+                for (int t = 0; t < kNT; ++t) mx[t][0] = mx[t][1] = -CUDART_INF_F;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float ks[2];
+                for (int st = 0; st < C::kStrips; ++st)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            ks[x] = kFp8 ? __shfl_sync(0xffffffffu, kscale, st * 16 + t * 8 + c * 2 + x) : 1.0f;
+                    for (int y = 0; y < 2; ++y) {
+                        const float f = kFp8 ? __shfl_sync(0xffffffffu, kscale, st * 16 + y * 8 + g) : 1.0f;
+                        const int key = key0 + st * 16 + y * 8 + g;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
+                        for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float v = sc[st][t][2 * h + x];
-                                if (kFp8) v *= ks[x];
-                                if (edge) {
-                                    const int key = key0 + st * 16 + t * 8 + c * 2 + x;
-                                    if (key < lo[h] || key >= hi[h]) v = -CUDART_INF_F;
-                                }
-                                sc[st][t][2 * h + x] = v;
-                                mx[h] = fmaxf(mx[h], v);
+                            for (int x = 0; x < 2; ++x) {
+                                float v = s[st][t][2 * y + x];
+                                if (kFp8) v *= f;
+                                if (edge && (key < range[t][x].x || key >= range[t][x].y)) v = -CUDART_INF_F;
+                                s[st][t][2 * y + x] = v;
+                                mx[t][x] = fmaxf(mx[t][x], v);
                             }
                     }
-                if (ch == kChunks - 1) {
+                if (ch == C::kChunks - 1) {
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&empty[ke]);
+                    if (lane == 0) tc::mbar_arrive(&empty[2 * stage]);
                 }
-                if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+                bool up = false;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                        const float mn = fmaxf(m[h], mx[h]);
-                        const float f = m[h] == -CUDART_INF_F ? 0.0f : exp2_fast((m[h] - mn) * row_scale[h]);
-                        m[h] = mn;
-                        base[h] = mn == -CUDART_INF_F ? 0.0f : -mn * row_scale[h];
-                        l[h] *= f;
+                for (int t = 0; t < kNT; ++t) up |= mx[t][0] > m[t][0] || mx[t][1] > m[t][1];
+                if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-                        for (int j = 0; j < kD / 8; ++j) {
-                            o[j][2 * h] *= f;
-                            o[j][2 * h + 1] *= f;
+                    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1)
+                                mx[t][x] = fmaxf(mx[t][x], __shfl_xor_sync(0xffffffffu, mx[t][x], w));
+                            const float mn = fmaxf(m[t][x], mx[t][x]);
+                            const float f =
+                                m[t][x] == -CUDART_INF_F ? 0.0f : exp2_fast((m[t][x] - mn) * row_scale[t][x]);
+                            m[t][x] = mn;
+                            base[t][x] = mn == -CUDART_INF_F ? 0.0f : -mn * row_scale[t][x];
+                            l[t][x] *= f;
+#pragma unroll
+                            for (int j = 0; j < kSteps; ++j) {
+                                o[j][t][x] *= f;
+                                o[j][t][2 + x] *= f;
+                            }
                         }
-                    }
                 }
-                // ---- probabilities, then o += p . v
-                if (ch == 0) wait_full();
+                // ---- probabilities
+                if (ch == 0) wait(&full[2 * stage + 1], parity);
                 // keys of this chunk that no row sees hold anything, NaN among it: their values read as 0
-                const bool tail = key0 < it.s.lo || key0 + 16 * kStrips > it.s.hi;
-                float vscale = 1.0f;
+                const bool tail = key0 < lo_any || key0 + 16 * C::kStrips > hi_any;
+                float vscale = 1.0f;  // e4m3: of key `lane`
                 if (kFp8) {
-                    const int key = key0 - in0 + mine;
-                    uint32_t vb = scales[e * kKeyTile + mine];
-                    if (tail && (key < it.s.lo || key >= it.s.hi)) vb = 0;
+                    uint32_t vb = sc_at[kKeyTile + in0 + lane];
+                    if (tail && (key0 + lane < lo_any || key0 + lane >= hi_any)) vb = 0;
                     if (__any_sync(0xffffffffu, vb > vref)) {
                         const uint32_t to = max(vref, __reduce_max_sync(0xffffffffu, vb));
                         const float f = pow2((int)vref - (int)to);
                         vref = to;
 #pragma unroll
-                        for (int j = 0; j < kD / 8; ++j)
+                        for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) o[j][i] *= f;
+                            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[j][t][i] *= f;
                     }
                     const int ex = (int)vb - (int)vref + 14 + 127;
                     vscale = vb == 255 ? CUDART_NAN_F : vb == 0 || ex <= 0 ? 0.0f : __int_as_float(ex << 23);
                 }
+                uint32_t pb[C::kStrips][kNT][2];  // (row g, keys 2c, 2c + 1) and 8 keys further
 #pragma unroll
-                for (int st = 0; st < kStrips; ++st) {
-                    uint32_t a[4];
-                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs 2c, 2c+1 and 8 further
+                for (int st = 0; st < C::kStrips; ++st)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float vs[2];
+                    for (int y = 0; y < 2; ++y) {
+                        const float f = kFp8 ? __shfl_sync(0xffffffffu, vscale, st * 16 + y * 8 + g) : 1.0f;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            vs[x] = kFp8 ? __shfl_sync(0xffffffffu, vscale, st * 16 + t * 8 + c * 2 + x) : 1.0f;
-                        if (tail) {
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int key = key0 + st * 16 + t * 8 + c * 2 + x;
-                                if (key < it.s.lo || key >= it.s.hi) keep[t] &= x ? 0x0000ffffu : 0xffff0000u;
-                            }
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float p0 = exp2_fast(fmaf(sc[st][t][2 * h], row_scale[h], base[h]));
-                            const float p1 = exp2_fast(fmaf(sc[st][t][2 * h + 1], row_scale[h], base[h]));
-                            l[h] += p0 + p1;
-                            a[2 * t + h] = kFp8 ? pack_f16x2(p0 * vs[0], p1 * vs[1]) : pack_bf16x2(p0, p1);
+                        for (int t = 0; t < kNT; ++t) {
+                            const float p0 = exp2_fast(fmaf(s[st][t][2 * y], row_scale[t][0], base[t][0]));
+                            const float p1 = exp2_fast(fmaf(s[st][t][2 * y + 1], row_scale[t][1], base[t][1]));
+                            l[t][0] += p0;
+                            l[t][1] += p1;
+                            pb[st][t][y] = transpose8(kFp8 ? pack_f16x2(p0 * f, p1 * f) : pack_bf16x2(p0, p1));
                         }
                     }
+                // ---- o += p v
 #pragma unroll
-                    for (int j = 0; j < C::kRowBytes * C::kHalves / 16; j += 2) {
-                        uint32_t w[4];  // keys 0-7 and 8-15 of chunk j, then of chunk j + 1
-                        ldsm_x4_t(w, v_addr + swizzled<C::kRowBytes>(in0 + st * 16 + ((lane >> 3) & 1) * 8 + (lane & 7),
-                                                                     j + (lane >> 4)));
+                for (int st = 0; st < C::kStrips; ++st) {
+                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs 2c, 2c + 1 and 8 further
+                    if (tail) {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            if (kFp8) {
-                                // bytes: a pair of keys of an even column, then of the odd one beside it
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int key = key0 + st * 16 + y * 8 + c * 2 + x;
+                                if (key < lo_any || key >= hi_any) keep[y] &= x ? 0x0000ffffu : 0xffff0000u;
+                            }
+                    }
+                    if (kFp8) {
+#pragma unroll
+                        for (int j = 0; j < kSteps; j += 2) {
+                            uint32_t w[4];  // keys 0-7 and 8-15 of chunk j, then of chunk j + 1
+                            ldsm_x4_t(w, v_addr + swizzled<C::kRowBytes>(
+                                                      in0 + st * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), j + (lane >> 4)));
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                // bytes: a pair of keys of column 2 g, then of column 2 g + 1
                                 uint32_t w0 = __byte_perm(w[2 * u], 0, 0x3120), w1 = __byte_perm(w[2 * u + 1], 0, 0x3120);
                                 if (tail) {
                                     w0 &= __byte_perm(keep[0], 0, 0x2020);
                                     w1 &= __byte_perm(keep[1], 0, 0x2020);
                                 }
-                                uint32_t ev0, od0, ev1, od1;
-                                e4m3x4_f16(w0, ev0, od0);
-                                e4m3x4_f16(w1, ev1, od1);
-                                mma16816_f16(o[2 * (j + u)], a, ev0, ev1);
-                                mma16816_f16(o[2 * (j + u) + 1], a, od0, od1);
-                            } else {
-                                if (tail) w[2 * u] &= keep[0], w[2 * u + 1] &= keep[1];
-                                mma16816(o[j + u], a, w[2 * u], w[2 * u + 1]);
+                                uint32_t a[4];
+                                e4m3x4_f16(w0, a[0], a[1]);
+                                e4m3x4_f16(w1, a[2], a[3]);
+#pragma unroll
+                                for (int t = 0; t < kNT; ++t) mma16816<true>(o[j + u][t], a, pb[st][t][0], pb[st][t][1]);
                             }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kSteps; ++j) {
+                            uint32_t a[4];
+                            ldsm_x4_t(a, v_addr + swizzled<C::kRowBytes>(in0 + st * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                                         2 * j + ((lane >> 3) & 1)));
+                            if (tail) a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
+#pragma unroll
+                            for (int t = 0; t < kNT; ++t) mma16816<false>(o[j][t], a, pb[st][t][0], pb[st][t][1]);
                         }
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&empty[e]);
-            next();
+            if (lane == 0) tc::mbar_arrive(&empty[2 * stage + 1]);
+        }
+        tiles += count;
+
+        // ---- put the key groups together: all to the rows' common maximum, then sums in a fixed order
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                m[t][x] *= row_scale[t][x];  // in powers of two
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
+                if (g == 0)
+                    group_ml[mg * C::kRows + rg * 8 * kNT + t * 8 + c * 2 + x] = make_float2(m[t][x], l[t][x]);
+            }
+        sync();
+        if (threadIdx.x < C::kRows) {
+            float rm = -CUDART_INF_F, rl = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C::kMerged; ++i) rm = fmaxf(rm, group_ml[i * C::kRows + threadIdx.x].x);
+#pragma unroll
+            for (int i = 0; i < C::kMerged; ++i) {
+                const float2 v = group_ml[i * C::kRows + threadIdx.x];
+                rl += v.y * exp2_fast(v.x - (rm == -CUDART_INF_F ? 0.0f : rm));
+            }
+            row_ml[threadIdx.x] = make_float2(rm, rl);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) m[h] *= row_scale[h];  // scores in powers of two from here
+        for (int t = 0; t < kNT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
-        if (kFp8) {
-            const int up = (int)vref - 127 - 14, u1 = up / 2, u2 = up - u1;
+            for (int x = 0; x < 2; ++x) {
+                const int r = rg * 8 * kNT + t * 8 + c * 2 + x;
+                float rm = -CUDART_INF_F;
 #pragma unroll
-            for (int j = 0; j < kD / 8; ++j)
+                for (int i = 0; i < C::kMerged; ++i) rm = fmaxf(rm, group_ml[i * C::kRows + r].x);
+                float f = exp2_fast(m[t][x] - (rm == -CUDART_INF_F ? 0.0f : rm)), f2 = 1.0f;
+                if (kFp8) {  // and back from 2^14 2^-r; 0 where this warp had no keys
+                    const int e2 = (int)vref - 127 - 14;
+                    f *= pow2(e2 / 2);
+                    f2 = pow2(e2 - e2 / 2);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * pow2(u1) * pow2(u2);
-        }
-        // ---- merge the key groups: the upper half hands its state to the lower half
-#pragma unroll
-        for (int half = kMerged / 2; half > 0; half >>= 1) {
-            float4* x = reinterpret_cast<float4*>(xchg) + ((mg % half) * kRowWarps + rg) * (kD / 8) * 32;
-            float2* xm = xml + ((mg % half) * kRowWarps + rg) * 16;
-            if (mg >= half && mg < 2 * half) {
-#pragma unroll
-                for (int j = 0; j < kD / 8; ++j) x[j * 32 + lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-                if (c == 0) {
-                    xm[g] = make_float2(m[0], l[0]);
-                    xm[g + 8] = make_float2(m[1], l[1]);
+                for (int j = 0; j < kSteps; ++j) {
+                    o[j][t][x] = o[j][t][x] * f * f2;
+                    o[j][t][2 + x] = o[j][t][2 + x] * f * f2;
                 }
             }
+        // where an element stands: column 16 j + g (+ 8), or 16 j + 2 g (+ 1) from e4m3 pairs
+        constexpr int kColG = kFp8 ? 2 : 1, kColHi = kFp8 ? 1 : 8;
+        float* mine = xchg + (mg % C::kSlots) * (C::kRows * C::kOStride) + (rg * 8 * kNT + c * 2) * C::kOStride + g * kColG;
+        auto put = [&] {
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mine[(t * 8 + (i & 1)) * C::kOStride + j * 16 + (i >> 1) * kColHi] = o[j][t][i];
+        };
+        // kSlots groups at a time hand their o to the first kSlots
+        constexpr int kFirst = (C::kMerged - 1) / C::kSlots * C::kSlots;
+#pragma unroll
+        for (int b = kFirst; b > 0; b -= C::kSlots) {
+            if (mg >= b && mg < b + C::kSlots) put();
             sync();
-            if (mg < half) {
-                float fa[2], fb[2];
+            if (mg < C::kSlots && mg + b < C::kMerged) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 ml = xm[g + 8 * h];
-                    const float mn = fmaxf(m[h], ml.x), b = mn == -CUDART_INF_F ? 0.0f : mn;
-                    fa[h] = exp2_fast(m[h] - b);
-                    fb[h] = exp2_fast(ml.x - b);
-                    m[h] = mn;
-                    l[h] = l[h] * fa[h] + ml.y * fb[h];
-                }
+                for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-                for (int j = 0; j < kD / 8; ++j) {
-                    const float4 v = x[j * 32 + lane];
-                    o[j][0] = o[j][0] * fa[0] + v.x * fb[0];
-                    o[j][1] = o[j][1] * fa[0] + v.y * fb[0];
-                    o[j][2] = o[j][2] * fa[1] + v.z * fb[1];
-                    o[j][3] = o[j][3] * fa[1] + v.w * fb[1];
-                }
+                    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[j][t][i] += mine[(t * 8 + (i & 1)) * C::kOStride + j * 16 + (i >> 1) * kColHi];
             }
             sync();
         }
-        if (mg == 0) {
+        if (mg < C::kSlots) put();
+        sync();
+        const Item& it = info->it;
+        const int rows = it.tokens * p.group;
+        for (int i = threadIdx.x; i < rows * (kD / 4); i += C::kConsumers) {
+            const int r = i / (kD / 4), d = (i % (kD / 4)) * 4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = rg * 16 + g + 8 * h;
-                if (r >= rows) continue;
-                if (it.whole) {
-                    const RowAt at = row_at(p, it, r);
-                    const float inv = l[h] > 0.0f ? 1.0f / l[h] : (l[h] == 0.0f ? 0.0f : l[h]);
-                    uint16_t* out = p.o + at.token * p.o_ld + at.head * p.o_head;
-                    if (kFp8) {
-#pragma unroll
-                        for (int j = 0; j < kD / 16; ++j)
-                            *reinterpret_cast<uint2*>(out + j * 16 + c * 4) =
-                                make_uint2(pack_bf16x2(o[2 * j][2 * h] * inv, o[2 * j + 1][2 * h] * inv),
-                                           pack_bf16x2(o[2 * j][2 * h + 1] * inv, o[2 * j + 1][2 * h + 1] * inv));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kD / 8; ++j)
-                            *reinterpret_cast<uint32_t*>(out + j * 8 + c * 2) =
-                                pack_bf16x2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
-                    }
-                    if (p.lse && c == 0)
-                        p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
-                            l[h] == 0.0f ? -CUDART_INF_F : (m[h] + log2f(l[h])) * 0.6931471805599453f;
-                } else {
-                    const int slot = it.first ? 0 : 1;
-                    float* out = part_o(p, blockIdx.x, slot) + (size_t)r * kD;
-                    if (kFp8) {
-#pragma unroll
-                        for (int j = 0; j < kD / 16; ++j)
-                            *reinterpret_cast<float4*>(out + j * 16 + c * 4) = make_float4(
-                                o[2 * j][2 * h], o[2 * j + 1][2 * h], o[2 * j][2 * h + 1], o[2 * j + 1][2 * h + 1]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kD / 8; ++j)
-                            *reinterpret_cast<float2*>(out + j * 8 + c * 2) =
-                                make_float2(o[j][2 * h], o[j][2 * h + 1]);
-                    }
-                    if (c == 0) part_ml(p, blockIdx.x, slot)[r] = make_float2(m[h], l[h]);
-                }
+            for (int k = 0; k < C::kSlots; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(xchg + (k * C::kRows + r) * C::kOStride + d);
+                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+            }
+            const float2 ml = row_ml[r];
+            if (it.whole) {
+                const RowAt at = row_at(p, it, r);
+                const float inv = ml.y > 0.0f ? 1.0f / ml.y : (ml.y == 0.0f ? 0.0f : ml.y);
+                *reinterpret_cast<uint2*>(p.o + at.token * p.o_ld + at.head * p.o_head + d) =
+                    make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+                if (p.lse && d == 0)
+                    p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
+                        ml.y == 0.0f ? -CUDART_INF_F : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+            } else {
+                const int slot = it.first ? 0 : 1;
+                *reinterpret_cast<float4*>(part_o(p, blockIdx.x, slot) + (size_t)r * kD + d) = a;
+                if (d == 0) part_ml(p, blockIdx.x, slot)[r] = ml;
             }
         }
         if (!it.whole)
-            join<kD, kConsumers>(p, it, start.total, threadIdx.x, &last_s, sync, rows, [](int r) { return r; });
+            join<kD, C::kConsumers>(p, it, start.total, threadIdx.x, &last_s, sync, rows, [](int r) { return r; });
+        else
+            sync();
+        if (threadIdx.x == 0) tc::mbar_arrive(&info_empty[buf]);
     }
 }
 
-template <int kD, bool kFp8, int kRowWarps>
-cudaError_t launch_as(const moe_kv_cache& c, const Params& p, int grid, cudaStream_t st) {
+template <int kD, bool kFp8, int kNT, int kRW>
+cudaError_t launch_as(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st) {
+    using C = Cfg<kD, kFp8, kNT, kRW>;
+    p.tokens_per_tile = C::kRows / p.group;
     CUtensorMap km, vm;
     if (!make_pool_map(&km, c, c.k) || !make_pool_map(&vm, c, c.v)) return cudaErrorInvalidValue;
-    auto kern = attn_rows_kernel<kD, kFp8, kRowWarps>;
-    constexpr int smem = Cfg<kD, kFp8>::kSmem;
-    cudaError_t e = ensure_max_dynamic_smem(kern, smem);
+    auto kern = attn_rows_kernel<kD, kFp8, kNT, kRW>;
+    cudaError_t e = ensure_max_dynamic_smem(kern, C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid, Cfg<kD, kFp8>::kThreads, smem, st, p, km, vm, c.k_scale, c.v_scale);
+    return launch_pdl(kern, grid_for(p, grid_cap), C::kThreads, C::kSmem, st, p, km, vm, c.k_scale, c.v_scale);
 }
 
 template <int kD, bool kFp8>
-cudaError_t launch_rows_as(const moe_kv_cache& c, const Params& p, int row_warps, int grid, cudaStream_t st) {
-    switch (row_warps) {
-        case 1: return launch_as<kD, kFp8, 1>(c, p, grid, st);
-        case 2: return launch_as<kD, kFp8, 2>(c, p, grid, st);
-        default: return launch_as<kD, kFp8, 4>(c, p, grid, st);
-    }
+cudaError_t launch_rows_as(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st) {
+    if (rows <= 8) return launch_as<kD, kFp8, 1, 1>(c, p, grid_cap, st);
+    if (rows <= 16) return launch_as<kD, kFp8, 2, 1>(c, p, grid_cap, st);
+    if (rows <= 32) return launch_as<kD, kFp8, 2, 2>(c, p, grid_cap, st);
+    return launch_as<kD, kFp8, 2, 4>(c, p, grid_cap, st);
 }
 
 }  // namespace
 
-cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int row_warps, int grid_cap, cudaStream_t st) {
-    p.tokens_per_tile = row_warps * 16 / p.group;
-    const int grid = grid_for(p, grid_cap);
+cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st) {
     const bool fp8 = c.dtype == MOE_FP8_E4M3;
     if (c.head_dim == 128)
-        return fp8 ? launch_rows_as<128, true>(c, p, row_warps, grid, st)
-                   : launch_rows_as<128, false>(c, p, row_warps, grid, st);
-    return fp8 ? launch_rows_as<64, true>(c, p, row_warps, grid, st)
-               : launch_rows_as<64, false>(c, p, row_warps, grid, st);
+        return fp8 ? launch_rows_as<128, true>(c, p, rows, grid_cap, st)
+                   : launch_rows_as<128, false>(c, p, rows, grid_cap, st);
+    return fp8 ? launch_rows_as<64, true>(c, p, rows, grid_cap, st)
+               : launch_rows_as<64, false>(c, p, rows, grid_cap, st);
 }
 
 }  // namespace attn
