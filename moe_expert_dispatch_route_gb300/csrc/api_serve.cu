@@ -93,8 +93,11 @@ moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, int
     if (!aligned16(a->q) || !aligned16(a->o) || a->q_ld % 8 || a->q_head_stride % 8 || a->o_ld % 8 ||
         a->o_head_stride % 8)
         return MOE_ERR_ALIGNMENT;
-    // work is counted per key/value head in 32 bits
-    if (((int64_t)a->T + a->B) * (a->max_kv / 128 + 2) > (int64_t)UINT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // work is counted in 31 bits: tiles of as few tokens as any kernel takes, against tiles of keys
+    const int64_t group = a->num_q_heads / cache->num_heads, rows = a->max_q * group;
+    const int64_t tokens = rows > 64 ? 128 / group * 2 : (rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64) / group;
+    if ((a->T / tokens + a->B) * cache->num_heads > INT32_MAX / ((int64_t)a->max_kv / 128 + 2))
+        return MOE_ERR_UNSUPPORTED;
     if (!a->workspace || a->workspace_bytes < attn_workspace_bytes()) return MOE_ERR_WORKSPACE;
     if (!aligned_to(a->workspace, 256)) return MOE_ERR_ALIGNMENT;
     return cuda_status(launch_attn(*cache, *a, grid_cap_of(max_ctas), (cudaStream_t)stream));

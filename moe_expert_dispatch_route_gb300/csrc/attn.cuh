@@ -8,8 +8,8 @@
 // Units.  A unit is one query tile against one tile of kKeyTile keys; masked-out key tiles
 // (after the causal diagonal, before the window) are no units, and a query tile that sees
 // no key at all counts as one.  Units are numbered request by request, head by head, query
-// tile by query tile, key tile by key tile, and CTA c of N = min(grid, U) takes units [c*U/N, (c+1)*U/N): ragged
-// lengths cost no balance, and few rows over a long context are split over the whole GPU by
+// tile by query tile, key tile by key tile, and each of the N = min(grid, U) CTAs takes a run of U/N of them, rounded up for the first
+// U mod N: ragged lengths cost no balance, and few rows over a long context are split over the whole GPU by
 // the same rule that gives a CTA many short requests.  Every CTA derives U and its first unit
 // from the lengths on the device, so nothing is read back to the host.
 //
@@ -95,20 +95,22 @@ __device__ __forceinline__ int tiles_of(const Params& p, const Request& r) {
 // CTA's range.
 struct Cursor {
     int b, head, tile;
-    int64_t unit;       // number of the tile's unit that comes first in this CTA's range
-    int64_t end;        // of the CTA's range
+    int unit;           // number of the tile's unit that comes first in this CTA's range
+    int end;            // of the CTA's range
     int skip;           // units of the tile before `unit`
     Request r;
 };
 
 struct Start {  // in shared memory, filled by locate()
     int b, head, tile, skip;
-    int64_t unit, end, total;
+    int unit, end;
+    int each, more;  // units of a CTA; the first `more` CTAs have one more
 };
 
-__device__ __forceinline__ int64_t range_begin(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int cta_of(int64_t total, int n, int64_t unit) {
-    return (int)(((unit + 1) * n - 1) / total);
+// The CTA that has unit u.
+__device__ __forceinline__ int cta_of(const Start& st, int u) {
+    const uint32_t first = (uint32_t)st.more * (st.each + 1), v = (uint32_t)u;
+    return v < first ? v / (st.each + 1) : st.more + (v - first) / st.each;
 }
 
 __device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
@@ -159,26 +161,28 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
         if (w < warp) before += scratch[w];
         all += scratch[w];
     }
-    const int64_t total = (int64_t)all * p.heads;
+    const uint32_t total = all * (uint32_t)p.heads;  // host: below 2^31
     // no CTA's range is empty but those of surplus CTAs: the CTAs of a split tile are consecutive
-    const int n = (int)min((int64_t)gridDim.x, total), me = (int)blockIdx.x;
-    const int64_t u0 = me < n ? range_begin(total, n, me) : total, u1 = me < n ? range_begin(total, n, me + 1) : total;
+    const uint32_t n = min((uint32_t)gridDim.x, total), me = blockIdx.x;
+    const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
+    const uint32_t u0 = me < n ? me * each + min(me, rest) : total, u1 = me < n ? u0 + each + (me < rest) : total;
     if (tid == 0) {
-        st->unit = u0;
-        st->end = u1;
-        st->total = total;
+        st->unit = (int)u0;
+        st->end = (int)u1;
+        st->each = (int)each;
+        st->more = (int)rest;
     }
-    int64_t at = (int64_t)(before + incl - mine) * p.heads;
-    if (u0 < u1 && u0 >= at && u0 < at + (int64_t)mine * p.heads) {
+    uint32_t at = (before + incl - mine) * (uint32_t)p.heads;
+    if (u0 < u1 && u0 >= at && u0 < at + mine * (uint32_t)p.heads) {
         for (int b = b0; b < b1; ++b) {
-            const int64_t n = (int64_t)per[b] * p.heads;
-            if (u0 < at + n) {
+            const uint32_t k = per[b] * (uint32_t)p.heads;
+            if (u0 < at + k) {
                 st->b = b;
                 st->head = (int)((u0 - at) / per[b]);
                 st->skip = (int)((u0 - at) % per[b]);  // units of this head's tiles before u0
                 break;
             }
-            at += n;
+            at += k;
         }
     }
     __syncthreads();
@@ -226,7 +230,7 @@ struct Item {
     int tokens;         // tokens of the query tile
     bool whole;         // no other CTA has units of this tile
     bool first;         // this CTA has the tile's first unit
-    int64_t tile_unit;  // number of the tile's first unit
+    int tile_unit;  // number of the tile's first unit
     int units;          // the tile's units
 };
 
@@ -242,7 +246,7 @@ __device__ __forceinline__ Item take(const Params& p, Cursor& c) {
     it.s = span(p, c.r, c.tile);
     it.units = max(1, it.s.units);
     it.tile_unit = c.unit - c.skip;
-    const int n = (int)min((int64_t)(it.units - c.skip), c.end - c.unit);
+    const int n = min(it.units - c.skip, c.end - c.unit);
     it.k0 = it.s.k0 + c.skip;
     it.n = it.s.units ? n : 0;
     it.first = c.skip == 0;
@@ -341,10 +345,9 @@ __device__ __forceinline__ RowAt row_at(const Params& p, const Item& it, int r) 
 // part, and, as the tile's last, forms the output rows from all parts.  `sync` is a barrier
 // over those threads, `last` a shared int.
 template <int kD, int kThreads, typename Sync, typename RowMap>
-__device__ void join(const Params& p, const Item& it, int64_t total, int tid, int* last, Sync sync, int rows,
+__device__ void join(const Params& p, const Item& it, const Start& st, int tid, int* last, Sync sync, int rows,
                      RowMap row_map) {
-    const int n = (int)min((int64_t)gridDim.x, total);
-    const int c0 = cta_of(total, n, it.tile_unit), c1 = cta_of(total, n, it.tile_unit + it.units - 1);
+    const int c0 = cta_of(st, it.tile_unit), c1 = cta_of(st, it.tile_unit + it.units - 1);
     __threadfence();
     sync();
     if (tid == 0) {
@@ -397,11 +400,14 @@ cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int rows, int grid_cap
 // attn_tile.cu: query tiles of up to 256 rows on tcgen05
 cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);
 
+inline int64_t most_units(const Params& p) {
+    return ((int64_t)p.T / p.tokens_per_tile + p.B) * p.heads * ((int64_t)p.max_kv / kKeyTile + 2);
+}
 // One CTA per SM, and no more CTAs than there can be units.
 inline int grid_for(const Params& p, int grid_cap) {
     int grid = device_info().num_sms;
     if (grid > grid_cap) grid = grid_cap;
-    const int64_t units = ((int64_t)p.T / p.tokens_per_tile + p.B) * p.heads * (p.max_kv / kKeyTile + 2);
+    const int64_t units = most_units(p);
     return units < grid ? (int)units : grid;
 }
 

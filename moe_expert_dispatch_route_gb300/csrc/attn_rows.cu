@@ -19,13 +19,21 @@
 // range exactly:
 //   q   a row is multiplied by a power of two that brings its largest element into [2^14, 2^15);
 //       an element 2^29 below that becomes subnormal, an absolute error of 2^-40 of the largest
-//   p   2^14 p 2^(s - r), s the value's scale exponent, r the largest s so far: at most 2^14, and
-//       what falls below fp16's range is under 2^-38 of the largest weight a key can have
+//   p   2^7 p 2^(s - r), s the value's scale exponent, r the largest s so far: at most 2^15, and
+//       what falls below fp16's range is under 2^-31 of the largest weight a key can have
+//
+// The running maximum is followed loosely: o and the sum stay relative to an older maximum
+// until a row's new one is 2^8 times as large (in the probabilities, which are then at most
+// 2^8).  The quotient o / sum does not depend on the reference point.  With 16 rows a warp
+// the exact maximum of one of them moved with almost every chunk, and o with it.
 #include "attn.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
+
+constexpr float kLoose = 8.0f;  // log2 of how far the maximum may run ahead
+constexpr int kPBits = 7;       // e4m3: probabilities are multiplied by 2^7
 
 // What the consumers know of a query tile, in shared memory.
 template <int kRows>
@@ -41,9 +49,12 @@ template <int kD, bool kFp8, int kNT, int kRW>
 struct Cfg {
     static constexpr int kElt = kFp8 ? 1 : 2;
     static constexpr int kRows = 8 * kNT * kRW;
-    // 64 rows: o of a key group takes as much shared memory as a key tile, so there are two
-    static constexpr int kTG = kRW == 4 ? 2 : 3;
-    static constexpr int kKW = kRW == 4 ? 1 : 4 / kRW;
+    // Tile groups: with two stages each they overlap each other's waits; a few rows take so
+    // little time that one each will do; many rows of wide bf16 tiles, whose ring holds three
+    // (two for 64 rows, whose o needs the room), stay together on one tile.
+    static constexpr bool kWide = kD * kElt == 256;
+    static constexpr int kTG = kRW == 1 ? 3 : kWide ? 1 : kRW == 2 ? 3 : 2;
+    static constexpr int kKW = kRW == 1 ? 4 : kWide ? 8 / kRW : kRW == 2 ? 2 : 1;
     static constexpr int kMerged = kKW * kTG;  // key groups to be put together
     static constexpr int kWarps = kRW * kMerged;
     static constexpr int kConsumers = 32 * kWarps;
@@ -62,7 +73,7 @@ struct Cfg {
     static constexpr int kQStride = 2 * kD + 16;  // bytes; rows fall into different banks
     static constexpr int kOStride = kD + 4;       // floats; likewise
     static constexpr int kGroupBytes = kRows * kOStride * 4;  // o of one key group
-    static constexpr int kFixed = 1024 + kRing + (kFp8 ? 2 * kStages * kKeyTile : 0) + kMerged * kRows * 8 + kRows * 8 +
+    static constexpr int kFixed = 1024 + kRing + (kFp8 ? 2 * kStages * kKeyTile : 0) + kMerged * kRows * 8 +
                                   (4 * kStages + 8) * 8;
     static constexpr int kInfoBytes = ((int)sizeof(TileInfo<kRows>) + 15) / 16 * 16 + kRows * kQStride;
     static constexpr int kBudget = 232448 - 256;  // less the static shared memory
@@ -131,6 +142,17 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
         return (uint32_t)(half * kKeyTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     }
     return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// 4 bytes global -> shared, or 4 zero bytes; and this thread's arrival on `bar` (one of those
+// it counts) once its copies so far have landed.
+__device__ __forceinline__ void cp_async_4_or_0(void* dst, const void* src, bool copy) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)),
+                 "l"(static_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(copy ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
 // ---------------------------------------------------------------- query rows
@@ -218,8 +240,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
     uint8_t* infos = reinterpret_cast<uint8_t*>(xchg) + C::kSlots * C::kGroupBytes;
     uint8_t* scales = infos + C::kInfos * C::kInfoBytes;
     float2* group_ml = reinterpret_cast<float2*>(scales + (kFp8 ? 2 * C::kStages * kKeyTile : 0));
-    float2* row_ml = group_ml + C::kMerged * C::kRows;
-    uint64_t* full = reinterpret_cast<uint64_t*>(row_ml + C::kRows);  // [stage][K, V]
+    uint64_t* full = reinterpret_cast<uint64_t*>(group_ml + C::kMerged * C::kRows);  // [stage][K, V]
     uint64_t* empty = full + 2 * C::kStages;
     uint64_t* info_full = empty + 2 * C::kStages;
     uint64_t* info_empty = info_full + 2;
@@ -232,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
     if (threadIdx.x == 0) {
         abort_s = 0;
         for (int i = 0; i < 2 * C::kStages; ++i) {
-            tc::mbar_init(&full[i], kFp8 ? 2 : 1);
+            tc::mbar_init(&full[i], kFp8 ? 33 : 1);
             tc::mbar_init(&empty[i], kRW * C::kKW);
         }
         for (int i = 0; i < C::kInfos; ++i) {
@@ -291,7 +312,34 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             }
             return;
         }
-        if (role == 2 && !kFp8) return;
+        if (role == 2) {
+            // scales: four keys of K and of V a lane, each 4-byte copy signalling the stage's barrier
+            // itself (as bulk copies they were 16 bytes each for 16-token pages, as many as of tiles' boxes)
+            if (!kFp8) return;
+            int stage = 0;
+            uint32_t turn = 0;
+            while (more(cur)) {
+                const Item it = take(p, cur);
+                Pages pages = pages_of(p, it);
+                for (int k = 0; k < it.n; ++k) {
+                    const int key0 = (it.k0 + k) * kKeyTile, key = key0 + lane * 4;
+                    const int page = page_of(p, it, pages, key0, (key >> p.page_shift) - (key0 >> p.page_shift));
+                    const bool want = key < it.s.hi && key + 4 > it.s.lo && page >= 0 && page < p.num_pages;
+                    const int64_t at =
+                        want ? ((int64_t)page * p.heads + it.head) * p.page_size + (key & (p.page_size - 1)) : 0;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (turn > 0) wait(&empty[2 * stage + kv], (turn - 1) & 1);
+                        cp_async_4_or_0(scales + (2 * stage + kv) * kKeyTile + lane * 4, (kv ? v_scale : k_scale) + at,
+                                        want);
+                        cp_async_arrive(&full[2 * stage + kv]);
+                    }
+                    if (++stage == C::kStages) stage = 0, ++turn;
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            return;
+        }
         const int box_keys = min(p.page_size, kKeyTile), npg = kKeyTile / box_keys;
         int stage = 0;
         uint32_t turn = 0;
@@ -310,45 +358,25 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             }
             for (int k = 0; k < it.n; ++k) {
                 const int key0 = (it.k0 + k) * kKeyTile;
-                // roles 0 and 1: lane i copies box i of the tile (page i / kHalves of it, column block
-                // i % kHalves); role 2: the scales of page i / 2 of it for K (i even) or V
-                const int per = role == 2 ? 2 : C::kHalves;
-                const int pg = lane / per, part = lane % per;
+                // lane i copies box i of the tile (page i / kHalves of it, column block i % kHalves)
+                const int pg = lane / C::kHalves, part = lane % C::kHalves;
                 const int key = key0 + pg * box_keys, off = key & (p.page_size - 1);
                 const bool want = pg < npg && key < it.s.hi && key + box_keys > it.s.lo;
                 int page = page_of(p, it, pages, key0, pg);
-                const bool bad = page < 0 || page >= p.num_pages;
-                if (want && bad) set_err(p.err, MOE_ERR_BAD_INDEX);
-                if (role < 2) {
-                    if (bad) page = p.num_pages;  // past the pool: the copy fills zeros
-                    uint64_t* bar = &full[2 * stage + role];
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * C::kRowBytes);
-                    if (turn > 0) wait(&empty[2 * stage + role], (turn - 1) & 1);
-                    if (!*abort) {
-                        if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
-                        __syncwarp();
-                        if (want)
-                            tc::tma_load_4d(ring + (2 * stage + role) * C::kTileBytes +
-                                                (part * kKeyTile + pg * box_keys) * C::kRowBytes,
-                                            role ? &vmap : &kmap, bar, part * (C::kRowBytes / C::kElt), off, it.head,
-                                            page);
-                    }
-                } else {
-                    const uint32_t copied = __ballot_sync(0xffffffffu, want && !bad);
-                    if (turn > 0) {
-                        wait(&empty[2 * stage], (turn - 1) & 1);
-                        wait(&empty[2 * stage + 1], (turn - 1) & 1);
-                    }
-                    if (!*abort) {
-                        if (lane < 2)  // as many pages for K as for V
-                            tc::mbar_arrive_expect_tx(&full[2 * stage + lane], __popc(copied) / 2 * box_keys);
-                        __syncwarp();
-                        if (want && !bad)
-                            tc::bulk_load(scales + (2 * stage + part) * kKeyTile + pg * box_keys,
-                                          (part ? v_scale : k_scale) +
-                                              ((int64_t)page * p.heads + it.head) * p.page_size + off,
-                                          box_keys, &full[2 * stage + part]);
-                    }
+                if (want && (page < 0 || page >= p.num_pages)) {
+                    set_err(p.err, MOE_ERR_BAD_INDEX);
+                    page = p.num_pages;  // past the pool: the copy fills zeros
+                }
+                uint64_t* bar = &full[2 * stage + role];
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * C::kRowBytes);
+                if (turn > 0) wait(&empty[2 * stage + role], (turn - 1) & 1);
+                if (!*abort) {
+                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (want)
+                        tc::tma_load_4d(ring + (2 * stage + role) * C::kTileBytes +
+                                            (part * kKeyTile + pg * box_keys) * C::kRowBytes,
+                                        role ? &vmap : &kmap, bar, part * (C::kRowBytes / C::kElt), off, it.head, page);
                 }
                 if (++stage == C::kStages) stage = 0, ++turn;
             }
@@ -356,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
         if (*abort)  // copies still in flight land (or a bounded wait gives up) before the CTA ends
             for (int i = 0; i < 2 * C::kStages; ++i) {
                 const uint32_t issued = turn + (i / 2 < stage ? 1 : 0);
-                if (issued > 0 && (role == 2 || i % 2 == role)) tc::mbar_wait_bounded(&full[i], (issued - 1) & 1);
+                if (issued > 0 && i % 2 == role) tc::mbar_wait_bounded(&full[i], (issued - 1) & 1);
             }
         return;
     }
@@ -474,7 +502,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                 }
                 bool up = false;
 #pragma unroll
-                for (int t = 0; t < kNT; ++t) up |= mx[t][0] > m[t][0] || mx[t][1] > m[t][1];
+                for (int t = 0; t < kNT; ++t)
+                    up |= (mx[t][0] - m[t][0]) * row_scale[t][0] > kLoose ||  // also from -inf
+                          (mx[t][1] - m[t][1]) * row_scale[t][1] > kLoose;
                 if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                     for (int t = 0; t < kNT; ++t)
@@ -515,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) o[j][t][i] *= f;
                     }
-                    const int ex = (int)vb - (int)vref + 14 + 127;
+                    const int ex = (int)vb - (int)vref + kPBits + 127;
                     vscale = vb == 255 ? CUDART_NAN_F : vb == 0 || ex <= 0 ? 0.0f : __int_as_float(ex << 23);
                 }
                 uint32_t pb[C::kStrips][kNT][2];  // (row g, keys 2c, 2c + 1) and 8 keys further
@@ -583,93 +613,97 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[2 * stage + 1]);
         }
-        tiles += count;
 
-        // ---- put the key groups together: all to the rows' common maximum, then sums in a fixed order
+        // ---- put the key groups that had keys together, relative to the rows' common maximum, in a
+        // fixed order.  rank: place of this warp's group among them
+        const int rank = (tg + C::kTG - (int)(tiles % C::kTG)) % C::kTG * C::kKW + kg;
+        const int groups = min(count, C::kTG) * C::kKW;
+        tiles += count;
+        if (rank < groups) {
 #pragma unroll
-        for (int t = 0; t < kNT; ++t)
+            for (int t = 0; t < kNT; ++t)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                m[t][x] *= row_scale[t][x];  // in powers of two
+                for (int x = 0; x < 2; ++x) {
+                    m[t][x] *= row_scale[t][x];  // in powers of two
 #pragma unroll
-                for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
-                if (g == 0)
-                    group_ml[mg * C::kRows + rg * 8 * kNT + t * 8 + c * 2 + x] = make_float2(m[t][x], l[t][x]);
-            }
-        sync();
-        if (threadIdx.x < C::kRows) {
-            float rm = -CUDART_INF_F, rl = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C::kMerged; ++i) rm = fmaxf(rm, group_ml[i * C::kRows + threadIdx.x].x);
-#pragma unroll
-            for (int i = 0; i < C::kMerged; ++i) {
-                const float2 v = group_ml[i * C::kRows + threadIdx.x];
-                rl += v.y * exp2_fast(v.x - (rm == -CUDART_INF_F ? 0.0f : rm));
-            }
-            row_ml[threadIdx.x] = make_float2(rm, rl);
-        }
-#pragma unroll
-        for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = rg * 8 * kNT + t * 8 + c * 2 + x;
-                float rm = -CUDART_INF_F;
-#pragma unroll
-                for (int i = 0; i < C::kMerged; ++i) rm = fmaxf(rm, group_ml[i * C::kRows + r].x);
-                float f = exp2_fast(m[t][x] - (rm == -CUDART_INF_F ? 0.0f : rm)), f2 = 1.0f;
-                if (kFp8) {  // and back from 2^14 2^-r; 0 where this warp had no keys
-                    const int e2 = (int)vref - 127 - 14;
-                    f *= pow2(e2 / 2);
-                    f2 = pow2(e2 - e2 / 2);
+                    for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
                 }
-#pragma unroll
-                for (int j = 0; j < kSteps; ++j) {
-                    o[j][t][x] = o[j][t][x] * f * f2;
-                    o[j][t][2 + x] = o[j][t][2 + x] * f * f2;
-                }
-            }
-        // where an element stands: column 16 j + g (+ 8), or 16 j + 2 g (+ 1) from e4m3 pairs
-        constexpr int kColG = kFp8 ? 2 : 1, kColHi = kFp8 ? 1 : 8;
-        float* mine = xchg + (mg % C::kSlots) * (C::kRows * C::kOStride) + (rg * 8 * kNT + c * 2) * C::kOStride + g * kColG;
-        auto put = [&] {
-#pragma unroll
-            for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-                for (int t = 0; t < kNT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mine[(t * 8 + (i & 1)) * C::kOStride + j * 16 + (i >> 1) * kColHi] = o[j][t][i];
-        };
-        // kSlots groups at a time hand their o to the first kSlots
-        constexpr int kFirst = (C::kMerged - 1) / C::kSlots * C::kSlots;
-#pragma unroll
-        for (int b = kFirst; b > 0; b -= C::kSlots) {
-            if (mg >= b && mg < b + C::kSlots) put();
-            sync();
-            if (mg < C::kSlots && mg + b < C::kMerged) {
+            if (kFp8) {  // back from 2^7 2^-r
+                const int e2 = (int)vref - 127 - kPBits;
+                const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j)
 #pragma unroll
                     for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[j][t][i] += mine[(t * 8 + (i & 1)) * C::kOStride + j * 16 + (i >> 1) * kColHi];
+                        for (int i = 0; i < 4; ++i) o[j][t][i] = o[j][t][i] * f1 * f2;
+            }
+        }
+        // where an element stands: column 16 j + g (+ 8), or 16 j + 2 g (+ 1) from e4m3 pairs
+        constexpr int kColG = kFp8 ? 2 : 1, kColHi = kFp8 ? 1 : 8;
+        float* mine =
+            xchg + (rank % C::kSlots) * (C::kRows * C::kOStride) + (rg * 8 * kNT + c * 2) * C::kOStride + g * kColG;
+        float2* mine_ml = group_ml + (rank % C::kSlots) * C::kRows + rg * 8 * kNT + c * 2;
+        auto put = [&] {
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mine[(t * 8 + (i & 1)) * C::kOStride + j * 16 + (i >> 1) * kColHi] = o[j][t][i];
+                if (g == 0) {
+                    mine_ml[t * 8] = make_float2(m[t][0], l[t][0]);
+                    mine_ml[t * 8 + 1] = make_float2(m[t][1], l[t][1]);
+                }
+            }
+        };
+        // kSlots groups at a time hand their state to the first kSlots
+        for (int b = (groups - 1) / C::kSlots * C::kSlots; b > 0; b -= C::kSlots) {
+            if (rank >= b && rank < b + C::kSlots && rank < groups) put();
+            sync();
+            if (rank < C::kSlots && rank + b < groups) {
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float2 ml = mine_ml[t * 8 + x];
+                        const float mn = fmaxf(m[t][x], ml.x), to = mn == -CUDART_INF_F ? 0.0f : mn;
+                        const float fa = exp2_fast(m[t][x] - to), fb = exp2_fast(ml.x - to);
+                        m[t][x] = mn;
+                        l[t][x] = l[t][x] * fa + ml.y * fb;
+#pragma unroll
+                        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                            for (int i = x; i < 4; i += 2)
+                                o[j][t][i] = o[j][t][i] * fa +
+                                             mine[(t * 8 + x) * C::kOStride + j * 16 + (i >> 1) * kColHi] * fb;
+                    }
             }
             sync();
         }
-        if (mg < C::kSlots) put();
+        const int left = min(groups, C::kSlots);
+        if (rank < left) put();
         sync();
         const Item& it = info->it;
         const int rows = it.tokens * p.group;
         for (int i = threadIdx.x; i < rows * (kD / 4); i += C::kConsumers) {
             const int r = i / (kD / 4), d = (i % (kD / 4)) * 4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            float2 ml = make_float2(-CUDART_INF_F, 0.0f);
 #pragma unroll
-            for (int k = 0; k < C::kSlots; ++k) {
-                const float4 v = *reinterpret_cast<const float4*>(xchg + (k * C::kRows + r) * C::kOStride + d);
-                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-            }
-            const float2 ml = row_ml[r];
+            for (int k = 0; k < C::kSlots; ++k)
+                if (k < left) ml.x = fmaxf(ml.x, group_ml[k * C::kRows + r].x);
+            const float to = ml.x == -CUDART_INF_F ? 0.0f : ml.x;
+#pragma unroll
+            for (int k = 0; k < C::kSlots; ++k)
+                if (k < left) {
+                    const float2 other = group_ml[k * C::kRows + r];
+                    const float f = exp2_fast(other.x - to);
+                    const float4 v = *reinterpret_cast<const float4*>(xchg + (k * C::kRows + r) * C::kOStride + d);
+                    ml.y += other.y * f;
+                    a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+                }
             if (it.whole) {
                 const RowAt at = row_at(p, it, r);
                 const float inv = ml.y > 0.0f ? 1.0f / ml.y : (ml.y == 0.0f ? 0.0f : ml.y);
@@ -685,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             }
         }
         if (!it.whole)
-            join<kD, C::kConsumers>(p, it, start.total, threadIdx.x, &last_s, sync, rows, [](int r) { return r; });
+            join<kD, C::kConsumers>(p, it, start, threadIdx.x, &last_s, sync, rows, [](int r) { return r; });
         else
             sync();
         if (threadIdx.x == 0) tc::mbar_arrive(&info_empty[buf]);

@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 }
                 if (valid) part_ml(p, blockIdx.x, slot)[h * kHalfRows + row] = make_float2(m2, l);
                 const int all = it.tokens * p.group, half_rows = v.rows;
-                join<kD, 256>(p, it, start.total, threadIdx.x, &last_s, sync, v.count * kHalfRows, [=](int r) {
+                join<kD, 256>(p, it, start, threadIdx.x, &last_s, sync, v.count * kHalfRows, [=](int r) {
                     const int in_half = r & (kHalfRows - 1), t = (r / kHalfRows) * half_rows + in_half;
                     return in_half < half_rows && t < all ? t : -1;
                 });
