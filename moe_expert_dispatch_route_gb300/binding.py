@@ -156,8 +156,8 @@ def _ptr(t):
 
 
 def _stream(s):
-    if s is None:
-        return torch.cuda.current_stream().cuda_stream
+    if s is None:  # torch.cuda.current_stream().cuda_stream, without the Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -344,7 +344,7 @@ def _same(what, *pairs):
 
 
 def _vector(what, t, dtype, n):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: a packed {dtype} vector of {n} is expected, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -370,16 +370,18 @@ def kv_cache(k, v, k_scale=None, v_scale=None) -> MoeKvCache:
 
 def moe_kv_write(cache: MoeKvCache, k, v, slots, err_flag=None, max_ctas=0, stream=None):
     """Stores k, v [T][heads][head_dim] (bf16, any token and head strides) at slots int64 [T]."""
-    T = k.shape[0]
-    rows = (T, cache.num_heads, cache.head_dim)
-    if k.shape != rows or v.shape != rows or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
-        raise ValueError(f"moe_kv_write: k and v are bf16 {rows}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    ks, vs = k.stride(), v.stride()
-    if ks[2] != 1 or vs[2] != 1 or ks[1] != vs[1]:
+    shape = k.shape
+    T = shape[0]
+    if shape != (T, cache.num_heads, cache.head_dim) or v.shape != shape or not (k.dtype is v.dtype is torch.bfloat16):
+        raise ValueError(f"moe_kv_write: k and v are bf16 {(T, cache.num_heads, cache.head_dim)}, got {k.dtype} "
+                         f"{tuple(shape)} and {v.dtype} {tuple(v.shape)}")
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if k2 != 1 or v2 != 1 or k1 != v1:
         raise ValueError("moe_kv_write: head_dim is contiguous and the head stride the same for k and v")
     _vector("moe_kv_write: slots", slots, torch.int64, T)
-    _check(lib().moe_kv_write(ctypes.byref(cache), T, k.data_ptr(), v.data_ptr(), ks[0], vs[0], ks[1],
-                              slots.data_ptr(), _ptr(err_flag), max_ctas, _stream(stream)), "moe_kv_write")
+    _check(lib().moe_kv_write(ctypes.byref(cache), T, k.data_ptr(), v.data_ptr(), k0, v0, k1, slots.data_ptr(),
+                              _ptr(err_flag), max_ctas, _stream(stream)), "moe_kv_write")
 
 
 def moe_kv_read(cache: MoeKvCache, block_table, start, cu_len, k_out, v_out, err_flag=None, max_ctas=0, stream=None):

@@ -98,6 +98,7 @@ struct Cursor {
     int unit;           // number of the tile's unit that comes first in this CTA's range
     int end;            // of the CTA's range
     int skip;           // units of the tile before `unit`
+    bool done;          // the tile has been taken: take() moves on first
     Request r;
 };
 
@@ -105,6 +106,7 @@ struct Start {  // in shared memory, filled by locate()
     int b, head, tile, skip;
     int unit, end;
     int each, more;  // units of a CTA; the first `more` CTAs have one more
+    Request r;
 };
 
 // The CTA that has unit u.
@@ -129,29 +131,32 @@ template <int kThreads>
 __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint32_t* per = scratch + 32;  // units of one head of request b
-    if (p.max_q <= p.tokens_per_tile) {
-        for (int b = tid; b < p.B; b += kThreads) {
-            const Request r = request(p, b, blockIdx.x == 0);
-            per[b] = r.n > 0 ? (uint32_t)max(1, span(p, r, 0).units) : 0u;
+    const bool single = p.max_q <= p.tokens_per_tile;  // one query tile a request
+    uint32_t* per = scratch + 32;  // units of one head of request b, unless a thread has one request
+    const int run = (p.B + kThreads - 1) / kThreads;  // requests per thread, consecutive
+    const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
+    uint32_t mine = 0;
+    Request r = {0, 0, 0};
+    if (single) {
+        for (int b = b0; b < b1; ++b) {
+            r = request(p, b, blockIdx.x == 0);
+            const uint32_t u = r.n > 0 ? (uint32_t)max(1, span(p, r, 0).units) : 0u;
+            if (run > 1) per[b] = u;
+            mine += u;
         }
     } else {
         for (int b = warp; b < p.B; b += kWarps) {
-            const Request r = request(p, b, blockIdx.x == 0 && lane == 0);
-            const int n = tiles_of(p, r);
+            const Request q = request(p, b, blockIdx.x == 0 && lane == 0);
+            const int n = tiles_of(p, q);
             uint32_t s = 0;
-            for (int i = lane; i < n; i += 32) s += (uint32_t)max(1, span(p, r, i).units);
+            for (int i = lane; i < n; i += 32) s += (uint32_t)max(1, span(p, q, i).units);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (lane == 0) per[b] = s;
         }
+        __syncthreads();
+        for (int b = b0; b < b1; ++b) mine += per[b];
     }
-    __syncthreads();
-    // sums over a run of requests per thread, then over warps
-    const int run = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
-    uint32_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += per[b];
     const uint32_t incl = warp_incl(mine);
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
@@ -175,23 +180,26 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     uint32_t at = (before + incl - mine) * (uint32_t)p.heads;
     if (u0 < u1 && u0 >= at && u0 < at + mine * (uint32_t)p.heads) {
         for (int b = b0; b < b1; ++b) {
-            const uint32_t k = per[b] * (uint32_t)p.heads;
+            const uint32_t one = single && run == 1 ? mine : per[b], k = one * (uint32_t)p.heads;
             if (u0 < at + k) {
                 st->b = b;
-                st->head = (int)((u0 - at) / per[b]);
-                st->skip = (int)((u0 - at) % per[b]);  // units of this head's tiles before u0
+                st->head = (int)((u0 - at) / one);
+                st->skip = (int)((u0 - at) % one);  // units of this head's tiles before u0
+                st->tile = 0;
+                st->r = single && run == 1 ? r : request(p, b, false);
                 break;
             }
             at += k;
         }
     }
     __syncthreads();
-    if (u0 < u1 && warp == 0) {
-        const Request r = request(p, st->b, false);
-        const int n = tiles_of(p, r);
+    if (single || u0 >= u1) return;
+    if (warp == 0) {
+        const Request q = st->r;
+        const int tiles = tiles_of(p, q);
         uint32_t left = (uint32_t)st->skip;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const uint32_t u = i0 + lane < n ? (uint32_t)max(1, span(p, r, i0 + lane).units) : 0u;
+        for (int i0 = 0; i0 < tiles; i0 += 32) {
+            const uint32_t u = i0 + lane < tiles ? (uint32_t)max(1, span(p, q, i0 + lane).units) : 0u;
             const uint32_t in = warp_incl(u);
             const uint32_t over = __ballot_sync(0xffffffffu, in > left);
             if (over) {
@@ -209,7 +217,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     __syncthreads();
 }
 
-__device__ __forceinline__ Cursor cursor(const Params& p, const Start& st) {
+__device__ __forceinline__ Cursor cursor(const Start& st) {
     Cursor c;
     c.b = st.b;
     c.head = st.head;
@@ -217,7 +225,8 @@ __device__ __forceinline__ Cursor cursor(const Params& p, const Start& st) {
     c.unit = st.unit;
     c.end = st.end;
     c.skip = st.skip;
-    if (c.unit < c.end) c.r = request(p, c.b, false);
+    c.done = false;
+    c.r = st.r;
     return c;
 }
 
@@ -236,8 +245,21 @@ struct Item {
 
 __device__ __forceinline__ bool more(const Cursor& c) { return c.unit < c.end; }
 
-// The item at the cursor; the cursor moves behind it.
+// The next item.  The cursor moves to it only now: the lengths of a request are not waited
+// for before its turn.
 __device__ __forceinline__ Item take(const Params& p, Cursor& c) {
+    if (c.done) {
+        c.skip = 0;
+        if (++c.tile >= tiles_of(p, c.r)) {
+            c.tile = 0;
+            if (++c.head >= p.heads) {
+                c.head = 0;
+                do {  // the range ends before the requests do
+                    c.r = request(p, ++c.b, false);
+                } while (c.r.n == 0);
+            }
+        }
+    }
     Item it;
     it.b = c.b;
     it.head = c.head;
@@ -253,18 +275,7 @@ __device__ __forceinline__ Item take(const Params& p, Cursor& c) {
     it.whole = n == it.units;
     it.tokens = min(p.tokens_per_tile, c.r.n - c.tile * p.tokens_per_tile);
     c.unit += n;
-    c.skip = 0;
-    if (more(c)) {
-        if (++c.tile >= tiles_of(p, c.r)) {
-            c.tile = 0;
-            if (++c.head >= p.heads) {
-                c.head = 0;
-                do {  // the range ends before the requests do
-                    c.r = request(p, ++c.b, false);
-                } while (c.r.n == 0);
-            }
-        }
-    }
+    c.done = true;
     return it;
 }
 
@@ -348,35 +359,47 @@ template <int kD, int kThreads, typename Sync, typename RowMap>
 __device__ void join(const Params& p, const Item& it, const Start& st, int tid, int* last, Sync sync, int rows,
                      RowMap row_map) {
     const int c0 = cta_of(st, it.tile_unit), c1 = cta_of(st, it.tile_unit + it.units - 1);
-    __threadfence();
-    sync();
+    sync();  // the CTA's stores come before thread 0's fence and count
     if (tid == 0) {
+        __threadfence();
         const uint32_t seen = atomicAdd(&p.counters[c0], 1u);
         *last = seen == (uint32_t)(c1 - c0);
         if (*last) p.counters[c0] = 0;
+        __threadfence();
     }
     sync();
-    const bool mine = *last;
-    if (mine) {
-        __threadfence();
+    if (*last) {
         constexpr int kPer = kD / 4;  // threads a row: four columns each
+        constexpr int kBatch = 8;     // parts whose loads are under way together
         for (int r = tid / kPer; r < rows; r += kThreads / kPer) {
             const int d = (tid % kPer) * 4;
             float m = -CUDART_INF_F, l = 0.0f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = c0; c <= c1; ++c) {
-                const int slot = c == c0 ? 0 : 1;
-                const float2 ml = __ldcg(part_ml(p, c, slot) + r);
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o(p, c, slot) + (size_t)r * kD + d));
-                const float mn = fmaxf(m, ml.x);
-                const float base = mn == -CUDART_INF_F ? 0.0f : mn;
-                const float fa = exp2_fast(m - base), fb = exp2_fast(ml.x - base);
-                l = l * fa + ml.y * fb;
-                o.x = o.x * fa + x.x * fb;
-                o.y = o.y * fa + x.y * fb;
-                o.z = o.z * fa + x.z * fb;
-                o.w = o.w * fa + x.w * fb;
-                m = mn;
+            for (int b0 = c0; b0 <= c1; b0 += kBatch) {
+                float2 ml[kBatch];
+                float4 x[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int c = b0 + i, slot = c == c0 ? 0 : 1;
+                    ml[i] = make_float2(-CUDART_INF_F, 0.0f);
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c <= c1) {
+                        ml[i] = __ldcg(part_ml(p, c, slot) + r);
+                        x[i] = __ldcg(reinterpret_cast<const float4*>(part_o(p, c, slot) + (size_t)r * kD + d));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float mn = fmaxf(m, ml[i].x);
+                    const float base = mn == -CUDART_INF_F ? 0.0f : mn;
+                    const float fa = exp2_fast(m - base), fb = exp2_fast(ml[i].x - base);
+                    l = l * fa + ml[i].y * fb;
+                    o.x = o.x * fa + x[i].x * fb;
+                    o.y = o.y * fa + x[i].y * fb;
+                    o.z = o.z * fa + x[i].z * fb;
+                    o.w = o.w * fa + x[i].w * fb;
+                    m = mn;
+                }
             }
             const int q = row_map(r);
             if (q < 0) continue;

@@ -156,14 +156,36 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 
 // ---------------------------------------------------------------- query rows
-// One warp: the rows of item `it` into `qs` (bf16 as they are; for an e4m3 cache fp16, scaled,
-// and in the order in which the keys' fragments hold their columns), and the rows' ranges.
+// One warp: loads of the first pieces of the item's rows, 16 bytes each, all under way at once.
+template <int kD, int kRows>
+struct RowLoads {
+    static constexpr int kPieces = kD / 8;                  // of a row
+    static constexpr int kAll = kRows * kPieces / 32;       // per lane
+    static constexpr int kBatch = kAll < 16 ? kAll : 16;
+    uint4 x[kBatch];
+
+    __device__ __forceinline__ void load(const Params& p, const Item& it, int i0) {
+        const int rows = it.tokens * p.group;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = (i0 + b) * 32 + (threadIdx.x & 31), r = i / kPieces;
+            x[b] = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const RowAt at = row_at(p, it, r);
+                x[b] = __ldg(reinterpret_cast<const uint4*>(p.q + at.token * p.q_ld + at.head * p.q_head) + i % kPieces);
+            }
+        }
+    }
+};
+// The same warp: the rows into `qs` (bf16 as they are; for an e4m3 cache fp16, scaled, and in the
+// order in which the keys' fragments hold their columns), and what else the consumers need.
 template <int kD, bool kFp8, int kRows>
-__device__ void stage_rows(const Params& p, const Item& it, TileInfo<kRows>* info, uint8_t* qs, int stride) {
+__device__ void stage_rows(const Params& p, const Item& it, RowLoads<kD, kRows>& loads, TileInfo<kRows>* info,
+                           uint8_t* qs, int stride) {
+    using Loads = RowLoads<kD, kRows>;
+    static_assert(kRows * Loads::kPieces % 32 == 0 && Loads::kAll % Loads::kBatch == 0, "");
     const int lane = threadIdx.x & 31;
     const int rows = it.tokens * p.group;
-    constexpr int kPieces = kD / 8;  // 16-byte pieces of a row
-    constexpr int kBatch = 4;
     if (lane == 0) {
         info->it = it;
         info->stop = 0;
@@ -181,34 +203,24 @@ __device__ void stage_rows(const Params& p, const Item& it, TileInfo<kRows>* inf
         info->range[r] = v;
         if (!kFp8) info->row_scale[r] = p.scale_log2;
     }
-    static_assert(kRows * kPieces % 32 == 0, "");
-    for (int i0 = 0; i0 < kRows * kPieces / 32; i0 += kBatch) {
-        uint4 x[kBatch];
+    for (int i0 = 0; i0 < Loads::kAll; i0 += Loads::kBatch) {
+        if (i0 > 0) loads.load(p, it, i0);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = (i0 + b) * 32 + lane, r = i / kPieces;
-            x[b] = make_uint4(0, 0, 0, 0);
-            if (i0 + b < kRows * kPieces / 32 && r < rows) {
-                const RowAt at = row_at(p, it, r);
-                x[b] = __ldg(reinterpret_cast<const uint4*>(p.q + at.token * p.q_ld + at.head * p.q_head) + i % kPieces);
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (i0 + b >= kRows * kPieces / 32) break;
-            const int i = (i0 + b) * 32 + lane, r = i / kPieces, piece = i % kPieces;
+        for (int b = 0; b < Loads::kBatch; ++b) {
+            const int i = (i0 + b) * 32 + lane, r = i / Loads::kPieces, piece = i % Loads::kPieces;
             uint8_t* row = qs + r * stride;
+            const uint4 x = loads.x[b];
             if (!kFp8) {
-                *reinterpret_cast<uint4*>(row + piece * 16) = x[b];
+                *reinterpret_cast<uint4*>(row + piece * 16) = x;
                 continue;
             }
-            const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t mx = 0;  // largest magnitude as bf16 bits
 #pragma unroll
             for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7fff7fffu);
             mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
-            for (int o = kPieces / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int o = Loads::kPieces / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             // largest element's exponent -> 14, by at most 2^100 (a row of zeros, or of numbers so small
             // that its scores are 0); in two factors, each a float
             const int up = min(14 - ((int)(mx >> 7) - 127), 100), u1 = up / 2, u2 = up - u1;
@@ -288,7 +300,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
     };
 
     if (warp >= C::kWarps) {
-        Cursor cur = cursor(p, start);
+        Cursor cur = cursor(start);
         const int role = warp - C::kWarps;  // 0: K, 1: V, 2: scales, 3: query rows
         if (role == 3) {
             uint32_t n = 0;
@@ -298,14 +310,18 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                 Info* info = reinterpret_cast<Info*>(at);
                 stop = !more(cur);
                 Item it;
-                if (!stop) it = take(p, cur);
+                RowLoads<kD, C::kRows> loads;
+                if (!stop) {
+                    it = take(p, cur);
+                    loads.load(p, it, 0);
+                }
                 // not cut short by an abort: the consumers meet for every query tile
                 if (n >= C::kInfos && !tc::mbar_wait_bounded(&info_empty[buf], (n / C::kInfos - 1) & 1)) break;
                 __syncwarp();
                 if (stop) {
                     if (lane == 0) info->stop = 1;
                 } else {
-                    stage_rows<kD, kFp8, C::kRows>(p, it, info, at + C::kInfoBytes - C::kRows * C::kQStride,
+                    stage_rows<kD, kFp8, C::kRows>(p, it, loads, info, at + C::kInfoBytes - C::kRows * C::kQStride,
                                                    C::kQStride);
                 }
                 tc::mbar_arrive(&info_full[buf]);
@@ -351,11 +367,14 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             pages = pages_of(p, it);
         }
         for (; more_now; it = after, pages = pages_after) {
-            more_now = more(cur);
-            if (more_now) {
-                after = take(p, cur);
-                pages_after = pages_of(p, after);
-            }
+            auto ahead = [&] {  // the next query tile's lengths and first table entries
+                more_now = more(cur);
+                if (more_now) {
+                    after = take(p, cur);
+                    pages_after = pages_of(p, after);
+                }
+            };
+            if (it.n == 0) ahead();
             for (int k = 0; k < it.n; ++k) {
                 const int key0 = (it.k0 + k) * kKeyTile;
                 // lane i copies box i of the tile (page i / kHalves of it, column block i % kHalves)
@@ -379,6 +398,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                                         role ? &vmap : &kmap, bar, part * (C::kRowBytes / C::kElt), off, it.head, page);
                 }
                 if (++stage == C::kStages) stage = 0, ++turn;
+                if (k == 0) ahead();
             }
         }
         if (*abort)  // copies still in flight land (or a bounded wait gives up) before the CTA ends

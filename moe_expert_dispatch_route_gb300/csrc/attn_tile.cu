@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_s;
-    Cursor cur = cursor(p, start);
+    Cursor cur = cursor(start);
     if (threadIdx.x == 0 || threadIdx.x == 128) cursors[threadIdx.x >> 7] = cur;
     __syncthreads();
     // a wait that runs out is reported and then passed, here and in every later wait, so that
@@ -266,12 +266,17 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 pages = pages_of(p, it);
             }
             for (; more_now; it = after, pages = pages_after) {
-                more_now = more(cur);
-                if (more_now) {
-                    after = take(p, cur);
-                    pages_after = pages_of(p, after);
+                auto ahead = [&] {  // the next query tile's lengths and first table entries
+                    more_now = more(cur);
+                    if (more_now) {
+                        after = take(p, cur);
+                        pages_after = pages_of(p, after);
+                    }
+                };
+                if (it.n == 0) {
+                    ahead();
+                    continue;
                 }
-                if (it.n == 0) continue;
                 if (items > 0) wait(q_empty, (items - 1) & 1);
                 if (!*abort && lane == 0) {
                     const int count = it.tokens > half_tokens ? 2 : 1;
@@ -316,6 +321,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                         }
                         if (++e == kRing) e = 0, ++turn;
                     }
+                    if (k == 0) ahead();
                 }
             }
             if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
