@@ -160,6 +160,19 @@ __device__ __forceinline__ Halves halves(const Params& p, const Item& it) {
 }
 __device__ __forceinline__ bool active(const Halves& v, int h, int kt) { return kt >= v.k0[h] && kt < v.k1[h]; }
 
+// What the MMA warp has to know of a K or V tile, put beside it by the copying warp: so it keeps
+// no account of query tiles itself, and its registers go to descriptors.  (With the account in
+// it, the spilled descriptors cost more than the MMAs: 110 cycles an instruction instead of 65.)
+enum : uint32_t {
+    kAct0 = 1u,       // half 0 (1: half 1) uses this tile; for V,
+    kFirst0 = 4u,     // it is the first one of half 0 (1)
+    kNewQ = 16u,      // K: the first tile of a query tile
+    kLastK = 32u,     // K: the last one
+    kStop = 64u,      // no more tiles
+    kSeenLo = 8,      // bits 8-15: first key of the tile that any row sees, 16-23: one past the last
+    kSeenHi = 16
+};
+
 template <int kD, bool kFp8>
 __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
@@ -182,6 +195,8 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     uint64_t* pv_done = p_full + 2;   // [2] they have been multiplied into o
     uint64_t* done = pv_done + 2;
     uint64_t* never = done + 1;
+    uint32_t* cmds = reinterpret_cast<uint32_t*>(never + 1);  // of the ring's tiles, then of the raw ones
+    uint32_t* raw_cmds = cmds + C::kEntries;
     __shared__ Start start;
     __shared__ Cursor cursors[2];  // where the two softmax groups stand: not held in registers
     __shared__ int abort_s, last_s;
@@ -277,6 +292,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     ahead();
                     continue;
                 }
+                const Halves v = halves(p, it);
                 if (items > 0) wait(q_empty, (items - 1) & 1);
                 if (!*abort && lane == 0) {
                     const int count = it.tokens > half_tokens ? 2 : 1;
@@ -302,10 +318,18 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     const bool scaled = kFp8 && want && page < p.num_pages;
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * kRowBytes) +
                                            __popc(__ballot_sync(0xffffffffu, scaled)) * box_keys;
-                    const int off = key & (p.page_size - 1);
+                    const int off = key & (p.page_size - 1), kt = it.k0 + k;
+                    uint32_t cmd = (uint32_t)min(max(it.s.lo - key0, 0), kKeyTile) << kSeenLo |
+                                   (uint32_t)min(it.s.hi - key0, kKeyTile) << kSeenHi;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (active(v, h, kt)) cmd |= kAct0 << h | (kt == v.k0[h] ? kFirst0 << h : 0);
+                    if (k == 0) cmd |= kNewQ;
+                    if (k == it.n - 1) cmd |= kLastK;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         if (turn > 0) wait(&to_empty[e], (turn - 1) & 1);
+                        if (lane == 0) (kFp8 ? raw_cmds : cmds)[e] = cmd;
                         if (!*abort) {
                             if (lane == 0) tc::mbar_arrive_expect_tx(&to_full[e], bytes);
                             __syncwarp();
@@ -324,6 +348,11 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     if (k == 0) ahead();
                 }
             }
+            if (turn > 0) wait(&to_empty[e], (turn - 1) & 1);
+            if (lane == 0) {
+                (kFp8 ? raw_cmds : cmds)[e] = kStop;
+                tc::mbar_arrive(&to_full[e]);
+            }
             if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
                 for (int i = 0; i < kRing; ++i) {
                     const uint32_t issued = turn + (i < e ? 1 : 0);
@@ -336,16 +365,19 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, kKeyTile);
             constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, kD) | kIdescBMn;
             int e = 0;
-            uint32_t turn = 0, items = 0;
-            uint32_t np[2] = {0, 0};  // probabilities of half h taken so far
+            uint32_t turn = 0, queries = 0;
+            uint32_t np0 = 0, np1 = 0;  // probabilities of a half taken so far
+            const uint64_t q_desc = tc::desc_sw128_kmajor(tc::smem_u32(qs));
+            const uint64_t k_desc = tc::desc_sw128_kmajor(tc::smem_u32(ring));
+            const uint64_t v_desc = desc_sw128_mnmajor(tc::smem_u32(ring), C::kBlockBytes);
             auto next = [&] {
                 if (++e == C::kEntries) e = 0, ++turn;
             };
-            auto scores = [&](int h) {  // S_h = Q_h K^T from the ring entry at e
-                if (lane == 0) {
+            auto scores = [&](int h, int at) {  // S_h = Q_h K^T from ring entry `at`
+                if (tc::elect_one()) {
                     // a step along K moves a descriptor's start address, its low bits (in 16 bytes)
-                    const uint64_t a = tc::desc_sw128_kmajor(tc::smem_u32(qs + h * C::kCols * kHalfRows * 128));
-                    const uint64_t b = tc::desc_sw128_kmajor(tc::smem_u32(ring + e * C::kEntryBytes));
+                    const uint64_t a = q_desc + (uint32_t)(h * (C::kCols * kHalfRows * 128 >> 4));
+                    const uint64_t b = k_desc + (uint32_t)(at * (C::kEntryBytes >> 4));
 #pragma unroll
                     for (int s = 0; s < kD / 16; ++s) {
                         const uint32_t off = ((s / 4) * C::kBlockBytes + (s % 4) * 32) >> 4;
@@ -355,73 +387,84 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 }
                 __syncwarp();
             };
-            while (more(cur)) {
-                const Item it = take(p, cur);
-                if (it.n == 0) continue;
-                const Halves v = halves(p, it);
-                wait(q_full, items & 1);
-                ++items;
-                wait(&full[e], turn & 1);
-                tc::tc_fence_after();
-                for (int h = 0; h < 2; ++h)
-                    if (active(v, h, it.k0)) scores(h);
-                if (lane == 0) tc::mma_commit(&empty[e]);
-                next();
-                for (int k = 0; k < it.n; ++k) {
-                    const int kt = it.k0 + k;
-                    const int ve = e;
-                    wait(&full[ve], turn & 1);
-                    const int key0 = kt * kKeyTile;
-                    if (!kFp8 && (key0 < it.s.lo || key0 + kKeyTile > it.s.hi)) {
-                        // keys that no row sees hold anything, NaN among it: 0 * NaN would reach o
-                        const int z0 = min(max(it.s.lo - key0, 0), kKeyTile);  // zero [0, z0) and [z1, end)
-                        const int z1 = min(it.s.hi - key0, kKeyTile);
-                        uint4* row = reinterpret_cast<uint4*>(ring + ve * C::kEntryBytes);
-                        for (int i = lane; i < kKeyTile * 8; i += 32)
-                            if (i / 8 < z0 || i / 8 >= z1)
+            auto values = [&](int h, int at, uint32_t accumulate) {  // O_h (+)= P_h V
+                if (tc::elect_one()) {
+                    const uint64_t b = v_desc + (uint32_t)(at * (C::kEntryBytes >> 4));
 #pragma unroll
-                                for (int b = 0; b < C::kCols; ++b)
-                                    row[b * (C::kBlockBytes / 16) + i] = make_uint4(0, 0, 0, 0);
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    next();
-                    const bool ahead = k + 1 < it.n;
-                    bool waited = false;
-                    for (int h = 0; h < 2; ++h) {
-                        if (active(v, h, kt)) {
-                            wait(&p_full[h], np[h]++ & 1);
-                            tc::tc_fence_after();
-                            if (lane == 0) {
-                                const uint64_t b = desc_sw128_mnmajor(tc::smem_u32(ring + ve * C::kEntryBytes),
-                                                                      C::kBlockBytes);
-#pragma unroll
-                                for (int s = 0; s < kKeyTile / 16; ++s)
-                                    mma_bf16_ta(tmem + 256 + h * 128, tmem + h * 128 + s * 8, b + s * (2048 >> 4),
-                                                kIdescO, s > 0 || kt > v.k0[h]);
-                                tc::mma_commit(&pv_done[h]);
-                            }
-                            __syncwarp();
-                        }
-                        if (ahead && active(v, h, kt + 1)) {
-                            if (!waited) {
-                                wait(&full[e], turn & 1);
-                                tc::tc_fence_after();
-                                waited = true;
-                            }
-                            scores(h);
-                        }
-                    }
-                    if (lane == 0) tc::mma_commit(&empty[ve]);
-                    if (ahead) {
-                        if (lane == 0) tc::mma_commit(&empty[e]);
-                        next();
-                    }
+                    for (int s = 0; s < kKeyTile / 16; ++s)
+                        mma_bf16_ta(tmem + 256 + h * 128, tmem + h * 128 + s * 8, b + s * (2048 >> 4), kIdescO,
+                                    s > 0 ? 1u : accumulate);
+                    tc::mma_commit(&pv_done[h]);
                 }
-                if (lane == 0) tc::mma_commit(q_empty);
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (tc::elect_one()) tc::mma_commit(bar);
+                __syncwarp();
+            };
+            // K tile at e is there: its command, with Q there too
+            auto keys = [&]() -> uint32_t {
+                wait(&full[e], turn & 1);
+                const uint32_t cmd = cmds[e];
+                if (cmd & kNewQ) wait(q_full, queries++ & 1);
+                tc::tc_fence_after();
+                return cmd;
+            };
+            auto keys_done = [&](uint32_t cmd) {
+                commit(&empty[e]);
+                if (cmd & kLastK) commit(q_empty);
+                next();
+            };
+            uint32_t cmd = keys();
+            if (!(cmd & kStop)) {
+                if (cmd & kAct0) scores(0, e);
+                if (cmd & (kAct0 << 1)) scores(1, e);
+                keys_done(cmd);
             }
-            if (lane == 0) tc::mma_commit(done);
-            __syncwarp();
+            while (!(cmd & kStop)) {
+                const int ve = e;
+                wait(&full[ve], turn & 1);
+                const int z0 = cmd >> kSeenLo & 255, z1 = cmd >> kSeenHi & 255;
+                if (!kFp8 && (z0 > 0 || z1 < kKeyTile)) {
+                    // keys that no row sees hold anything, NaN among it: 0 * NaN would reach o
+                    uint4* row = reinterpret_cast<uint4*>(ring + ve * C::kEntryBytes);
+                    for (int i = lane; i < kKeyTile * 8; i += 32)
+                        if (i / 8 < z0 || i / 8 >= z1)
+#pragma unroll
+                            for (int b = 0; b < C::kCols; ++b)
+                                row[b * (C::kBlockBytes / 16) + i] = make_uint4(0, 0, 0, 0);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                next();
+                // within a query tile the next scores of a half follow its product at once; those of
+                // another query tile wait for its rows, and both halves' products come first
+                const bool last = cmd & kLastK;
+                uint32_t then = 0;
+                if (cmd & kAct0) {
+                    wait(&p_full[0], np0++ & 1);
+                    tc::tc_fence_after();
+                    values(0, ve, cmd & kFirst0 ? 0 : 1);
+                }
+                if (!last) {
+                    then = keys();
+                    if (then & kAct0) scores(0, e);
+                }
+                if (cmd & (kAct0 << 1)) {
+                    wait(&p_full[1], np1++ & 1);
+                    tc::tc_fence_after();
+                    values(1, ve, cmd & (kFirst0 << 1) ? 0 : 1);
+                }
+                commit(&empty[ve]);
+                if (last) {
+                    then = keys();
+                    if (then & kAct0) scores(0, e);
+                }
+                if (then & (kAct0 << 1)) scores(1, e);
+                if (!(then & kStop)) keys_done(then);
+                cmd = then;
+            }
+            commit(done);
             tc::mbar_wait_bounded(done, 0);
         }
     } else if (kFp8 && warp >= 8) {
@@ -434,18 +477,24 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
         // lane fall into different banks.
         const int quad = lane >> 2, c4 = lane & 3;
         const int row8 = (quad >> 1) ^ ((quad & 1) * 5);
-        while (more(cur)) {
-            const Item it = take(p, cur);
-            for (int i = 0; i < 2 * it.n; ++i) {  // K, V, K, V, ...
-                const int key0 = (it.k0 + i / 2) * kKeyTile;
+        {
+            for (;;) {  // K, V, K, V, ...
                 wait(&raw_full[re], rturn & 1);
                 if (turn > 0) wait(&empty[e], (turn - 1) & 1);
+                const uint32_t cmd = raw_cmds[re];
+                if (lane == 0 && warp == 8) cmds[e] = cmd;
+                if (cmd & kStop) {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&full[e]);
+                    break;
+                }
+                const int z0 = cmd >> kSeenLo & 255, z1 = cmd >> kSeenHi & 255;
                 const uint8_t* src = raw + re * C::kRawBytes;
                 uint8_t* dst = ring + e * C::kEntryBytes;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int r = (warp - 8) * 32 + g * 8 + row8;
-                    const bool seen = key0 + r >= it.s.lo && key0 + r < it.s.hi;
+                    const bool seen = r >= z0 && r < z1;
                     const int b = seen ? scales[re * kKeyTile + r] : 0;
                     // code * 2^-120 -> code * 2^(b - 127): in one exact product while 2^(b - 7) is finite
                     const uint32_t f1 = (uint32_t)(b == 255 ? 0x7fc0 : b > 134 ? 0x7b80 : (b + 120) << 7) * 0x10001u;
