@@ -32,7 +32,7 @@ constexpr int kKeyTile = 128;
 constexpr int kMaxCtas = 1024;     // counters at the front of the workspace
 constexpr int kMaxRows = 256;      // rows of the largest query tile
 
-// One part of a split tile: [rows][head_dim] o, then [rows] (max, sum).
+// One part of a split tile: o (rows x head_dim, in the kernel's own order), then [rows] (max, sum).
 constexpr size_t kPartBytes = (size_t)kMaxRows * 128 * 4 + (size_t)kMaxRows * 8;
 
 struct Params {
@@ -315,26 +315,31 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// 2^e as a float, 0 below its range.
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __int_as_float((min(e, 127) + 127) << 23); }
+
+// Four e4m3 codes as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+// The power of two that brings a row whose largest magnitude has the bf16 bits mx into
+// [2^14, 2^15), at most 2^100 (a row of zeros, or of numbers so small that its scores are 0).
+__device__ __forceinline__ int f16_row_exp(uint32_t mx) { return min(14 - ((int)(mx >> 7) - 127), 100); }
+
+constexpr int kPBits = 7;       // e4m3: probabilities are multiplied by 2^7
+constexpr float kLoose = 8.0f;  // log2 of how far a row's maximum may run ahead of the one in use
+
 // The value of a UE8M0 scale byte (255: NaN).
 __device__ __forceinline__ float scale_of(uint8_t b) {
     return b == 255 ? CUDART_NAN_F : __uint_as_float((uint32_t)b << 23);
 }
-
-// Four e4m3 codes -> the bf16 pairs of bytes (a, b) and (c, d), times 2^-120.
-template <int kSelLo, int kSelHi>
-__device__ __forceinline__ void e4m3_spread(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    // a code's sign, exponent and significand moved to bf16's places: its value times 2^-120
-    // (subnormal codes included), which one exact product undoes
-    const uint32_t x = __byte_perm(w, 0, kSelLo), y = __byte_perm(w, 0, kSelHi);
-    lo = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-    hi = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-constexpr uint32_t kTwo120 = 0x7b807b80u;  // 2^120 twice
 
 __device__ __forceinline__ float* part_o(const Params& p, int cta, int slot) {
     return reinterpret_cast<float*>(p.parts + ((size_t)cta * 2 + slot) * kPartBytes);
@@ -352,68 +357,29 @@ __device__ __forceinline__ RowAt row_at(const Params& p, const Item& it, int r) 
     return {it.r.row0 + it.tile * p.tokens_per_tile + t, it.head * p.group + (r - t * p.group)};
 }
 
-// kThreads threads (ids 0 .. kThreads-1, each with its barrier): counts this CTA's stored
-// part, and, as the tile's last, forms the output rows from all parts.  `sync` is a barrier
-// over those threads, `last` a shared int.
-template <int kD, int kThreads, typename Sync, typename RowMap>
-__device__ void join(const Params& p, const Item& it, const Start& st, int tid, int* last, Sync sync, int rows,
-                     RowMap row_map) {
-    const int c0 = cta_of(st, it.tile_unit), c1 = cta_of(st, it.tile_unit + it.units - 1);
+// The CTAs whose parts make up a split tile.
+struct Parts {
+    int first, last;
+};
+// Threads with ids 0 .. n-1 and their barrier `sync`: counts this CTA's stored part; true in all of
+// them if it was the tile's last (`flag`: a shared int).
+template <typename Sync>
+__device__ bool join_last(const Params& p, const Item& it, const Start& st, int tid, int* flag, Sync sync,
+                          Parts& parts) {
+    parts.first = cta_of(st, it.tile_unit);
+    parts.last = cta_of(st, it.tile_unit + it.units - 1);
     sync();  // the CTA's stores come before thread 0's fence and count
     if (tid == 0) {
         __threadfence();
-        const uint32_t seen = atomicAdd(&p.counters[c0], 1u);
-        *last = seen == (uint32_t)(c1 - c0);
-        if (*last) p.counters[c0] = 0;
+        const uint32_t seen = atomicAdd(&p.counters[parts.first], 1u);
+        *flag = seen == (uint32_t)(parts.last - parts.first);
+        if (*flag) p.counters[parts.first] = 0;
         __threadfence();
     }
     sync();
-    if (*last) {
-        constexpr int kPer = kD / 4;  // threads a row: four columns each
-        constexpr int kBatch = 8;     // parts whose loads are under way together
-        for (int r = tid / kPer; r < rows; r += kThreads / kPer) {
-            const int d = (tid % kPer) * 4;
-            float m = -CUDART_INF_F, l = 0.0f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int b0 = c0; b0 <= c1; b0 += kBatch) {
-                float2 ml[kBatch];
-                float4 x[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int c = b0 + i, slot = c == c0 ? 0 : 1;
-                    ml[i] = make_float2(-CUDART_INF_F, 0.0f);
-                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c <= c1) {
-                        ml[i] = __ldcg(part_ml(p, c, slot) + r);
-                        x[i] = __ldcg(reinterpret_cast<const float4*>(part_o(p, c, slot) + (size_t)r * kD + d));
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const float mn = fmaxf(m, ml[i].x);
-                    const float base = mn == -CUDART_INF_F ? 0.0f : mn;
-                    const float fa = exp2_fast(m - base), fb = exp2_fast(ml[i].x - base);
-                    l = l * fa + ml[i].y * fb;
-                    o.x = o.x * fa + x[i].x * fb;
-                    o.y = o.y * fa + x[i].y * fb;
-                    o.z = o.z * fa + x[i].z * fb;
-                    o.w = o.w * fa + x[i].w * fb;
-                    m = mn;
-                }
-            }
-            const int q = row_map(r);
-            if (q < 0) continue;
-            const RowAt at = row_at(p, it, q);
-            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-            *reinterpret_cast<uint2*>(p.o + at.token * p.o_ld + at.head * p.o_head + d) =
-                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            if (p.lse && d == 0)
-                p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
-                    l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-        }
-    }
-    sync();
+    return *flag;
 }
+__device__ __forceinline__ int part_slot(const Parts& parts, int c) { return c == parts.first ? 0 : 1; }
 
 // Tensor map of a pool for boxes of up to kKeyTile tokens of one head: (d, token, head, page).
 bool make_pool_map(CUtensorMap* m, const moe_kv_cache& c, const void* base);

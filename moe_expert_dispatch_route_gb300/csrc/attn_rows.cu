@@ -32,9 +32,6 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr float kLoose = 8.0f;  // log2 of how far the maximum may run ahead
-constexpr int kPBits = 7;       // e4m3: probabilities are multiplied by 2^7
-
 // What the consumers know of a query tile, in shared memory.
 template <int kRows>
 struct TileInfo {
@@ -120,20 +117,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four e4m3 codes as two fp16 pairs.
-__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-// 2^e as a float, 0 below its range.
-__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __int_as_float((min(e, 127) + 127) << 23); }
-
 // Byte offset of 16-byte chunk `c` of key row `r` in a tile as TMA's swizzle left it.
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
@@ -221,9 +204,7 @@ __device__ void stage_rows(const Params& p, const Item& it, RowLoads<kD, kRows>&
             mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
             for (int o = Loads::kPieces / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // largest element's exponent -> 14, by at most 2^100 (a row of zeros, or of numbers so small
-            // that its scores are 0); in two factors, each a float
-            const int up = min(14 - ((int)(mx >> 7) - 127), 100), u1 = up / 2, u2 = up - u1;
+            const int up = f16_row_exp(mx), u1 = up / 2, u2 = up - u1;  // in two factors, each a float
             uint32_t f[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -235,6 +216,51 @@ __device__ void stage_rows(const Params& p, const Item& it, RowLoads<kD, kRows>&
             *reinterpret_cast<uint2*>(at + 16) = make_uint2(f[1], f[3]);
             if (piece == 0) info->row_scale[r] = p.scale_log2 * pow2(-u1) * pow2(-u2);
         }
+    }
+}
+
+// The output rows of a split tile from its parts, in CTA order: a thread takes four columns of a
+// row, the loads of eight parts under way together (a long context is split over the whole GPU).
+template <int kD, int kThreads>
+__device__ void join_rows(const Params& p, const Item& it, const Parts& parts, int rows) {
+    constexpr int kPer = kD / 4, kBatch = 8;
+    for (int r = threadIdx.x / kPer; r < rows; r += kThreads / kPer) {
+        const int d = (threadIdx.x % kPer) * 4;
+        float m = -CUDART_INF_F, l = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b0 = parts.first; b0 <= parts.last; b0 += kBatch) {
+            float2 ml[kBatch];
+            float4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int c = b0 + i, slot = part_slot(parts, c);
+                ml[i] = make_float2(-CUDART_INF_F, 0.0f);
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c <= parts.last) {
+                    ml[i] = __ldcg(part_ml(p, c, slot) + r);
+                    x[i] = __ldcg(reinterpret_cast<const float4*>(part_o(p, c, slot) + (size_t)r * kD + d));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float mn = fmaxf(m, ml[i].x);
+                const float base = mn == -CUDART_INF_F ? 0.0f : mn;
+                const float fa = exp2_fast(m - base), fb = exp2_fast(ml[i].x - base);
+                l = l * fa + ml[i].y * fb;
+                o.x = o.x * fa + x[i].x * fb;
+                o.y = o.y * fa + x[i].y * fb;
+                o.z = o.z * fa + x[i].z * fb;
+                o.w = o.w * fa + x[i].w * fb;
+                m = mn;
+            }
+        }
+        const RowAt at = row_at(p, it, r);
+        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        *reinterpret_cast<uint2*>(p.o + at.token * p.o_ld + at.head * p.o_head + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse && d == 0)
+            p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
+                l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -738,10 +764,11 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                 if (d == 0) part_ml(p, blockIdx.x, slot)[r] = ml;
             }
         }
-        if (!it.whole)
-            join<kD, C::kConsumers>(p, it, start, threadIdx.x, &last_s, sync, rows, [](int r) { return r; });
-        else
-            sync();
+        if (!it.whole) {
+            Parts parts;
+            if (join_last(p, it, start, threadIdx.x, &last_s, sync, parts)) join_rows<kD, C::kConsumers>(p, it, parts, rows);
+        }
+        sync();
         if (threadIdx.x == 0) tc::mbar_arrive(&info_empty[buf]);
     }
 }
