@@ -12,6 +12,8 @@ using namespace moe;
 
 namespace {
 
+// A call without an SM budget may have more CTAs than fit at once where they are short and alike.
+int grid_cap_any(int max_ctas) { return max_ctas > 0 ? max_ctas : INT32_MAX; }
 int grid_cap_of(int max_ctas) { return max_ctas > 0 ? max_ctas : device_info().num_sms * 8; }
 
 moe_status cuda_status(cudaError_t e) {
@@ -57,7 +59,7 @@ moe_status moe_kv_write(const moe_kv_cache* cache, int32_t T, const void* k, con
     if (!aligned16(k) || !aligned16(v) || !aligned_to(slots, 8) || ld_k % 8 || ld_v % 8 || head_stride % 8)
         return MOE_ERR_ALIGNMENT;
     return cuda_status(launch_kv_write(*cache, T, k, v, ld_k, ld_v, head_stride, slots, err_flag,
-                                       grid_cap_of(max_ctas), (cudaStream_t)stream));
+                                       grid_cap_any(max_ctas), (cudaStream_t)stream));
 }
 
 moe_status moe_kv_read(const moe_kv_cache* cache, int32_t B, int32_t T, const int32_t* block_table, int32_t table_ld,
@@ -70,7 +72,7 @@ moe_status moe_kv_read(const moe_kv_cache* cache, int32_t B, int32_t T, const in
     if (!block_table || !start || !cu_len || !k_out || !v_out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(k_out) || !aligned16(v_out)) return MOE_ERR_ALIGNMENT;
     return cuda_status(launch_kv_read(*cache, B, T, block_table, table_ld, start, cu_len, k_out, v_out, err_flag,
-                                      grid_cap_of(max_ctas), (cudaStream_t)stream));
+                                      grid_cap_any(max_ctas), (cudaStream_t)stream));
 }
 
 size_t moe_attn_workspace_size(const moe_kv_cache* cache, int32_t num_q_heads) {
@@ -117,7 +119,7 @@ moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t
     if (!aligned_to(target, el) || !aligned_to(draft, el)) return MOE_ERR_ALIGNMENT;
     return cuda_status(launch_draft_verify(B, vocab, max_draft, dtype == MOE_F32, target, target_ld, draft, draft_ld,
                                            cu_draft, ids, u, u_draw, out_ids, out_len, err_flag,
-                                           grid_cap_of(max_ctas), (cudaStream_t)stream));
+                                           grid_cap_any(max_ctas), (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -564,22 +564,32 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             if (values) ++tile;
             const uint8_t* src = raw + re * C::kRawBytes;
             uint8_t* dst = ring + e * C::kEntryBytes;
+            auto chunk_at = [&](int r, int hf) {
+                return *reinterpret_cast<const uint4*>(src + (kD == 128 ? r * 128 + (((hf * 4 + c4) ^ (r & 7)) << 4)
+                                                                        : r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)));
+            };
+            const int first = (warp - 8) * 32 + row8;
+            uint4 w[C::kCols];  // read a step ahead
+            int b = sc[first];
+#pragma unroll
+            for (int hf = 0; hf < C::kCols; ++hf) w[hf] = chunk_at(first, hf);
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
-                const int r = (warp - 8) * 32 + g * 8 + row8;
+                const int r = first + g * 8, r2 = first + (g < 3 ? g + 1 : 3) * 8;
                 const bool seen = r >= z0 && r < z1;
-                const int b = sc[r], ex = b - (int)top;  // 2^ex in fp16, subnormal below 2^-14
+                const int ex = b - (int)top;  // 2^ex in fp16, subnormal below 2^-14
                 const uint32_t f = (b == 255    ? 0x7e00u
                                     : ex >= -14 ? (uint32_t)(ex + 15) << 10
                                     : ex >= -24 ? 1u << (ex + 24)
                                                 : 0u) *
                                    0x10001u;
+                const int b2 = sc[r2];
+                uint4 w2[C::kCols];
+#pragma unroll
+                for (int hf = 0; hf < C::kCols; ++hf) w2[hf] = chunk_at(r2, hf);
 #pragma unroll
                 for (int hf = 0; hf < C::kCols; ++hf) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(
-                        src + (kD == 128 ? r * 128 + (((hf * 4 + c4) ^ (r & 7)) << 4)
-                                         : r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)));
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    const uint32_t x[4] = {w[hf].x, w[hf].y, w[hf].z, w[hf].w};
                     uint32_t o[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -595,7 +605,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     *reinterpret_cast<uint4*>(to + (((2 * c4) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4*>(to + (((2 * c4 + 1) ^ (r & 7)) << 4)) =
                         make_uint4(o[4], o[5], o[6], o[7]);
+                    w[hf] = w2[hf];
                 }
+                b = b2;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();

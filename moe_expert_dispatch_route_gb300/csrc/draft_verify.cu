@@ -4,7 +4,8 @@
 // of 2^-40), so partial sums may be formed in any order and split over any number of threads,
 // and the token is the same: a thread-block cluster shares one request's row, each warp sums
 // a contiguous segment, the 8 CTAs exchange their totals over distributed shared memory, and
-// the one warp whose segment holds the threshold walks that segment again (it is in L2).
+// the CTA whose part holds the threshold reads the one warp's segment again (it is in L2), a few
+// elements a thread.
 // HBM bounds a large batch (one row of the target, two where a token was refused, read once);
 // a single request is bound by the latency of the few dependent steps.
 #include "common.cuh"
@@ -14,7 +15,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;  // CTAs sharing one request's row (the portable cluster size)
 constexpr int kSegs = kCluster * kWarps;
@@ -50,7 +51,7 @@ __device__ __forceinline__ void fixed40(float r, uint32_t& hi, uint32_t& lo) {
     lo = __float_as_uint(b) - 0x41000000u;
 }
 
-// kVec consecutive values from element i (a multiple of kVec).
+// kVec consecutive values from element i (a multiple of kVec): 16 bytes, or one value.
 template <bool kF32, int kVec>
 __device__ __forceinline__ void load_vec(const void* row, int i, float (&x)[kVec]) {
     if (kVec == 1) {
@@ -59,9 +60,10 @@ __device__ __forceinline__ void load_vec(const void* row, int i, float (&x)[kVec
         const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + i);
         x[0] = f.x, x[1 % kVec] = f.y, x[2 % kVec] = f.z, x[3 % kVec] = f.w;
     } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + i);
-        x[0] = bf16_bits_to_f((uint16_t)w.x), x[1 % kVec] = bf16_bits_to_f((uint16_t)(w.x >> 16));
-        x[2 % kVec] = bf16_bits_to_f((uint16_t)w.y), x[3 % kVec] = bf16_bits_to_f((uint16_t)(w.y >> 16));
+        const uint4 f = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
+        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = bf16_bits_to_f((uint16_t)(w[e / 2 % 4] >> (16 * (e & 1))));
     }
 }
 
@@ -96,14 +98,14 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 // This warp's sum over elements [lo, hi); the same in every lane.
 template <bool kF32, int kVec>
 __device__ uint64_t segment_sum(const Row<kF32, kVec>& row, int lo, int hi) {
-    constexpr int kUnroll = kVec == 1 ? 8 : 4;
+    constexpr int kUnroll = kVec == 1 ? 16 : 16 / kVec;
     const int lane = threadIdx.x & 31;
     uint64_t sum = 0;
     for (int i0 = lo + lane * kVec; i0 < hi; i0 += 32 * kVec * kUnroll) {
         float a[kUnroll][kVec], b[kUnroll][kVec];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) row.load(i0 + u * 32 * kVec, hi, a[u], b[u]);
-        uint32_t his = 0, los = 0;  // at most 16 * 2^20: no overflow
+        uint32_t his = 0, los = 0;  // at most 16 * 2^20 each: no overflow
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
@@ -119,19 +121,21 @@ __device__ uint64_t segment_sum(const Row<kF32, kVec>& row, int lo, int hi) {
     return warp_sum64(sum);
 }
 
-// The lowest element of [lo, hi) whose cumulative sum within the segment exceeds `want`
-// (there is one); the same in every lane.
+// Whole CTA: the lowest element of [lo, hi) whose cumulative sum within the segment exceeds `want`
+// (there is one), in the thread that finds it; -1 in the others.
 template <bool kF32, int kVec>
-__device__ int segment_find(const Row<kF32, kVec>& row, int lo, int hi, uint64_t want) {
-    const int lane = threadIdx.x & 31;
-    for (int i0 = lo; i0 < hi; i0 += 32 * kVec) {
-        const int i = i0 + lane * kVec;
-        float a[kVec], b[kVec];
-        row.load(i, hi, a, b);
-        uint64_t w[kVec], mine = 0;
+__device__ int segment_find(const Row<kF32, kVec>& row, int lo, int hi, uint64_t want, uint64_t* warp_sums) {
+    constexpr int kPer = 8, kLoads = kPer / kVec;  // consecutive elements of a thread
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i0 = lo; i0 < hi; i0 += kThreads * kPer) {
+        const int i = i0 + threadIdx.x * kPer;
+        float a[kLoads][kVec], b[kLoads][kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            w[e] = i < hi ? row.weight(i + e, a[e], b[e]) : 0;
+        for (int u = 0; u < kLoads; ++u) row.load(i + u * kVec, hi, a[u], b[u]);
+        uint64_t w[kPer], mine = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            w[e] = i + e < hi ? row.weight(i + e, a[e / kVec][e % kVec], b[e / kVec][e % kVec]) : 0;
             mine += w[e];
         }
         uint64_t incl = mine;
@@ -140,29 +144,32 @@ __device__ int segment_find(const Row<kF32, kVec>& row, int lo, int hi, uint64_t
             const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
         }
-        const uint32_t over = __ballot_sync(0xffffffffu, incl > want);
-        if (over) {
-            const int src = __ffs(over) - 1;
-            uint64_t run = incl - mine;
-            int found = kVec - 1;
+        if (lane == 31) warp_sums[warp] = incl;
+        __syncthreads();
+        uint64_t run = incl - mine, all = 0;
 #pragma unroll
-            for (int e = kVec - 1; e >= 0; --e) {
-                uint64_t upto = run;
-#pragma unroll
-                for (int f = 0; f <= e; ++f) upto += w[f];
-                if (upto > want) found = e;
-            }
-            return __shfl_sync(0xffffffffu, i + found, src);
+        for (int k = 0; k < kWarps; ++k) {
+            if (k < warp) run += warp_sums[k];
+            all += warp_sums[k];
         }
-        want -= __shfl_sync(0xffffffffu, incl, 31);
+        __syncthreads();
+        if (want < all) {  // the same in every thread
+            if (want < run || want >= run + mine) return -1;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                run += w[e];
+                if (want < run) return i + e;
+            }
+        }
+        want -= all;
     }
     return -1;
 }
 
 template <bool kF32, int kVec>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
+__global__ void __launch_bounds__(kThreads, 4) __cluster_dims__(kCluster, 1, 1)
     draft_verify_kernel(const __grid_constant__ VerifyParams p, int B) {
-    __shared__ uint64_t warp_tot[kWarps];
+    __shared__ uint64_t warp_tot[kWarps], find_sums[kWarps];
     __shared__ uint64_t cta_tot[2][kCluster];  // [pass][rank]: every CTA's total, written by its owner
     __shared__ int count_s;
     tc::cluster_sync();  // every CTA of the cluster runs before any writes another's shared memory
@@ -249,12 +256,11 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
         int32_t* out = p.out_ids + (int64_t)b * (p.max_draft + 1);
         if (want >= before && want < before + own) {  // this CTA's part holds the token
             uint64_t w = want - before;
-            int mine = 0;
-            for (; mine < kWarps - 1 && w >= warp_tot[mine]; ++mine) w -= warp_tot[mine];
-            if (mine == warp) {
-                const int tok = segment_find(row, s0, s1, w);
-                if (lane == 0) out[c] = tok;
-            }
+            int seg_of = 0;
+            for (; seg_of < kWarps - 1 && w >= warp_tot[seg_of]; ++seg_of) w -= warp_tot[seg_of];
+            const int lo = min((int)(rank * kWarps + seg_of) * seg, p.V), hi = min(lo + seg, p.V);
+            const int tok = segment_find(row, lo, hi, w, find_sums);
+            if (tok >= 0) out[c] = tok;
         }
         if (rank == 0) {
             if (threadIdx.x == 0) {
@@ -279,14 +285,13 @@ cudaError_t launch_draft_verify(int B, int V, int max_draft, bool f32, const voi
                                 const float* u, const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err,
                                 int grid_cap, cudaStream_t st) {
     VerifyParams p{V, max_draft, ids && u ? max_draft : 0, target, target_ld, draft, draft_ld, cu, ids, u, u_draw, out_ids, out_len, err};
-    // four values a load where every row starts on such a boundary and ends on one
+    // 16 bytes a load where every row starts on such a boundary and ends on one
     const int64_t lds = target_ld | (draft ? draft_ld : 0) | V;
-    const uintptr_t mask = f32 ? 15 : 7;
-    const bool vec = lds % 4 == 0 && ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & mask) == 0;
+    const bool vec = lds % (f32 ? 4 : 8) == 0 && aligned16(target) && aligned16(draft);
     int64_t clusters = grid_cap / kCluster < 1 ? 1 : grid_cap / kCluster;
     if (clusters > B) clusters = B;
     auto kern = f32 ? (vec ? draft_verify_kernel<true, 4> : draft_verify_kernel<true, 1>)
-                    : (vec ? draft_verify_kernel<false, 4> : draft_verify_kernel<false, 1>);
+                    : (vec ? draft_verify_kernel<false, 8> : draft_verify_kernel<false, 1>);
     return launch_pdl(kern, (int)clusters * kCluster, kThreads, 0, st, p, B);
 }
 

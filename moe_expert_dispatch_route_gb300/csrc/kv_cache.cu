@@ -14,9 +14,14 @@ __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w <<
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // ---------------------------------------------------------------- write
-// kLanes = head_dim / 8 lanes hold one (token, k or v, head) row, 8 values each.  A row's
-// largest magnitude is a maximum over packed bf16 pairs and kLanes lanes (shuffles).
-template <int kLanes, bool kFp8, int kUnroll>
+// kLanes = head_dim / 8 lanes hold one (token, k or v, head) row, 8 values each, and take the
+// heads of a token in turn, kUnroll rows on their way at once: slot and addresses are found once a
+// token.  A row's largest magnitude is a maximum over packed bf16 pairs and kLanes lanes.
+// The e4m3 form is bound by issue slots before it is by HBM, so its scale comes from the bits of
+// the largest bf16 magnitude and scaling is one product.
+constexpr int kUnroll = 4;
+
+template <int kLanes, bool kFp8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ moe_kv_cache c, int T,
                                                             const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ v, int64_t ld_k, int64_t ld_v,
@@ -25,71 +30,62 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
     pdl_begin();
     const int lane = threadIdx.x % kLanes;
     const int H = c.num_heads;
-    const int rows = T * 2 * H;  // host: fits
     const int64_t pool = (int64_t)c.num_pages * c.page_size;
     const int shift = __ffs(c.page_size) - 1;
-    const int group = (blockIdx.x * kThreads + threadIdx.x) / kLanes;
+    // groups of kLanes lanes over (token, k or v, run of kUnroll heads); every lane of a warp runs
+    // the same trips (shuffles below)
+    const int runs = (H + kUnroll - 1) / kUnroll, items = T * 2 * runs;  // host: fits
     const int ngroups = gridDim.x * (kThreads / kLanes);
-    const int base_step = ngroups * kUnroll;
-    // every lane of a warp runs the same trips (shuffles below): the bound is rounded up
-    const int warp_group0 = (blockIdx.x * kThreads + (threadIdx.x & ~31)) / kLanes;
-    for (int r0 = group, w0 = warp_group0; w0 < rows; r0 += base_step, w0 += base_step) {
+    const int mine = (blockIdx.x * kThreads + threadIdx.x) / kLanes;
+    const int warp_first = (blockIdx.x * kThreads + (threadIdx.x & ~31)) / kLanes;
+    for (int i = mine, w0 = warp_first; w0 < items; i += ngroups, w0 += ngroups) {
+        const int at = min(i, items - 1), h0 = at % runs * kUnroll, t = at / runs >> 1;
+        const bool is_v = at / runs & 1;
+        const uint16_t* src = (is_v ? v + t * ld_v : k + t * ld_k) + h0 * head_stride;
         uint4 x[kUnroll];
-        int64_t slot[kUnroll];
-        int h[kUnroll], is_v[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int r = r0 + i * ngroups;
-            slot[i] = -1;
-            x[i] = make_uint4(0, 0, 0, 0);
-            h[i] = is_v[i] = 0;
-            if (r < rows) {
-                const int t = r / (2 * H), rem = r - t * 2 * H;
-                is_v[i] = rem >= H;
-                h[i] = is_v[i] ? rem - H : rem;
-                slot[i] = slots[t];
-                const uint16_t* src = is_v[i] ? v + t * ld_v : k + t * ld_k;
-                x[i] = __ldcs(reinterpret_cast<const uint4*>(src + h[i] * head_stride) + lane);
-            }
+        for (int u = 0; u < kUnroll; ++u) {
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (h0 + u < H) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * head_stride) + lane);
         }
+        const int64_t slot = i < items ? slots[t] : -1;
+        if (slot >= pool && lane == 0) set_err(err, MOE_ERR_BAD_INDEX);
+        const bool ok = slot >= 0 && slot < pool;
+        const int64_t page = slot >> shift;
+        const int tok = (int)slot & (c.page_size - 1);
+        void* dst = is_v ? c.v : c.k;
+        const int64_t to = page * c.stride_page + h0 * c.stride_head + tok * c.stride_token;
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            bool ok = slot[i] >= 0;
-            if (slot[i] >= pool) {
-                if (lane == 0) set_err(err, MOE_ERR_BAD_INDEX);
-                ok = false;
-            }
-            const int64_t page = slot[i] >> shift;
-            const int tok = (int)slot[i] & (c.page_size - 1);
-            const int64_t at = page * c.stride_page + h[i] * c.stride_head + tok * c.stride_token;
-            void* dst = is_v[i] ? c.v : c.k;
+        for (int u = 0; u < kUnroll; ++u) {
+            if (h0 + u >= H) break;
             if (!kFp8) {
-                if (ok) reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + at)[lane] = x[i];
+                if (ok) reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + to + u * c.stride_head)[lane] = x[u];
                 continue;
             }
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
             uint32_t m = 0;  // the largest magnitude as bf16 bits: ordered as integers, NaN above infinity
 #pragma unroll
             for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
             m = max(m & 0xffffu, m >> 16);
+            // the lanes of a group alone: the other group of the warp may have fewer heads left
+            const uint32_t group = kLanes == 32 ? 0xffffffffu
+                                                : ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(group, m, o));
             if (!ok) continue;
-            const bool nan = m > 0x7f80u;
-            int s = m >= 0x7f80u ? kMaxExp : fp8_scale_exp(__uint_as_float(m << 16));  // infinite: saturates
-            s = min(max(s, kMinExp), kMaxExp);
-            const Pow2Factors f = pow2_neg(s);
+            // 448 = 1.75 * 2^8: s is amax's exponent less 8, one more above a significand of 1.75; the
+            // limits cover subnormals and infinity
+            const int s = m == 0 ? 0 : min(max((int)(m >> 7) - 135 + ((m & 0x7f) > 0x60), kMinExp), kMaxExp);
+            const float f = __int_as_float((127 - s) << 23);
             uint32_t q[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                q[j] = (uint32_t)f2_to_e4m3x2(scale_by(bf_lo(w[2 * j]), f), scale_by(bf_hi(w[2 * j]), f)) |
-                       ((uint32_t)f2_to_e4m3x2(scale_by(bf_lo(w[2 * j + 1]), f), scale_by(bf_hi(w[2 * j + 1]), f))
-                        << 16);
-            reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + at)[lane] = make_uint2(q[0], q[1]);
-            if (lane == 0) {
-                uint8_t* sc = is_v[i] ? c.v_scale : c.k_scale;
-                sc[(page * H + h[i]) * c.page_size + tok] = nan ? 255 : (uint8_t)(s + 127);
-            }
+                q[j] = (uint32_t)f2_to_e4m3x2(bf_lo(w[2 * j]) * f, bf_hi(w[2 * j]) * f) |
+                       ((uint32_t)f2_to_e4m3x2(bf_lo(w[2 * j + 1]) * f, bf_hi(w[2 * j + 1]) * f) << 16);
+            reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + to + u * c.stride_head)[lane] = make_uint2(q[0], q[1]);
+            if (lane == 0)
+                (is_v ? c.v_scale : c.k_scale)[(page * H + h0 + u) * c.page_size + tok] =
+                    m > 0x7f80u ? 255 : (uint8_t)(s + 127);
         }
     }
 }
@@ -196,15 +192,10 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 template <int kLanes, bool kFp8>
 cudaError_t write_as(const moe_kv_cache& c, int T, const void* k, const void* v, int64_t ld_k, int64_t ld_v,
                      int64_t head_stride, const int64_t* slots, int32_t* err, int grid_cap, cudaStream_t st) {
-    constexpr int kUnroll = 4;
-    const int64_t rows = (int64_t)T * 2 * c.num_heads;
-    const int64_t per_cta = kThreads / kLanes;
-    // one row a thread group while the GPU has room for it, several in flight beyond that
-    int64_t grid = (rows + per_cta - 1) / per_cta;
-    const bool few = grid <= (int64_t)device_info().num_sms * 8;
-    if (!few) grid = (grid + kUnroll - 1) / kUnroll;
+    const int64_t items = (int64_t)T * 2 * ((c.num_heads + kUnroll - 1) / kUnroll);
+    int64_t grid = (items * kLanes + kThreads - 1) / kThreads;
     if (grid > grid_cap) grid = grid_cap;
-    auto kern = few ? kv_write_kernel<kLanes, kFp8, 1> : kv_write_kernel<kLanes, kFp8, kUnroll>;
+    auto kern = kv_write_kernel<kLanes, kFp8>;
     return launch_pdl(kern, (int)grid, kThreads, 0, st, c, T, static_cast<const uint16_t*>(k),
                       static_cast<const uint16_t*>(v), ld_k, ld_v, head_stride, slots, err);
 }
