@@ -7,11 +7,15 @@
 //
 // Units.  A unit is one query tile against one tile of kKeyTile keys; masked-out key tiles
 // (after the causal diagonal, before the window) are no units, and a query tile that sees
-// no key at all counts as one.  Units are numbered request by request, head by head, query
-// tile by query tile, key tile by key tile, and each of the N = min(grid, U) CTAs takes a run of U/N of them, rounded up for the first
-// U mod N: ragged lengths cost no balance, and few rows over a long context are split over the whole GPU by
-// the same rule that gives a CTA many short requests.  Every CTA derives U and its first unit
-// from the lengths on the device, so nothing is read back to the host.
+// no key at all counts as one.  What a query tile takes beside its key tiles (its rows, its
+// output, the pipeline's turn) stands in front of them as item_cost units more.  Units are
+// numbered request by request, head by head, query tile by query tile, key tile by key tile,
+// and each of the N = min(grid, U) CTAs takes a run of U/N of them, rounded up for the first
+// U mod N: ragged lengths cost no balance, and few rows over a long context are split over
+// the whole GPU by the same rule that gives a CTA many short requests.  A boundary that falls
+// into a tile's item_cost, or leaves fewer than item_slack of its units, moves to the tile's
+// edge: no part of a tile is without keys, and none costs more than it spares.  Every CTA
+// derives its two boundaries from the lengths on the device, so nothing is read back.
 //
 // Joining.  A query tile whose units span CTAs c0 < .. < c1 is finished by the last of them
 // to arrive: each stores its part (unnormalised o, running maximum, sum) in its own slot of
@@ -50,6 +54,7 @@ struct Params {
     int num_pages, page_shift, page_size;
     float scale_log2;         // scale * log2(e): scores in powers of two
     int causal, window;
+    int item_cost, item_slack;  // in units
     int32_t* err;
     uint32_t* counters;       // [kMaxCtas], all zero between calls
     uint8_t* parts;           // [grid][2] parts: slot 0 the tile begun last, slot 1 the tile continued
@@ -97,22 +102,31 @@ struct Cursor {
     int b, head, tile;
     int unit;           // number of the tile's unit that comes first in this CTA's range
     int end;            // of the CTA's range
-    int skip;           // units of the tile before `unit`
+    int skip;           // units of the tile before `unit`, item_cost among them
     bool done;          // the tile has been taken: take() moves on first
     Request r;
 };
 
-struct Start {  // in shared memory, filled by locate()
-    int b, head, tile, skip;
-    int unit, end;
-    int each, more;  // units of a CTA; the first `more` CTAs have one more
+// The tile that a CTA's boundary falls into.
+struct Spot {
+    int b, head, tile;
+    int off, cost;  // units of the tile before the boundary, and all of them, item_cost among them
     Request r;
 };
+struct Start {  // in shared memory, filled by locate()
+    Spot spot[2];    // of the CTA's first unit and of the one past its last
+    int unit, end;   // its range, boundaries moved
+    bool next;       // it begins at the tile after spot[0]'s
+    int each, more;  // units of a CTA; the first `more` CTAs have one more
+};
 
-// The CTA that has unit u.
+// The CTA whose unmoved range has unit u.
 __device__ __forceinline__ int cta_of(const Start& st, int u) {
     const uint32_t first = (uint32_t)st.more * (st.each + 1), v = (uint32_t)u;
     return v < first ? v / (st.each + 1) : st.more + (v - first) / st.each;
+}
+__device__ __forceinline__ uint32_t cost_of(const Params& p, int units) {
+    return (uint32_t)(max(1, units) + p.item_cost);
 }
 
 __device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
@@ -140,7 +154,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     if (single) {
         for (int b = b0; b < b1; ++b) {
             r = request(p, b, blockIdx.x == 0);
-            const uint32_t u = r.n > 0 ? (uint32_t)max(1, span(p, r, 0).units) : 0u;
+            const uint32_t u = r.n > 0 ? cost_of(p, span(p, r, 0).units) : 0u;
             if (run > 1) per[b] = u;
             mine += u;
         }
@@ -149,7 +163,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
             const Request q = request(p, b, blockIdx.x == 0 && lane == 0);
             const int n = tiles_of(p, q);
             uint32_t s = 0;
-            for (int i = lane; i < n; i += 32) s += (uint32_t)max(1, span(p, q, i).units);
+            for (int i = lane; i < n; i += 32) s += cost_of(p, span(p, q, i).units);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (lane == 0) per[b] = s;
@@ -167,66 +181,91 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
         all += scratch[w];
     }
     const uint32_t total = all * (uint32_t)p.heads;  // host: below 2^31
-    // no CTA's range is empty but those of surplus CTAs: the CTAs of a split tile are consecutive
+    // no CTA's range is empty (before boundaries move) but those of surplus CTAs: the CTAs of a
+    // split tile are consecutive
     const uint32_t n = min((uint32_t)gridDim.x, total), me = blockIdx.x;
     const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
-    const uint32_t u0 = me < n ? me * each + min(me, rest) : total, u1 = me < n ? u0 + each + (me < rest) : total;
-    if (tid == 0) {
-        st->unit = (int)u0;
-        st->end = (int)u1;
-        st->each = (int)each;
-        st->more = (int)rest;
-    }
-    uint32_t at = (before + incl - mine) * (uint32_t)p.heads;
-    if (u0 < u1 && u0 >= at && u0 < at + mine * (uint32_t)p.heads) {
+    const uint32_t u[2] = {me < n ? me * each + min(me, rest) : total,
+                           me + 1 < n ? (me + 1) * each + min(me + 1, rest) : total};
+    const uint32_t at0 = (before + incl - mine) * (uint32_t)p.heads;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (u[i] >= total || u[i] < at0 || u[i] >= at0 + mine * (uint32_t)p.heads) continue;
+        uint32_t at = at0;
         for (int b = b0; b < b1; ++b) {
             const uint32_t one = single && run == 1 ? mine : per[b], k = one * (uint32_t)p.heads;
-            if (u0 < at + k) {
-                st->b = b;
-                st->head = (int)((u0 - at) / one);
-                st->skip = (int)((u0 - at) % one);  // units of this head's tiles before u0
-                st->tile = 0;
-                st->r = single && run == 1 ? r : request(p, b, false);
+            if (u[i] < at + k) {
+                Spot& s = st->spot[i];
+                s.b = b;
+                s.head = (int)((u[i] - at) / one);
+                s.tile = 0;
+                s.off = (int)((u[i] - at) % one);  // units of this head's tiles before it
+                s.cost = (int)one;
+                s.r = single && run == 1 ? r : request(p, b, false);
                 break;
             }
             at += k;
         }
     }
     __syncthreads();
-    if (single || u0 >= u1) return;
-    if (warp == 0) {
-        const Request q = st->r;
-        const int tiles = tiles_of(p, q);
-        uint32_t left = (uint32_t)st->skip;
-        for (int i0 = 0; i0 < tiles; i0 += 32) {
-            const uint32_t u = i0 + lane < tiles ? (uint32_t)max(1, span(p, q, i0 + lane).units) : 0u;
-            const uint32_t in = warp_incl(u);
-            const uint32_t over = __ballot_sync(0xffffffffu, in > left);
-            if (over) {
-                const int l = __ffs(over) - 1;
-                const uint32_t ex = __shfl_sync(0xffffffffu, in - u, l);
-                if (lane == 0) {
-                    st->tile = i0 + l;
-                    st->skip = (int)(left - ex);
+    if (!single) {
+        if (warp < 2 && u[warp & 1] < total) {
+            Spot& s = st->spot[warp];
+            const Request q = s.r;
+            const int tiles = tiles_of(p, q);
+            uint32_t left = (uint32_t)s.off;
+            __syncwarp();
+            for (int i0 = 0; i0 < tiles; i0 += 32) {
+                const uint32_t c = i0 + lane < tiles ? cost_of(p, span(p, q, i0 + lane).units) : 0u;
+                const uint32_t in = warp_incl(c);
+                const uint32_t over = __ballot_sync(0xffffffffu, in > left);
+                if (over) {
+                    if (lane == __ffs(over) - 1) {
+                        s.tile = i0 + lane;
+                        s.off = (int)(left - (in - c));
+                        s.cost = (int)c;
+                    }
+                    break;
                 }
-                break;
+                left -= __shfl_sync(0xffffffffu, in, 31);
             }
-            left -= __shfl_sync(0xffffffffu, in, 31);
         }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        int moved[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            moved[i] = (int)u[i];
+            if (i == 0) st->next = false;
+            if (u[i] >= total) continue;
+            const Spot& s = st->spot[i];
+            if (s.off <= p.item_cost) {
+                moved[i] -= s.off;
+                if (i == 0) st->spot[0].off = 0;
+            } else if (s.off >= s.cost - p.item_slack) {
+                moved[i] += s.cost - s.off;
+                if (i == 0) st->next = true;
+            }
+        }
+        st->unit = moved[0];
+        st->end = moved[1];
+        st->each = (int)each;
+        st->more = (int)rest;
     }
     __syncthreads();
 }
 
 __device__ __forceinline__ Cursor cursor(const Start& st) {
     Cursor c;
-    c.b = st.b;
-    c.head = st.head;
-    c.tile = st.tile;
+    c.b = st.spot[0].b;
+    c.head = st.spot[0].head;
+    c.tile = st.spot[0].tile;
+    c.skip = st.spot[0].off;
+    c.r = st.spot[0].r;
     c.unit = st.unit;
     c.end = st.end;
-    c.skip = st.skip;
-    c.done = false;
-    c.r = st.r;
+    c.done = st.next;
     return c;
 }
 
@@ -239,8 +278,8 @@ struct Item {
     int tokens;         // tokens of the query tile
     bool whole;         // no other CTA has units of this tile
     bool first;         // this CTA has the tile's first unit
-    int tile_unit;  // number of the tile's first unit
-    int units;          // the tile's units
+    int tile_unit;      // number of the tile's first unit
+    int cost;           // the tile's units, item_cost among them
 };
 
 __device__ __forceinline__ bool more(const Cursor& c) { return c.unit < c.end; }
@@ -266,13 +305,13 @@ __device__ __forceinline__ Item take(const Params& p, Cursor& c) {
     it.tile = c.tile;
     it.r = c.r;
     it.s = span(p, c.r, c.tile);
-    it.units = max(1, it.s.units);
+    it.cost = (int)cost_of(p, it.s.units);
     it.tile_unit = c.unit - c.skip;
-    const int n = min(it.units - c.skip, c.end - c.unit);
-    it.k0 = it.s.k0 + c.skip;
-    it.n = it.s.units ? n : 0;
+    const int n = min(it.cost - c.skip, c.end - c.unit);  // past item_cost: boundaries were moved
     it.first = c.skip == 0;
-    it.whole = n == it.units;
+    it.whole = n == it.cost;
+    it.k0 = it.s.k0 + (it.first ? 0 : c.skip - p.item_cost);
+    it.n = it.s.units ? n - (it.first ? p.item_cost : 0) : 0;
     it.tokens = min(p.tokens_per_tile, c.r.n - c.tile * p.tokens_per_tile);
     c.unit += n;
     c.done = true;
@@ -366,8 +405,8 @@ struct Parts {
 template <typename Sync>
 __device__ bool join_last(const Params& p, const Item& it, const Start& st, int tid, int* flag, Sync sync,
                           Parts& parts) {
-    parts.first = cta_of(st, it.tile_unit);
-    parts.last = cta_of(st, it.tile_unit + it.units - 1);
+    parts.first = cta_of(st, it.tile_unit + p.item_cost);
+    parts.last = cta_of(st, it.tile_unit + it.cost - p.item_slack - 1);
     sync();  // the CTA's stores come before thread 0's fence and count
     if (tid == 0) {
         __threadfence();
@@ -390,7 +429,7 @@ cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int rows, int grid_cap
 cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);
 
 inline int64_t most_units(const Params& p) {
-    return ((int64_t)p.T / p.tokens_per_tile + p.B) * p.heads * ((int64_t)p.max_kv / kKeyTile + 2);
+    return ((int64_t)p.T / p.tokens_per_tile + p.B) * p.heads * ((int64_t)p.max_kv / kKeyTile + 2 + p.item_cost);
 }
 // One CTA per SM, and no more CTAs than there can be units.
 inline int grid_for(const Params& p, int grid_cap) {

@@ -884,6 +884,9 @@ cudaError_t launch_as(const moe_kv_cache& c, const Params& p, int grid, cudaStre
 
 cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st) {
     p.tokens_per_tile = 2 * (kHalfRows / p.group);
+    // what a query tile costs beside its key tiles (1.7 us each) is about 7 us
+    p.item_cost = 4;
+    p.item_slack = 2;
     const int grid = grid_for(p, grid_cap);
     const bool fp8 = c.dtype == MOE_FP8_E4M3;
     if (c.head_dim == 128)
