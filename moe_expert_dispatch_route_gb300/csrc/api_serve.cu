@@ -97,7 +97,7 @@ moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, int
         return MOE_ERR_ALIGNMENT;
     // work is counted in 31 bits: tiles of as few tokens as any kernel takes, against tiles of keys
     const int64_t group = a->num_q_heads / cache->num_heads, rows = a->max_q * group;
-    const int64_t tokens = rows > 64 ? 128 / group * 2 : (rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64) / group;
+    const int64_t tokens = rows > kFewRows ? 128 / group * 2 : (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) / group;
     if ((a->T / tokens + a->B) * cache->num_heads > INT32_MAX / ((int64_t)a->max_kv / 128 + 16))
         return MOE_ERR_UNSUPPORTED;
     if (!a->workspace || a->workspace_bytes < attn_workspace_bytes()) return MOE_ERR_WORKSPACE;

@@ -146,6 +146,54 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool single = p.max_q <= p.tokens_per_tile;  // one query tile a request
+    if (single && p.B <= 32) {
+        // a small batch, whose call is mostly this and other latencies: one warp, one barrier
+        if (warp == 0) {
+            Request r = {0, 0, 0};
+            uint32_t one = 0;
+            if (lane < p.B) {
+                r = request(p, lane, blockIdx.x == 0);
+                if (r.n > 0) one = cost_of(p, span(p, r, 0).units);
+            }
+            const uint32_t k = one * (uint32_t)p.heads, upto = warp_incl(k), at = upto - k;
+            const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
+            const uint32_t n = min((uint32_t)gridDim.x, total), me = blockIdx.x;
+            const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
+            int moved[2];
+            bool next = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t u = me + i < n ? (me + i) * each + min(me + i, rest) : total;
+                moved[i] = (int)u;
+                const uint32_t mine = __ballot_sync(0xffffffffu, u < total && u >= at && u < upto);
+                if (mine == 0) continue;
+                const int b = __ffs(mine) - 1;
+                const uint32_t cost = __shfl_sync(0xffffffffu, one, b), in = u - __shfl_sync(0xffffffffu, at, b);
+                int off = (int)(in % cost);
+                if (off <= p.item_cost) {
+                    moved[i] -= off;
+                    off = 0;
+                } else if (off >= (int)cost - p.item_slack) {
+                    moved[i] += (int)cost - off;
+                    if (i == 0) next = true;
+                }
+                if (i == 0) {
+                    const int row0 = __shfl_sync(0xffffffffu, r.row0, b), rows = __shfl_sync(0xffffffffu, r.n, b);
+                    const int kv = __shfl_sync(0xffffffffu, r.kv, b);
+                    if (lane == 0) st->spot[0] = Spot{b, (int)(in / cost), 0, off, (int)cost, {row0, rows, kv}};
+                }
+            }
+            if (lane == 0) {
+                st->unit = moved[0];
+                st->end = moved[1];
+                st->next = next;
+                st->each = (int)each;
+                st->more = (int)rest;
+            }
+        }
+        __syncthreads();
+        return;
+    }
     uint32_t* per = scratch + 32;  // units of one head of request b, unless a thread has one request
     const int run = (p.B + kThreads - 1) / kThreads;  // requests per thread, consecutive
     const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
@@ -423,7 +471,7 @@ __device__ __forceinline__ int part_slot(const Parts& parts, int c) { return c =
 // Tensor map of a pool for boxes of up to kKeyTile tokens of one head: (d, token, head, page).
 bool make_pool_map(CUtensorMap* m, const moe_kv_cache& c, const void* base);
 
-// attn_rows.cu: requests of up to 64 rows a key/value head, on mma.sync, a tile's keys shared by warps
+// attn_rows.cu: requests of up to kFewRows rows a key/value head, on mma.sync, a tile's keys shared by warps
 cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st);
 // attn_tile.cu: query tiles of up to 256 rows on tcgen05
 cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);

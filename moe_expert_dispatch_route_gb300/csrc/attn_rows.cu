@@ -1,4 +1,4 @@
-// Paged attention for query tiles of up to 64 rows (a decode step, a draft).  The keys and
+// Paged attention for query tiles of up to 32 rows (a decode step, a draft).  The keys and
 // values of a request are read once and HBM bounds the work; the products run on mma.sync,
 // whose fragments keep scores, probabilities and output in registers, transposed:
 //   S^T = K Q^T    m = 16 keys, n = 8 rows      O^T += V^T P^T    m = 16 columns, n = 8 rows
@@ -47,11 +47,11 @@ struct Cfg {
     static constexpr int kElt = kFp8 ? 1 : 2;
     static constexpr int kRows = 8 * kNT * kRW;
     // Tile groups: with two stages each they overlap each other's waits; a few rows take so
-    // little time that one each will do; many rows of wide bf16 tiles, whose ring holds three
-    // (two for 64 rows, whose o needs the room), stay together on one tile.
+    // little time that one each will do; 32 rows of wide bf16 tiles, whose ring holds three,
+    // stay together on one tile.
     static constexpr bool kWide = kD * kElt == 256;
-    static constexpr int kTG = kRW == 1 ? 3 : kWide ? 1 : kRW == 2 ? 3 : 2;
-    static constexpr int kKW = kRW == 1 ? 4 : kWide ? 8 / kRW : kRW == 2 ? 2 : 1;
+    static constexpr int kTG = kRW == 2 && kWide ? 1 : 3;
+    static constexpr int kKW = kRW == 1 ? 4 : kWide ? 4 : 2;
     static constexpr int kMerged = kKW * kTG;  // key groups to be put together
     static constexpr int kWarps = kRW * kMerged;
     static constexpr int kConsumers = 32 * kWarps;
@@ -63,9 +63,8 @@ struct Cfg {
     static constexpr int kRowBytes = kD * kElt < 128 ? kD * kElt : 128;
     static constexpr int kHalves = kD * kElt / kRowBytes;  // 128-byte column blocks
     // stages of K and V: a multiple of kTG, so that a stage always serves the same tile group and
-    // no warp's wait can miss a phase.  192 KB in flight (128 KB for 64 rows) cover HBM's latency.
-    static constexpr int kStages = kRW == 4 ? (kTileBytes == 32768 ? 2 : kTileBytes == 16384 ? 4 : 8)
-                                            : (kTileBytes == 32768 ? 3 : kTileBytes == 16384 ? 6 : 9);
+    // no warp's wait can miss a phase.  192 KB in flight (144 KB of the smallest) cover HBM's latency.
+    static constexpr int kStages = kTileBytes == 32768 ? 3 : kTileBytes == 16384 ? 6 : 9;
     static constexpr int kRing = 2 * kStages * kTileBytes;
     static constexpr int kQStride = 2 * kD + 16;  // bytes; rows fall into different banks
     static constexpr int kOStride = kD + 4;       // floats; likewise
@@ -779,7 +778,7 @@ cudaError_t launch_as(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream
     p.tokens_per_tile = C::kRows / p.group;
     // what a query tile costs beside its key tiles is about 3 us, a K and V tile 1.5 us per 64 KB
     p.item_cost = 2 * 32768 / C::kTileBytes;
-    p.item_slack = p.item_cost / 2;
+    p.item_slack = 1;
     CUtensorMap km, vm;
     if (!make_pool_map(&km, c, c.k) || !make_pool_map(&vm, c, c.v)) return cudaErrorInvalidValue;
     auto kern = attn_rows_kernel<kD, kFp8, kNT, kRW>;
@@ -792,8 +791,7 @@ template <int kD, bool kFp8>
 cudaError_t launch_rows_as(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st) {
     if (rows <= 8) return launch_as<kD, kFp8, 1, 1>(c, p, grid_cap, st);
     if (rows <= 16) return launch_as<kD, kFp8, 2, 1>(c, p, grid_cap, st);
-    if (rows <= 32) return launch_as<kD, kFp8, 2, 2>(c, p, grid_cap, st);
-    return launch_as<kD, kFp8, 2, 4>(c, p, grid_cap, st);
+    return launch_as<kD, kFp8, 2, 2>(c, p, grid_cap, st);
 }
 
 }  // namespace

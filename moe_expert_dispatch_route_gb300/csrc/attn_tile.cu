@@ -886,7 +886,7 @@ cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStr
     p.tokens_per_tile = 2 * (kHalfRows / p.group);
     // what a query tile costs beside its key tiles (1.7 us each) is about 7 us
     p.item_cost = 4;
-    p.item_slack = 2;
+    p.item_slack = 1;
     const int grid = grid_for(p, grid_cap);
     const bool fp8 = c.dtype == MOE_FP8_E4M3;
     if (c.head_dim == 128)
