@@ -140,7 +140,8 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
 }
 
 // Whole CTA (kThreads threads): the CTA's range of units and the query tile it begins in.
-// scratch: shared, p.B + 32 uint32.  Ends with a barrier; st->unit == st->end: nothing to do.
+// scratch: shared, p.B + 32 uint32, free again for copies after it.  Ends with a barrier;
+// st->unit == st->end: nothing to do.
 template <int kThreads>
 __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     constexpr int kWarps = kThreads / 32;
@@ -301,6 +302,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
         st->each = (int)each;
         st->more = (int)rest;
     }
+    tc::fence_proxy_async_smem();  // the scratch may become copies' destination
     __syncthreads();
 }
 
@@ -455,13 +457,15 @@ __device__ bool join_last(const Params& p, const Item& it, const Start& st, int 
                           Parts& parts) {
     parts.first = cta_of(st, it.tile_unit + p.item_cost);
     parts.last = cta_of(st, it.tile_unit + it.cost - p.item_slack - 1);
-    sync();  // the CTA's stores come before thread 0's fence and count
+    sync();  // the CTA's stores come before thread 0's count, which releases them
     if (tid == 0) {
-        __threadfence();
-        const uint32_t seen = atomicAdd(&p.counters[parts.first], 1u);
+        uint32_t seen;  // and acquires those of the CTAs that counted before
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                     : "=r"(seen)
+                     : "l"(static_cast<uint64_t>(__cvta_generic_to_global(&p.counters[parts.first])))
+                     : "memory");
         *flag = seen == (uint32_t)(parts.last - parts.first);
         if (*flag) p.counters[parts.first] = 0;
-        __threadfence();
     }
     sync();
     return *flag;

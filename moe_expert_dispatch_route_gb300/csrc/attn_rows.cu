@@ -312,8 +312,6 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
         return;
     }
     locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
-    tc::fence_proxy_async_smem();  // the scratch becomes the copies' destination
-    __syncthreads();
     // a wait that runs out is reported and then passed, here and in every later wait, so that
     // each barrier is still met; the results are void
     auto wait = [&](uint64_t* bar, uint32_t parity) {

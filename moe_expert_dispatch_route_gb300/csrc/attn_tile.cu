@@ -295,8 +295,6 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
         tc::tc_fence_before();
     }
     locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
-    tc::fence_proxy_async_smem();  // the scratch becomes the copies' destination
-    __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_s;
     Cursor cur = cursor(start);
