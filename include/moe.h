@@ -481,10 +481,10 @@ typedef struct {
     const int32_t* kv_len;      /* device int32 [B] */
     const int32_t* block_table; /* device int32 [B][table_ld]: pages in order */
     int32_t table_ld;
-    int32_t T;                  /* rows of q and o */
+    int32_t T;                  /* rows of q and o, at most 2^30 */
     int32_t B;                  /* requests, at most 8192 */
     int32_t max_q;              /* upper bounds of the requests' query rows and kv_len; they size */
-    int32_t max_kv;             /* the launch, and a request above one sets MOE_ERR_BAD_INDEX */
+    int32_t max_kv;             /* the launch, and a request above one sets MOE_ERR_BAD_INDEX; max_kv <= 2^30 */
     int32_t num_q_heads;        /* a multiple of the cache's num_heads, at most 64 times it */
     float scale;                /* > 0 */
     int32_t causal;             /* 0 or 1 */
@@ -523,7 +523,8 @@ MOE_API moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args
  *          MOE_ERR_BAD_INDEX, and so does a request with n > max_draft (out_len 0).
  * u, u_draw device fp32 [cu_draft[B]], [B], in [0, 1) (outside it is taken as the nearest).
  * out_ids  device int32 [B][max_draft + 1] (out): kept tokens, the drawn one, then -1.
- * out_len  device int32 [B] (out): c + 1.   max_draft <= 255. */
+ * out_len  device int32 [B] (out): c + 1.   max_draft <= 255.
+ * max_ctas is rounded down to clusters of 8 CTAs, and up to one. */
 MOE_API moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t dtype, const void* target,
                                     int64_t target_ld, const void* draft, int64_t draft_ld,
                                     const int32_t* cu_draft, const int32_t* ids, const float* u,
@@ -537,8 +538,9 @@ MOE_API moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft,
  * wait, limited to timeout_ns, on a barrier that nothing ever completes, before it
  * issues any copy: the wait runs out, the kernel stores MOE_ERR_TIMEOUT in err_flag,
  * skips its work, frees its tensor memory and returns normally, so the context stays
- * usable.  The staged combine kernel takes the same path (its error goes to the
- * layer's err_flag, or, called on its own, to the word moe_comm_error reads).
+ * usable.  The attention kernels do the same.  The staged combine kernel takes the same
+ * path (its error goes to the layer's err_flag, or, called on its own, to the word
+ * moe_comm_error reads).
  * enable = 0 (the default) turns it off.  Process-wide, host-side only;
  * enable != 0 with timeout_ns <= 0 is MOE_ERR_INVALID_ARG. */
 MOE_API moe_status moe_debug_inject_wait(int32_t enable, int64_t timeout_ns);

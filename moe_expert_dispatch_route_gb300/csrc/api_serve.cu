@@ -89,6 +89,7 @@ moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, int
         return MOE_ERR_INVALID_ARG;
     if (a->causal != 0 && a->causal != 1) return MOE_ERR_INVALID_ARG;
     if (a->num_q_heads / cache->num_heads > 64 || a->B > kMaxRequests) return MOE_ERR_UNSUPPORTED;
+    if (a->T > kMaxTokens || a->max_kv > kMaxTokens) return MOE_ERR_UNSUPPORTED;
     if (a->T == 0 || a->B == 0 || a->max_q == 0) return MOE_OK;
     if (!a->q || !a->o || !a->cu_q || !a->kv_len || (a->table_ld > 0 && !a->block_table)) return MOE_ERR_INVALID_ARG;
     if (a->q_ld < 0 || a->q_head_stride < 0 || a->o_ld < 0 || a->o_head_stride < 0) return MOE_ERR_INVALID_ARG;

@@ -57,7 +57,7 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_
     while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.causal = a.causal;
-    p.window = a.window;
+    p.window = a.window < kMaxTokens ? a.window : kMaxTokens;  // no row is further from a token
     p.err = a.err_flag;
     p.counters = static_cast<uint32_t*>(a.workspace);
     p.parts = static_cast<uint8_t*>(a.workspace) + kMaxCtas * sizeof(uint32_t);

@@ -30,6 +30,29 @@
 #include "tc_ptx.cuh"
 
 namespace moe {
+namespace tc {
+
+// 4-D tiled load of the box at (c0 innermost, c1, c2, c3); completion is signalled on `bar` as
+// transaction bytes.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+        "%6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// True in one lane of a converged warp: the form in which single-thread instructions
+// (tcgen05.mma, its commit) are best issued, since the rest of the warp stays uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+}  // namespace tc
+
 namespace attn {
 
 constexpr int kKeyTile = 128;

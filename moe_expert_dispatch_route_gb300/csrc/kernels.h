@@ -152,6 +152,7 @@ cudaError_t launch_kv_read(const moe_kv_cache& c, int B, int T, const int32_t* t
 
 // attn.cu: paged attention (the kernels are in attn_rows.cu and attn_tile.cu)
 constexpr int kMaxRequests = 8192;
+constexpr int kMaxTokens = 1 << 30;  // rows, and cached tokens: positions less a window stay within 32 bits
 constexpr int kFewRows = 32;  // rows of a request and key/value head up to which attn_rows.cu takes the call
 size_t attn_workspace_bytes();
 cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_cap, cudaStream_t st);

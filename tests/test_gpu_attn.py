@@ -155,6 +155,16 @@ def test_windows(dtype, q_lens, window):
     Case(q_lens, [300, 700, 129], window=window, dtype=dtype).check()
 
 
+@pytest.mark.parametrize("q_lens", [[1, 4, 0], [150, 33, 5]])
+def test_the_widest_window(q_lens):
+    """A window past every position is none, also for rows that stand before the first token."""
+    c = Case(q_lens, [200, 3, 129])
+    o, lse = c.run()
+    c.args = c.make_args(window=2**31 - 1)
+    o2, lse2 = c.run()
+    assert np.array_equal(o, o2) and np.array_equal(lse, lse2)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("q_lens", [[1, 2, 3], [70, 5, 150]])
 @pytest.mark.parametrize("window", [0, 20])
@@ -204,6 +214,33 @@ def test_large_scores_and_a_large_scale():
         assert (np.abs(o[first:first + n] - ro) <= 2.0**-8 * np.abs(ro) + (2.0**-8 + 4e-3) * mag).all()
         assert np.abs(lse[first:first + n] - rl).max() <= 4e-3
         first += n
+
+
+@pytest.mark.parametrize("n", [1, 20, 70])
+@pytest.mark.parametrize("what", ["q0", "tiny q", "huge q", "far scales"])
+def test_e4m3_ranges(n, what):
+    """Rows of zeros and of extreme size, and key and value scales far from 1 and from each other:
+    what fp16 operands have to be scaled for.  An error may be 2^-31 of the largest number of its
+    kind (see the kernels), under the bound by far for these."""
+    c = Case([n, n], [300, 200], dtype="e4m3", seed=7)
+    f = {"q0": 0.0, "tiny q": 2.0**-120, "huge q": 2.0**100, "far scales": 1.0}[what]
+    c.q = (c.q.float() * f).to(torch.bfloat16)
+    c.qd[:, :c.Hq] = c.q.to(DEV)
+    if what == "huge q":  # against keys as small
+        c.keep[0] = torch.where(c.keep[0] == 255, c.keep[0], c.keep[0] - 90)
+        c.k = [k * 2.0**-90 for k in c.k]
+        c.scale = c.scale * 2.0**-10
+        c.args = c.make_args()
+    if what == "far scales":
+        rng = np.random.default_rng(1)
+        for b, kv in enumerate(c.kv_lens):
+            for j in range(kv):
+                page, at = int(c.table[b, j // 16]), j % 16
+                for i, t in ((0, c.k), (1, c.v)):
+                    up = int(rng.integers(-20, 21)) if i else -int(rng.integers(0, 30))
+                    c.keep[i, page, :, at] += up
+                    t[b][j] *= 2.0**up
+    c.check()
 
 
 @pytest.mark.parametrize("q_lens", [[1, 2], [150, 33]])

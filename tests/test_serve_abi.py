@@ -107,7 +107,7 @@ def test_attention_arguments(P):
                dict(o_head_stride=-8)):
         assert attn(P, c, **kw) == INVALID, kw
     big = 1 << 30
-    for kw in (dict(num_q_heads=130), dict(B=8193), dict(T=big, max_kv=big)):
+    for kw in (dict(num_q_heads=130), dict(B=8193), dict(T=big, max_kv=big), dict(T=big + 1), dict(max_kv=big + 1)):
         assert attn(P, c, **kw) == UNSUPPORTED, kw
     for kw in (dict(q=P(8)), dict(o=P(2)), dict(q_ld=1028), dict(q_head_stride=12), dict(o_ld=4)):
         assert attn(P, c, **kw) == ALIGNMENT, kw
