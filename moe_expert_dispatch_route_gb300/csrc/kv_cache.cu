@@ -91,15 +91,16 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- read
-// The 8 values of 8 e4m3 codes under 2^s: both steps exact for a scale moe_kv_write stores.
+// The 8 values of 8 e4m3 codes under 2^s: every step is exact for a scale moe_kv_write stores.
 __device__ __forceinline__ uint4 dequant8(uint2 q, uint8_t b) {
     const float f = b == 255 ? __uint_as_float(0x7fc00000u) : b == 0 ? 0x1p-127f : __uint_as_float((uint32_t)b << 23);
     const uint32_t w[2] = {q.x, q.y};
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint32_t two = w[j >> 1] >> (16 * (j & 1));
-        o[j] = pack_bf16x2(e4m3_to_f((uint8_t)two) * f, e4m3_to_f((uint8_t)(two >> 8)) * f);
+        const __half2_raw two = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+        const float2 v = __half22float2(__half2(two));
+        o[j] = pack_bf16x2(v.x * f, v.y * f);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
