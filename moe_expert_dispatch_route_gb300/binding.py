@@ -344,7 +344,7 @@ def _same(what, *pairs):
 
 
 def _vector(what, t, dtype, n):
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not dtype or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
         raise ValueError(f"{what}: a packed {dtype} vector of {n} is expected, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -386,21 +386,21 @@ def moe_kv_write(cache: MoeKvCache, k, v, slots, err_flag=None, max_ctas=0, stre
 
 def moe_kv_read(cache: MoeKvCache, block_table, start, cu_len, k_out, v_out, err_flag=None, max_ctas=0, stream=None):
     """Cached tokens [start[b], start[b] + n_b) of every request to rows of k_out, v_out (bf16)."""
-    B, T = start.shape[0], k_out.shape[0]
-    rows = (T, cache.num_heads, cache.head_dim)
-    for t in (k_out, v_out):
-        if t.shape != rows or t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError(f"moe_kv_read: outputs are packed bf16 {rows}, got {t.dtype} {tuple(t.shape)}")
+    B, shape = start.size(0), k_out.shape
+    if shape != (shape[0], cache.num_heads, cache.head_dim) or v_out.shape != shape or \
+            not (k_out.dtype is v_out.dtype is torch.bfloat16) or not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError(f"moe_kv_read: outputs are packed bf16 [rows][{cache.num_heads}][{cache.head_dim}], got "
+                         f"{k_out.dtype} {tuple(shape)} and {v_out.dtype} {tuple(v_out.shape)}")
     _table_ok("moe_kv_read", block_table, B)
     _vector("moe_kv_read: start", start, torch.int32, B)
     _vector("moe_kv_read: cu_len", cu_len, torch.int32, B + 1)
-    _check(lib().moe_kv_read(ctypes.byref(cache), B, T, _ptr(block_table), block_table.shape[1], _ptr(start),
-                             _ptr(cu_len), _ptr(k_out), _ptr(v_out), _ptr(err_flag), max_ctas, _stream(stream)),
-           "moe_kv_read")
+    _check(lib().moe_kv_read(ctypes.byref(cache), B, shape[0], block_table.data_ptr(), block_table.size(1),
+                             start.data_ptr(), cu_len.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _ptr(err_flag),
+                             max_ctas, _stream(stream)), "moe_kv_read")
 
 
 def _table_ok(where, t, B):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.size(0) != B or not t.is_contiguous():
         raise ValueError(f"{where}: the block table is packed int32 [{B}][pages], got {t.dtype} {tuple(t.shape)}")
 
 
@@ -437,25 +437,30 @@ def moe_draft_verify(target, draft, cu_draft, ids, u, u_draw, out_ids, out_len, 
                      stream=None):
     """Drafted tokens ids against target [N + B][vocab] and draft [N][vocab] (or None) probabilities
     (fp32 or bf16, rows at any stride) from uniform numbers u [N], u_draw [B]; see moe.h."""
-    B, V = out_len.shape[0], target.shape[1]
-    N = ids.shape[0] if ids is not None else 0
-    if target.dtype not in (torch.float32, torch.bfloat16) or target.stride(1) != 1 or target.shape[0] != N + B:
-        raise ValueError(f"moe_draft_verify: target is fp32 or bf16 [{N + B}][vocab], got {target.dtype} "
-                         f"{tuple(target.shape)}")
-    if draft is not None and (draft.dtype != target.dtype or draft.shape != (N, V) or draft.stride(1) != 1):
-        raise ValueError(f"moe_draft_verify: draft is {target.dtype} [{N}][{V}], got {draft.dtype} "
-                         f"{tuple(draft.shape)}")
-    _vector("moe_draft_verify: cu_draft", cu_draft, torch.int32, B + 1)
-    _vector("moe_draft_verify: u_draw", u_draw, torch.float32, B)
-    _vector("moe_draft_verify: out_len", out_len, torch.int32, B)
+    i32, f32 = torch.int32, torch.float32
+    B, (rows, V), dtype = out_len.size(0), target.shape, target.dtype
+    N = ids.size(0) if ids is not None else 0
+    target_ld, one = target.stride()
+    if one != 1 or rows != N + B or (dtype is not f32 and dtype is not torch.bfloat16):
+        raise ValueError(f"moe_draft_verify: target is fp32 or bf16 [{N + B}][vocab], got {dtype} {tuple(target.shape)}")
+    q, draft_ld = None, 0
+    if draft is not None:
+        draft_ld, one = draft.stride()
+        if one != 1 or draft.dtype is not dtype or draft.shape != (N, V):
+            raise ValueError(f"moe_draft_verify: draft is {dtype} [{N}][{V}], got {draft.dtype} {tuple(draft.shape)}")
+        if N:
+            q = draft.data_ptr()
+    _vector("moe_draft_verify: cu_draft", cu_draft, i32, B + 1)
+    _vector("moe_draft_verify: u_draw", u_draw, f32, B)
+    _vector("moe_draft_verify: out_len", out_len, i32, B)
     if N:
-        _vector("moe_draft_verify: ids", ids, torch.int32, N)
-        _vector("moe_draft_verify: u", u, torch.float32, N)
-    if out_ids.dtype != torch.int32 or out_ids.dim() != 2 or out_ids.shape[0] != B or not out_ids.is_contiguous():
+        _vector("moe_draft_verify: ids", ids, i32, N)
+        _vector("moe_draft_verify: u", u, f32, N)
+    if out_ids.dtype is not i32 or out_ids.dim() != 2 or out_ids.size(0) != B or not out_ids.is_contiguous():
         raise ValueError(f"moe_draft_verify: out_ids is packed int32 [{B}][max_draft + 1]")
-    _check(lib().moe_draft_verify(B, V, out_ids.shape[1] - 1, F32 if target.dtype == torch.float32 else BF16,
-                                  target.data_ptr(), target.stride(0) if target.shape[0] > 1 else V,
-                                  draft.data_ptr() if draft is not None and N else None,
-                                  0 if draft is None else draft.stride(0) if N > 1 else V, cu_draft.data_ptr(),
-                                  _ptr(ids), _ptr(u), u_draw.data_ptr(), out_ids.data_ptr(), out_len.data_ptr(),
-                                  _ptr(err_flag), max_ctas, _stream(stream)), "moe_draft_verify")
+    # the stride of a single row is not used, and may be any number
+    _check(lib().moe_draft_verify(B, V, out_ids.size(1) - 1, F32 if dtype is f32 else BF16, target.data_ptr(),
+                                  target_ld if rows > 1 else V, q, draft_ld if N > 1 else V, cu_draft.data_ptr(),
+                                  ids.data_ptr() if N else None, u.data_ptr() if N else None, u_draw.data_ptr(),
+                                  out_ids.data_ptr(), out_len.data_ptr(), _ptr(err_flag), max_ctas, _stream(stream)),
+           "moe_draft_verify")
