@@ -65,7 +65,8 @@ class Case:
         if fp8:
             pool = pool.view(E4M3)
             sc = torch.tensor(scales, device=DEV)
-        self.pool = pool if order == "hnd" else pool.transpose(2, 3).contiguous().transpose(2, 3)
+        a, b = {"hnd": (0, 0), "nhd": (2, 3), "head first": (1, 2)}[order]
+        self.pool = pool.transpose(a, b).contiguous().transpose(a, b)
         self.cache = B.kv_cache(self.pool[0], self.pool[1], *((sc[0], sc[1]) if fp8 else ()))
         self.keep = sc if fp8 else None
         # q and o as parts of wider buffers
@@ -117,6 +118,30 @@ class Case:
         assert torch.all(self.od[:, self.Hq:] == 77.0), "only o's heads are written"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_lens", [[1, 2, 1], [50, 200, 3]])
+def test_loose_bounds_and_spare_rows(dtype, q_lens):
+    """max_q and max_kv far above the lengths (so that a kernel for many rows gets few), a wider block
+    table, rows of q and o past the last request, and heads apart from each other in q and o."""
+    c = Case(q_lens, [90, 300, 257], dtype=dtype)
+    T, Hq, D = c.qd.shape
+    wide = lambda t, fill: torch.full((T + 5, Hq, 2 * D), fill, dtype=torch.bfloat16, device=DEV)
+    q, o = wide(c.qd, float("nan")), wide(c.od, 77.0)
+    q[:T, :, :D] = c.qd
+    table = torch.full((3, 40), -9, dtype=torch.int32, device=DEV)
+    table[:, :c.table.shape[1]] = c.table
+    lse = torch.full((T + 5, Hq), 77.0, device=DEV)
+    args = B.attn_args(q[:, :, :D], o[:, :, :D], c.cu, c.kv, table, 1000, 600, c.scale, lse=lse, workspace=c.ws,
+                       err_flag=c.err)
+    B.moe_attn_paged(c.cache, args)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0 and torch.all(o[T:] == 77.0) and torch.all(o[:, :, D:] == 77.0)
+    assert torch.all(lse[T:] == 77.0)
+    c.od[:, :], c.lse[:, :] = o[:T, :, :D], lse[:T]
+    c.run, go = (lambda **kw: go), (c.od.double().cpu().numpy(), c.lse.double().cpu().numpy())
+    c.check()
+
+
 KV_EDGES = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 1000]
 
 
@@ -129,7 +154,7 @@ def test_decode(dtype, D, Hq, H):
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-@pytest.mark.parametrize("order", ["hnd", "nhd"])
+@pytest.mark.parametrize("order", ["hnd", "nhd", "head first"])
 def test_pages_and_orders(page, dtype, order):
     Case([1, 3, 1, 2], [5, 300, 513, 700], page=page, dtype=dtype, order=order, q_pad=3).check()
 
