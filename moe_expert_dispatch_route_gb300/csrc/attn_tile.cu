@@ -4,11 +4,17 @@
 // A query tile is two halves of up to 128 rows over the same key tiles; while the softmax of
 // one half runs, the tensor cores work on the other.  Per half and 128-key tile:
 //   S = Q K^T    A = Q (shared memory), B = K tile (d contiguous), 128 columns of fp32
-//   P = 2^(s - m) in bf16, written over S's first 64 columns: the A operand of
+//   P = 2^(s - m) in 16 bits, written over S's first 64 columns: the A operand of
 //   O += P V     A = P (tensor memory), B = V tile with the columns contiguous
 // which fills the 512 columns of tensor memory: S0 | S1 | O0 | O1.  The MMA thread issues
 // PV(j), S(j+1) for each half in turn; tcgen05.mma instructions of one thread execute in
 // order, so S(j+1) may overwrite P(j) without a wait.
+//
+// What bounds it: a pair of tiles (both halves, 128 keys, head_dim 128) is 32 MMAs of 64.7 cycles,
+// 2070, during which they read 192 KB of operands and the copies write 64 KB at 128 bytes a
+// cycle, 2048: shared memory is as busy as the tensor cores, and what is left shows as 3450
+// cycles a pair.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1120 us, 1470 TFLOP/s
+// (64 columns: 1010 us, bound by the softmax, which is the same for half the products).
 //
 // The running maximum is followed loosely: o and the sum stay relative to an older maximum
 // until a row's new one is 2^8 times as large (in the probabilities), and only then are they
@@ -16,20 +22,21 @@
 // with the same relative precision, and bf16 probabilities up to 256 round like those up to 1.
 // So the rescaling, a round trip of o through registers, happens a few times a row.
 //
-//   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row)
-//   warps 8-11       e4m3 only: turn raw K and V tiles into fp16 tiles, and the rows of Q
-//   last four warps  one issues the MMAs, one the copies
-#include <cudaTypedefs.h>
-
-#include "attn.cuh"
-
-//
 // An e4m3 cache is multiplied in fp16: a conversion instruction and a product turn two codes
 // into two elements (bf16 takes ten for four: shifts, masks and products).  What is multiplied is
 //   q   a row times a power of two that brings its largest element into [2^14, 2^15)
 //   k   code * 2^(s - r), s the key's scale exponent, r the largest in the tile; v likewise
 //   p   2^7 p 2^(r - R) for a V tile with reference r, R the largest so far, to which o refers
 // Each is exact but for what lies under 2^-31 of the largest number of its kind (2^-33 for k, v).
+// The same chunk takes 1540 us: the conversion shares shared memory and issue slots with the rest
+// (without it, which is of course no result, the pipeline takes 1250).
+//
+//   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row; e4m3: its row of Q too)
+//   warps 8-11       e4m3 only: turn raw K and V tiles into fp16 tiles
+//   last four warps  one issues the MMAs, one the copies
+#include <cudaTypedefs.h>
+
+#include "attn.cuh"
 
 namespace moe {
 namespace attn {
@@ -41,7 +48,7 @@ constexpr int kRefs = 8;  // tiles whose references are kept: more than the pipe
 template <int kD, bool kFp8>
 struct Cfg {
     static constexpr int kThreads = kFp8 ? 512 : 384;
-    static constexpr int kCols = kD / 64;                             // 128-byte column blocks of a bf16 tile
+    static constexpr int kCols = kD / 64;                             // 128-byte column blocks of a 16-bit tile
     static constexpr int kBlockBytes = kKeyTile * 128;                // one of them
     static constexpr int kQBytes = 2 * kCols * kHalfRows * 128;       // both halves of Q
     static constexpr int kEntryBytes = kCols * kBlockBytes;           // a K or V tile of 16-bit elements
@@ -78,7 +85,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem], A's row i in lane i, two bf16 of K per column.
+// D[tmem] (+)= A[tmem] * B[smem], A's row i in lane i, two 16-bit elements of K per column.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
     asm volatile(
@@ -708,10 +715,10 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     tc::tmem_wait_ld();
                     if (edge) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int key = key0 + i * 32 + j;
-                                if (key < lo || key >= hi) s[j] = 0xff800000u;
-                            }
+                        for (int j = 0; j < 32; ++j) {
+                            const int key = key0 + i * 32 + j;
+                            if (key < lo || key >= hi) s[j] = 0xff800000u;
+                        }
                     }
                 };
                 float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
