@@ -29,7 +29,7 @@
 //
 // Measured: 128 requests of up to 16384 bf16 tokens, 32 / 4 heads of 128, 288 us (6.8 TB/s); 96 of up
 // to 20001 e4m3 tokens, 64 / 8 heads, 311 us (6.5 TB/s); drafts of 30 rows over a 4096 window, 8 heads
-// of 64, 54 us (4.1 TB/s: start, joins and the consumers' latency); one request of 777 tokens 7.7 us,
+// of 64, 51 us (4.3 TB/s: start, joins and the consumers' latency); one request of 777 tokens 7.7 us,
 // a chain of dependent loads and barriers.
 #include "attn.cuh"
 
@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
     using Info = TileInfo<C::kRows>;
     constexpr int kSteps = kD / 16;  // k-steps of the first product, column tiles of the second
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // aligned by an offset, so that accesses stay in the shared window with 32-bit addresses
+    uint8_t* ring = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);
     float* xchg = reinterpret_cast<float*>(ring + C::kRing);  // o of kSlots key groups
     uint8_t* infos = reinterpret_cast<uint8_t*>(xchg) + C::kSlots * C::kGroupBytes;
     uint8_t* scales = infos + C::kInfos * C::kInfoBytes;

@@ -13,7 +13,7 @@
 // What bounds it: a pair of tiles (both halves, 128 keys, head_dim 128) is 32 MMAs of 64.7 cycles,
 // 2070, during which they read 192 KB of operands and the copies write 64 KB at 128 bytes a
 // cycle, 2048: shared memory is as busy as the tensor cores, and what is left shows as 3450
-// cycles a pair.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1120 us, 1470 TFLOP/s
+// cycles a pair.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1123 us, 1470 TFLOP/s
 // (64 columns: 1010 us, bound by the softmax, which is the same for half the products).
 //
 // The running maximum is followed loosely: o and the sum stay relative to an older maximum
@@ -28,7 +28,7 @@
 //   k   code * 2^(s - r), s the key's scale exponent, r the largest in the tile; v likewise
 //   p   2^7 p 2^(r - R) for a V tile with reference r, R the largest so far, to which o refers
 // Each is exact but for what lies under 2^-31 of the largest number of its kind (2^-33 for k, v).
-// The same chunk takes 1540 us: the conversion shares shared memory and issue slots with the rest
+// The same chunk takes 1430 us: the conversion shares shared memory and issue slots with the rest
 // (without it, which is of course no result, the pipeline takes 1250).
 //
 //   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row; e4m3: its row of Q too)
@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                      const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale) {
     using C = Cfg<kD, kFp8>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // aligned by an offset: rounding the address itself would make every access a generic one, with
+    // 64-bit addresses (e4m3 1560 us instead of 1445, bf16 1145 instead of 1123)
+    uint8_t* qs = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);
     uint8_t* ring = qs + C::kQBytes;                          // bf16 tiles, as the MMAs read them
     uint8_t* raw = ring + C::kEntries * C::kEntryBytes;       // e4m3 tiles
     uint8_t* scales = raw + C::kRaw * C::kRawBytes;
@@ -573,25 +575,30 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 return *reinterpret_cast<const uint4*>(src + (kD == 128 ? r * 128 + (((hf * 4 + c4) ^ (r & 7)) << 4)
                                                                         : r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)));
             };
+            // lane i: the factor of key 32 * (warp - 8) + i: 2^ex in fp16, subnormal below 2^-14
+            uint32_t factor;
+            {
+                const int key = (warp - 8) * 32 + lane, b = sc[key], ex = b - (int)top;
+                factor = (b == 255    ? 0x7e00u
+                          : ex >= -14 ? (uint32_t)(ex + 15) << 10
+                          : ex >= -24 ? 1u << (ex + 24)
+                                      : 0u) *
+                         0x10001u;
+                if (key < z0 || key >= z1) factor = 0;
+            }
+            const bool edge = z0 > 0 || z1 < kKeyTile;
             const int first = (warp - 8) * 32 + row8;
-            uint4 w[C::kCols];  // read a step ahead
-            int b = sc[first];
-#pragma unroll
-            for (int hf = 0; hf < C::kCols; ++hf) w[hf] = chunk_at(first, hf);
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
-                const int r = first + g * 8, r2 = first + (g < 3 ? g + 1 : 3) * 8;
-                const bool seen = r >= z0 && r < z1;
-                const int ex = b - (int)top;  // 2^ex in fp16, subnormal below 2^-14
-                const uint32_t f = (b == 255    ? 0x7e00u
-                                    : ex >= -14 ? (uint32_t)(ex + 15) << 10
-                                    : ex >= -24 ? 1u << (ex + 24)
-                                                : 0u) *
-                                   0x10001u;
-                const int b2 = sc[r2];
-                uint4 w2[C::kCols];
+                const int r = first + g * 8;
+                uint4 w[C::kCols];
 #pragma unroll
-                for (int hf = 0; hf < C::kCols; ++hf) w2[hf] = chunk_at(r2, hf);
+                for (int hf = 0; hf < C::kCols; ++hf) w[hf] = chunk_at(r, hf);
+                const uint32_t f = __shfl_sync(0xffffffffu, factor, g * 8 + row8);
+                if (edge && (r < z0 || r >= z1)) {
+#pragma unroll
+                    for (int hf = 0; hf < C::kCols; ++hf) w[hf] = make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
                 for (int hf = 0; hf < C::kCols; ++hf) {
                     const uint32_t x[4] = {w[hf].x, w[hf].y, w[hf].z, w[hf].w};
@@ -602,17 +609,11 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                         o[2 * j] = mul_f16x2(o[2 * j], f);
                         o[2 * j + 1] = mul_f16x2(o[2 * j + 1], f);
                     }
-                    if (!seen) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = 0;
-                    }
                     uint8_t* to = dst + hf * C::kBlockBytes + r * 128;
                     *reinterpret_cast<uint4*>(to + (((2 * c4) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4*>(to + (((2 * c4 + 1) ^ (r & 7)) << 4)) =
                         make_uint4(o[4], o[5], o[6], o[7]);
-                    w[hf] = w2[hf];
                 }
-                b = b2;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
