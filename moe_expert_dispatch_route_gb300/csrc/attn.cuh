@@ -19,8 +19,10 @@
 //
 // Joining.  A query tile whose units span CTAs c0 < .. < c1 is finished by the last of them
 // to arrive: each stores its part (unnormalised o, running maximum, sum) in its own slot of
-// the workspace, then counts itself in counter c0; the last sums the parts in CTA order, so
-// the result does not depend on who came last.  It also clears the counter for the next call.
+// the workspace, then counts itself in one of the tile's counters; the last sums the parts in CTA
+// order, so the result does not depend on who came last.  It also clears the counter for the
+// next call.  (Large parts are summed a few at a time in the same way.)  A counter is that of a
+// CTA that continues the tile; a CTA continues no other.
 #pragma once
 
 #include <math_constants.h>
@@ -473,22 +475,22 @@ __device__ __forceinline__ RowAt row_at(const Params& p, const Item& it, int r) 
 struct Parts {
     int first, last;
 };
-// Threads with ids 0 .. n-1 and their barrier `sync`: counts this CTA's stored part; true in all of
-// them if it was the tile's last (`flag`: a shared int).
+__device__ __forceinline__ Parts parts_of(const Params& p, const Item& it, const Start& st) {
+    return {cta_of(st, it.tile_unit + p.item_cost), cta_of(st, it.tile_unit + it.cost - p.item_slack - 1)};
+}
+// Threads with ids 0 .. n-1 and their barrier `sync`: counts this CTA, whose part is stored; true in
+// all of them if it was the last of `of` (`flag`: a shared int).
 template <typename Sync>
-__device__ bool join_last(const Params& p, const Item& it, const Start& st, int tid, int* flag, Sync sync,
-                          Parts& parts) {
-    parts.first = cta_of(st, it.tile_unit + p.item_cost);
-    parts.last = cta_of(st, it.tile_unit + it.cost - p.item_slack - 1);
+__device__ bool last_of(uint32_t* counter, int of, int tid, int* flag, Sync sync) {
     sync();  // the CTA's stores come before thread 0's count, which releases them
     if (tid == 0) {
         uint32_t seen;  // and acquires those of the CTAs that counted before
         asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
                      : "=r"(seen)
-                     : "l"(static_cast<uint64_t>(__cvta_generic_to_global(&p.counters[parts.first])))
+                     : "l"(static_cast<uint64_t>(__cvta_generic_to_global(counter)))
                      : "memory");
-        *flag = seen == (uint32_t)(parts.last - parts.first);
-        if (*flag) p.counters[parts.first] = 0;
+        *flag = seen == (uint32_t)(of - 1);
+        if (*flag) *counter = 0;
     }
     sync();
     return *flag;

@@ -768,8 +768,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             }
         }
         if (!it.whole) {
-            Parts parts;
-            if (join_last(p, it, start, threadIdx.x, &last_s, sync, parts)) join_rows<kD, C::kConsumers>(p, it, parts, rows);
+            const Parts parts = parts_of(p, it, start);
+            if (last_of(p.counters + parts.last, parts.last - parts.first + 1, threadIdx.x, &last_s, sync))
+                join_rows<kD, C::kConsumers>(p, it, parts, rows);
         }
         sync();
         if (threadIdx.x == 0) tc::mbar_arrive(&info_empty[buf]);

@@ -10,11 +10,12 @@
 // PV(j), S(j+1) for each half in turn; tcgen05.mma instructions of one thread execute in
 // order, so S(j+1) may overwrite P(j) without a wait.
 //
-// What bounds it: a pair of tiles (both halves, 128 keys, head_dim 128) is 32 MMAs of 64.7 cycles,
-// 2070, during which they read 192 KB of operands and the copies write 64 KB at 128 bytes a
-// cycle, 2048: shared memory is as busy as the tensor cores, and what is left shows as 3450
-// cycles a pair.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1123 us, 1470 TFLOP/s
-// (64 columns: 1010 us, bound by the softmax, which is the same for half the products).
+// What bounds it: the chain of one half's scores, softmax and product, which two halves in turn cover
+// in part; a pair of tiles (both halves, 128 keys, head_dim 128) takes 3400 cycles.  Its 32 MMAs
+// last 2070 (64.7 each), during which they read 192 KB of operands and the copies write 64 KB at
+// 128 bytes a cycle, 2048: shared memory is as busy as the tensor cores, which stretches them to
+// 2450.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1120 us, 1470 TFLOP/s (64 columns:
+// 1010 us, bound by the softmax, which is the same for half the products).
 //
 // The running maximum is followed loosely: o and the sum stay relative to an older maximum
 // until a row's new one is 2^8 times as large (in the probabilities), and only then are they
@@ -183,25 +184,28 @@ enum : uint32_t {
     kSeenHi = 16
 };
 
-// One thread: row r of a split tile from its parts, in CTA order.
-template <int kD>
-__device__ void join_row(const Params& p, const Parts& parts, const RowAt& at, int r) {
+// One thread: the sum of row r of n parts of a split tile, those of CTAs first, first + step, ..., in
+// this order.  kLast: it goes to the output, otherwise to the place of the first part.
+template <int kD, bool kLast>
+__device__ void join_row(const Params& p, const Parts& parts, int first, int step, int n, const RowAt& at, int r) {
+    const int end = first + n * step;
     float m = -CUDART_INF_F, l = 0.0f;
-    for (int c = parts.first; c <= parts.last; ++c) m = fmaxf(m, __ldcg(part_ml(p, c, part_slot(parts, c)) + r).x);
+    for (int c = first; c < end; c += step) m = fmaxf(m, __ldcg(part_ml(p, c, part_slot(parts, c)) + r).x);
     const float to = m == -CUDART_INF_F ? 0.0f : m;
-    for (int c = parts.first; c <= parts.last; ++c) {
+    for (int c = first; c < end; c += step) {
         const float2 ml = __ldcg(part_ml(p, c, part_slot(parts, c)) + r);
         l += ml.y * exp2_fast(ml.x - to);
     }
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
     uint16_t* out = p.o + at.token * p.o_ld + at.head * p.o_head;
+    float4* sum = reinterpret_cast<float4*>(part_o(p, first, part_slot(parts, first))) + r;
     constexpr int kBatch = 8;  // loads under way together, four columns each
 #pragma unroll
     for (int b = 0; b < kD / 4; b += kBatch) {
         float4 o[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = parts.first; c <= parts.last; ++c) {
+        for (int c = first; c < end; c += step) {
             const int slot = part_slot(parts, c);
             const float4* from = reinterpret_cast<const float4*>(part_o(p, c, slot)) + r;
             float4 x[kBatch];
@@ -214,15 +218,50 @@ __device__ void join_row(const Params& p, const Parts& parts, const RowAt& at, i
                 o[j].z += x[j].z * f, o[j].w += x[j].w * f;
             }
         }
+        if (kLast) {
 #pragma unroll
-        for (int j = 0; j < kBatch; j += 2)
-            *reinterpret_cast<uint4*>(out + (b + j) * 4) =
-                make_uint4(cvt_bf16x2(o[j].x * inv, o[j].y * inv), cvt_bf16x2(o[j].z * inv, o[j].w * inv),
-                           cvt_bf16x2(o[j + 1].x * inv, o[j + 1].y * inv), cvt_bf16x2(o[j + 1].z * inv, o[j + 1].w * inv));
+            for (int j = 0; j < kBatch; j += 2)
+                *reinterpret_cast<uint4*>(out + (b + j) * 4) = make_uint4(
+                    cvt_bf16x2(o[j].x * inv, o[j].y * inv), cvt_bf16x2(o[j].z * inv, o[j].w * inv),
+                    cvt_bf16x2(o[j + 1].x * inv, o[j + 1].y * inv), cvt_bf16x2(o[j + 1].z * inv, o[j + 1].w * inv));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) sum[(b + j) * kMaxRows] = o[j];
+        }
     }
-    if (p.lse)
+    if (!kLast)
+        part_ml(p, first, part_slot(parts, first))[r] = make_float2(m, l);
+    else if (p.lse)
         p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
             l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// The softmax threads of a CTA whose part of a split tile is stored; r and `at` are the thread's row,
+// if valid.  A part is up to 128 KB, which a CTA takes two microseconds to add, so parts are
+// summed kFan at a time, each group by the last of its CTAs to arrive, and the sums again: one
+// request's 256 rows a head over 16384 tokens, 38 parts a tile: 51 us, 95 with one CTA adding them
+// all; groups of 6 or 8: 57.  The counter is that of a group's second member, which is the second
+// of no other group.
+template <int kD, typename Sync>
+__device__ void join(const Params& p, const Item& it, const Start& st, const RowAt& at, int r, bool valid, int* flag,
+                     Sync sync) {
+    constexpr int kFan = 4;
+    const Parts parts = parts_of(p, it, st);
+    const int n = parts.last - parts.first + 1;
+    int step = 1;
+    if (n > kFan) {
+        const int me = (int)blockIdx.x - parts.first;
+        for (; step * kFan < n; step *= kFan) {
+            const int head = me / (step * kFan) * (step * kFan), members = min(kFan, (n - head + step - 1) / step);
+            if (members == 1) continue;
+            const int first = parts.first + head;
+            if (!last_of(p.counters + first + step, members, threadIdx.x, flag, sync)) return;
+            if (valid) join_row<kD, false>(p, parts, first, step, members, at, r);
+        }
+    }
+    const int members = (n + step - 1) / step;
+    if (last_of(p.counters + parts.first + step, members, threadIdx.x, flag, sync) && valid)
+        join_row<kD, true>(p, parts, parts.first, step, members, at, r);
 }
 
 template <int kD, bool kFp8>
@@ -845,8 +884,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     }
                 }
                 if (valid) part_ml(p, blockIdx.x, slot)[r] = make_float2(m, l);
-                Parts parts;
-                if (join_last(p, it, start, threadIdx.x, &last_s, sync, parts) && valid) join_row<kD>(p, parts, at, r);
+                join<kD>(p, it, start, at, r, valid, &last_s, sync);
                 sync();  // the flag may be written again
             }
             tc::tc_fence_before();  // o has been read: the next item's first arrival on p_full says so

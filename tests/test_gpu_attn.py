@@ -221,6 +221,14 @@ def test_one_long_context(dtype, n):
     Case([n], [20000], Hq=2, H=1, dtype=dtype, page=64).check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_ctas", [9, 37, 1000])
+def test_tiles_of_many_parts(dtype, D, max_ctas):
+    """Few query tiles over many CTAs, whose parts are summed in groups of groups."""
+    Case([130, 40], [6000, 2500], Hq=8, H=2, D=D, dtype=dtype, page=64).check(max_ctas=max_ctas)
+
+
 def test_many_requests():
     rng = np.random.default_rng(3)
     n = 700
