@@ -15,7 +15,7 @@
 // last 2070 (64.7 each), during which they read 192 KB of operands and the copies write 64 KB at
 // 128 bytes a cycle, 2048: shared memory is as busy as the tensor cores, which stretches them to
 // 2450.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1120 us, 1470 TFLOP/s (64 columns:
-// 1010 us, bound by the softmax, which is the same for half the products).
+// 977 us, bound by the softmax, which is the same for half the products).
 //
 // The running maximum is followed loosely: o and the sum stay relative to an older maximum
 // until a row's new one is 2^8 times as large (in the probabilities), and only then are they
@@ -29,8 +29,8 @@
 //   k   code * 2^(s - r), s the key's scale exponent, r the largest in the tile; v likewise
 //   p   2^7 p 2^(r - R) for a V tile with reference r, R the largest so far, to which o refers
 // Each is exact but for what lies under 2^-31 of the largest number of its kind (2^-33 for k, v).
-// The same chunk takes 1430 us: the conversion shares shared memory and issue slots with the rest
-// (without it, which is of course no result, the pipeline takes 1250).
+// The same chunk takes 1412 us: the conversion shares shared memory and issue slots with the rest
+// (left out, when this took 1540, it left 1250).
 //
 //   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row; e4m3: its row of Q too)
 //   warps 8-11       e4m3 only: turn raw K and V tiles into fp16 tiles
@@ -54,8 +54,8 @@ struct Cfg {
     static constexpr int kQBytes = 2 * kCols * kHalfRows * 128;       // both halves of Q
     static constexpr int kEntryBytes = kCols * kBlockBytes;           // a K or V tile of 16-bit elements
     static constexpr int kRawBytes = kKeyTile * kD;                   // an e4m3 one
-    static constexpr int kEntries = kFp8 ? (kD == 64 ? 6 : 3) : kD == 64 ? 8 : 5;
-    static constexpr int kRaw = kFp8 ? (kD == 64 ? 6 : 4) : 0;
+    static constexpr int kEntries = kFp8 ? (kD == 64 ? 6 : 4) : kD == 64 ? 8 : 5;
+    static constexpr int kRaw = kFp8 ? (kD == 64 ? 6 : 2) : 0;
     static constexpr int kFp8Bytes = kFp8 ? kRaw * (kRawBytes + kKeyTile) + 2 * kRefs : 0;
     static constexpr int kSmem = 1024 + kQBytes + kEntries * kEntryBytes + kFp8Bytes + 512;
     static_assert(kSmem <= 232448 - 256, "");
