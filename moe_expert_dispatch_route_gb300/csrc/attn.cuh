@@ -10,8 +10,8 @@
 // no key at all counts as one.  What a query tile takes beside its key tiles (its rows, its
 // output, the pipeline's turn) stands in front of them as item_cost units more.  Units are
 // numbered request by request, head by head, query tile by query tile, key tile by key tile,
-// and each of the N = min(grid, U) CTAs takes a run of U/N of them, rounded up for the first
-// U mod N: ragged lengths cost no balance, and few rows over a long context are split over
+// and each of N CTAs, the grid or U / cta_units if that is less, takes a run of U/N of them, rounded
+// up for the first U mod N: ragged lengths cost no balance, and few rows over a long context are split over
 // the whole GPU by the same rule that gives a CTA many short requests.  A boundary that falls
 // into a tile's item_cost, or leaves fewer than item_slack of its units, moves to the tile's
 // edge: no part of a tile is without keys, and none costs more than it spares.  Every CTA
@@ -79,7 +79,7 @@ struct Params {
     int num_pages, page_shift, page_size;
     float scale_log2;         // scale * log2(e): scores in powers of two
     int causal, window;
-    int item_cost, item_slack;  // in units
+    int item_cost, item_slack, cta_units;  // in units
     int32_t* err;
     uint32_t* counters;       // [kMaxCtas], all zero between calls
     uint8_t* parts;           // [grid][2] parts: slot 0 the tile begun last, slot 1 the tile continued
@@ -164,6 +164,11 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
     return v;
 }
 
+// CTAs that get units, at least one each: no CTA has too few to be worth a part.
+__device__ __forceinline__ uint32_t ctas_for(const Params& p, uint32_t total) {
+    return total == 0 ? 0 : min((uint32_t)gridDim.x, max(total / (uint32_t)p.cta_units, 1u));
+}
+
 // Whole CTA (kThreads threads): the CTA's range of units and the query tile it begins in.
 // scratch: shared, p.B + 32 uint32, free again for copies after it.  Ends with a barrier;
 // st->unit == st->end: nothing to do.
@@ -183,7 +188,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
             }
             const uint32_t k = one * (uint32_t)p.heads, upto = warp_incl(k), at = upto - k;
             const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
-            const uint32_t n = min((uint32_t)gridDim.x, total), me = blockIdx.x;
+            const uint32_t n = ctas_for(p, total), me = blockIdx.x;
             const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
             int moved[2];
             bool next = false;
@@ -257,7 +262,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     const uint32_t total = all * (uint32_t)p.heads;  // host: below 2^31
     // no CTA's range is empty (before boundaries move) but those of surplus CTAs: the CTAs of a
     // split tile are consecutive
-    const uint32_t n = min((uint32_t)gridDim.x, total), me = blockIdx.x;
+    const uint32_t n = ctas_for(p, total), me = blockIdx.x;
     const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
     const uint32_t u[2] = {me < n ? me * each + min(me, rest) : total,
                            me + 1 < n ? (me + 1) * each + min(me + 1, rest) : total};

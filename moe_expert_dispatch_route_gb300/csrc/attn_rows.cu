@@ -784,6 +784,7 @@ cudaError_t launch_as(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream
     // what a query tile costs beside its key tiles is about 3 us, a K and V tile 1.5 us per 64 KB
     p.item_cost = 2 * 32768 / C::kTileBytes;
     p.item_slack = 1;
+    p.cta_units = 1;
     CUtensorMap km, vm;
     if (!make_pool_map(&km, c, c.k) || !make_pool_map(&vm, c, c.v)) return cudaErrorInvalidValue;
     auto kern = attn_rows_kernel<kD, kFp8, kNT, kRW>;

@@ -186,38 +186,57 @@ enum : uint32_t {
 
 // One thread: the sum of row r of n parts of a split tile, those of CTAs first, first + step, ..., in
 // this order.  kLast: it goes to the output, otherwise to the place of the first part.
+constexpr int kFan = 4;  // the most parts summed together
 template <int kD, bool kLast>
 __device__ void join_row(const Params& p, const Parts& parts, int first, int step, int n, const RowAt& at, int r) {
-    const int end = first + n * step;
+    auto ml_of = [&](int i) {
+        const int c = first + i * step;
+        return __ldcg(part_ml(p, c, part_slot(parts, c)) + r);
+    };
+    float2 ml[kFan];
     float m = -CUDART_INF_F, l = 0.0f;
-    for (int c = first; c < end; c += step) m = fmaxf(m, __ldcg(part_ml(p, c, part_slot(parts, c)) + r).x);
+#pragma unroll
+    for (int i = 0; i < kFan; ++i) ml[i] = i < n ? ml_of(i) : make_float2(-CUDART_INF_F, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kFan; ++i) m = fmaxf(m, ml[i].x);
     const float to = m == -CUDART_INF_F ? 0.0f : m;
-    for (int c = first; c < end; c += step) {
-        const float2 ml = __ldcg(part_ml(p, c, part_slot(parts, c)) + r);
-        l += ml.y * exp2_fast(ml.x - to);
-    }
+#pragma unroll
+    for (int i = 0; i < kFan; ++i) l += ml[i].y * exp2_fast(ml[i].x - to);
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
     uint16_t* out = p.o + at.token * p.o_ld + at.head * p.o_head;
     float4* sum = reinterpret_cast<float4*>(part_o(p, first, part_slot(parts, first))) + r;
+    // batches of columns one after another, each over all parts, in one rolled loop: this code is cold in
+    // the instruction caches; the next loads go out before a batch is stored
     constexpr int kBatch = 8;  // loads under way together, four columns each
+    float4 x[kBatch], o[kBatch];
+    float f;
+    int load_b = 0, load_i = 0;
+    auto load = [&] {
+        if (load_b >= kD / 4) return;
+        const int c = first + load_i * step;
+        const float4* from = reinterpret_cast<const float4*>(part_o(p, c, part_slot(parts, c))) + r;
 #pragma unroll
-    for (int b = 0; b < kD / 4; b += kBatch) {
-        float4 o[kBatch];
+        for (int j = 0; j < kBatch; ++j) x[j] = __ldcg(from + (load_b + j) * kMaxRows);
+        f = ml_of(load_i).x;
+        if (++load_i == n) load_i = 0, load_b += kBatch;
+    };
+    auto clear = [&] {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = first; c < end; c += step) {
-            const int slot = part_slot(parts, c);
-            const float4* from = reinterpret_cast<const float4*>(part_o(p, c, slot)) + r;
-            float4 x[kBatch];
+    };
+    clear();
+    load();
+    int i = 0;
+#pragma unroll 1
+    for (int b = 0; b < kD / 4;) {
+        const float w = exp2_fast(f - to);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) x[j] = __ldcg(from + (b + j) * kMaxRows);
-            const float f = exp2_fast(__ldcg(part_ml(p, c, slot) + r).x - to);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                o[j].x += x[j].x * f, o[j].y += x[j].y * f;
-                o[j].z += x[j].z * f, o[j].w += x[j].w * f;
-            }
+        for (int j = 0; j < kBatch; ++j) {
+            o[j].x += x[j].x * w, o[j].y += x[j].y * w;
+            o[j].z += x[j].z * w, o[j].w += x[j].w * w;
         }
+        load();
+        if (++i < n) continue;
         if (kLast) {
 #pragma unroll
             for (int j = 0; j < kBatch; j += 2)
@@ -228,6 +247,9 @@ __device__ void join_row(const Params& p, const Parts& parts, int first, int ste
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) sum[(b + j) * kMaxRows] = o[j];
         }
+        clear();
+        i = 0;
+        b += kBatch;
     }
     if (!kLast)
         part_ml(p, first, part_slot(parts, first))[r] = make_float2(m, l);
@@ -239,13 +261,12 @@ __device__ void join_row(const Params& p, const Parts& parts, int first, int ste
 // The softmax threads of a CTA whose part of a split tile is stored; r and `at` are the thread's row,
 // if valid.  A part is up to 128 KB, which a CTA takes two microseconds to add, so parts are
 // summed kFan at a time, each group by the last of its CTAs to arrive, and the sums again: one
-// request's 256 rows a head over 16384 tokens, 38 parts a tile: 51 us, 95 with one CTA adding them
-// all; groups of 6 or 8: 57.  The counter is that of a group's second member, which is the second
-// of no other group.
+// request's 256 rows a head over 16384 tokens, 38 parts a tile: 42 us, 95 with one CTA adding them
+// all; groups of 6 or 8 take 6 us more than groups of 4.  The counter is that of a group's second
+// member, which is the second of no other group.
 template <int kD, typename Sync>
 __device__ void join(const Params& p, const Item& it, const Start& st, const RowAt& at, int r, bool valid, int* flag,
                      Sync sync) {
-    constexpr int kFan = 4;
     const Parts parts = parts_of(p, it, st);
     const int n = parts.last - parts.first + 1;
     int step = 1;
@@ -931,6 +952,9 @@ cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStr
     // what a query tile costs beside its key tiles (1.7 us each) is about 7 us
     p.item_cost = 4;
     p.item_slack = 1;
+    // a part costs its CTA and the joining one 2 us each and a join 2 more: with runs of at least 4 units
+    // 128 rows over 500 tokens take 18 us, 24 with runs of 1, 22 of 6 (for the larger calls the same)
+    p.cta_units = 4;
     const int grid = grid_for(p, grid_cap);
     const bool fp8 = c.dtype == MOE_FP8_E4M3;
     if (c.head_dim == 128)
