@@ -29,7 +29,7 @@
 //
 // Measured: 128 requests of up to 16384 bf16 tokens, 32 / 4 heads of 128, 288 us (6.8 TB/s); 96 of up
 // to 20001 e4m3 tokens, 64 / 8 heads, 311 us (6.5 TB/s); drafts of 30 rows over a 4096 window, 8 heads
-// of 64, 51 us (4.3 TB/s: start, joins and the consumers' latency); one request of 777 tokens 7.7 us,
+// of 64, 51 us (4.3 TB/s: start, joins and the consumers' latency); one request of 777 tokens 7.8 us,
 // a chain of dependent loads and barriers.
 #include "attn.cuh"
 
@@ -784,7 +784,9 @@ cudaError_t launch_as(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream
     // what a query tile costs beside its key tiles is about 3 us, a K and V tile 1.5 us per 64 KB
     p.item_cost = 2 * 32768 / C::kTileBytes;
     p.item_slack = 1;
-    p.cta_units = 1;
+    // runs of at least 2 units: one request of 4000 tokens 8.8 us, with runs of 1 9.9 and of 3 9.0 (32 rows
+    // over 2000: 15.2, 17.8 and 15.9; 777 tokens 7.8, 7.5 and 7.8)
+    p.cta_units = 2;
     CUtensorMap km, vm;
     if (!make_pool_map(&km, c, c.k) || !make_pool_map(&vm, c, c.v)) return cudaErrorInvalidValue;
     auto kern = attn_rows_kernel<kD, kFp8, kNT, kRW>;
