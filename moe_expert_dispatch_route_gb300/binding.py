@@ -412,7 +412,7 @@ def attn_args(q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal=True
               workspace=None, err_flag=None) -> MoeAttnArgs:
     """MoeAttnArgs from tensors: q, o bf16 [T][heads][head_dim] (any token and head strides), lse
     fp32 [T][heads]; workspace: moe_attn_workspace_size bytes, zeroed once before its first use."""
-    T, H, _ = q.shape
+    T, H, D = q.shape
     B = kv_len.shape[0]
     _same("attn_args: o", (o.shape, q.shape), (o.dtype, torch.bfloat16), (q.dtype, torch.bfloat16))
     if q.stride(2) != 1 or o.stride(2) != 1:
@@ -423,12 +423,16 @@ def attn_args(q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal=True
     if lse is not None:
         _same("attn_args: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
     size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    return MoeAttnArgs(_ptr(q), _ptr(o), _ptr(lse), q.stride(0), q.stride(1), o.stride(0), o.stride(1), _ptr(cu_q),
+    args = MoeAttnArgs(_ptr(q), _ptr(o), _ptr(lse), q.stride(0), q.stride(1), o.stride(0), o.stride(1), _ptr(cu_q),
                        _ptr(kv_len), _ptr(block_table), block_table.shape[1], T, B, max_q, max_kv, H, float(scale),
                        int(causal), window, _ptr(err_flag), _ptr(workspace), size)
+    args.head_dim = D  # the C structure has no field for it: the cache's is meant
+    return args
 
 
 def moe_attn_paged(cache: MoeKvCache, args: MoeAttnArgs, max_ctas=0, stream=None):
+    if getattr(args, "head_dim", cache.head_dim) != cache.head_dim:  # a structure filled by hand has none
+        raise ValueError(f"moe_attn_paged: q and o have heads of {args.head_dim}, the cache of {cache.head_dim}")
     _check(lib().moe_attn_paged(ctypes.byref(cache), ctypes.byref(args), max_ctas, _stream(stream)),
            "moe_attn_paged")
 

@@ -176,6 +176,19 @@ def test_the_binding_checks_tensors():
             B.moe_draft_verify(*args)
 
 
+@pytest.mark.parametrize("D,other", [(64, 128), (128, 64)])
+def test_the_binding_checks_the_width_of_q_and_o(D, other):
+    """Heads of another width than the cache's are refused before the C call, which sees pointers and
+    strides only: too narrow ones would be read and written past their end."""
+    z, bf, i32 = torch.zeros, torch.bfloat16, torch.int32
+    k = z(3, 2, 16, D, dtype=bf)
+    c = B.kv_cache(k, k)
+    tab, kv, cu = z(1, 4, dtype=i32), z(1, dtype=i32), z(2, dtype=i32)
+    q = z(5, 4, other, dtype=bf)
+    with pytest.raises(ValueError):
+        B.moe_attn_paged(c, B.attn_args(q, q.clone(), cu, kv, tab, 5, 64, 0.1), stream=0)
+
+
 # ---------------------------------------------------------------- the plain implementations
 def test_reference_quantisation():
     t = e4m3_table()
