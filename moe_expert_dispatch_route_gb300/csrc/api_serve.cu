@@ -44,6 +44,19 @@ moe_status check_cache(const moe_kv_cache* c) {
     return MOE_OK;
 }
 
+// Whether rows of `width` elements at t * ld + h * hs, t < T, h < H, lie apart from each other.
+bool rows_apart(int64_t T, int64_t H, int64_t ld, int64_t hs, int64_t width) {
+    if ((T > 1 && ld < width) || (H > 1 && hs < width)) return false;
+    if (T == 1 || H == 1) return true;
+    if (ld - width >= (H - 1) * hs || hs - width >= (T - 1) * ld) return true;  // one inside the other
+    // the tokens nearest to each head, before it and after it
+    for (int64_t h = 1; h < H; ++h) {
+        const int64_t t = h * hs / ld, past = h * hs - t * ld;
+        if ((t < T && past < width) || (t + 1 < T && ld - past < width)) return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -96,6 +109,14 @@ moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, int
     if (!aligned16(a->q) || !aligned16(a->o) || a->q_ld % 8 || a->q_head_stride % 8 || a->o_ld % 8 ||
         a->o_head_stride % 8)
         return MOE_ERR_ALIGNMENT;
+    // no stride that is used reaches past a tensor map's (below 2^40 bytes) or what 64 bits count
+    const int64_t T = a->T, H = a->num_q_heads, most = INT64_MAX / 2 / (T > H ? T : H), far = (int64_t)1 << 39;
+    const int64_t limit = most < far ? most : far;
+    if ((T > 1 && (a->q_ld >= limit || a->o_ld >= limit)) ||
+        (H > 1 && (a->q_head_stride >= limit || a->o_head_stride >= limit)))
+        return MOE_ERR_UNSUPPORTED;
+    // rows of o that overlap would be written by several threads at once
+    if (!rows_apart(T, H, a->o_ld, a->o_head_stride, cache->head_dim)) return MOE_ERR_INVALID_ARG;
     // work is counted in 31 bits: tiles of as few tokens as any kernel takes, against tiles of keys
     const int64_t group = a->num_q_heads / cache->num_heads, rows = a->max_q * group;
     const int64_t tokens = rows > kFewRows ? 128 / group * 2 : (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) / group;

@@ -176,6 +176,29 @@ def test_the_binding_checks_tensors():
             B.moe_draft_verify(*args)
 
 
+def test_rows_of_o_lie_apart(P):
+    """Overlapping rows of o are refused, whatever their order; layouts without overlap are not (they go on to
+    the check of the workspace)."""
+    c = cache(P)  # heads of 128
+    for o_ld, o_head in ((0, 128), (1024, 0), (1024, 64), (120, 128), (128, 128), (896, 128), (128, 512), (128, 632),
+                         (128 * 5, 128 * 3), (256, 384)):
+        assert attn(P, c, T=5, max_q=5, o_ld=o_ld, o_head_stride=o_head, workspace=None) == INVALID, (o_ld, o_head)
+    for o_ld, o_head in ((1024, 128), (128, 640), (128, 648), (2048, 256), (1 << 30, 128), (128 * 8, 128 * 40), (256, 128 * 11)):
+        assert attn(P, c, T=5, max_q=5, o_ld=o_ld, o_head_stride=o_head, workspace=None) == WORKSPACE, (o_ld, o_head)
+    # by counting, for every small layout of both orders
+    for T in (1, 2, 3):
+        for ld in range(0, 1200, 64):
+            for hs in range(0, 1200, 64):
+                at = sorted(t * ld + h * hs for t in range(T) for h in range(4))
+                apart = all(b - a >= 128 for a, b in zip(at, at[1:]))
+                got = attn(P, c, T=T, max_q=T, num_q_heads=4, o_ld=ld, o_head_stride=hs, workspace=None)
+                assert got == (WORKSPACE if apart else INVALID), (T, ld, hs)
+    assert attn(P, c, o_ld=0, workspace=None) == WORKSPACE, "one token: its stride is not used"
+    big = 1 << 39
+    for kw in (dict(o_ld=big), dict(q_ld=big), dict(o_head_stride=big), dict(q_head_stride=big)):
+        assert attn(P, c, T=2, max_q=2, workspace=None, **kw) == UNSUPPORTED, kw
+
+
 @pytest.mark.parametrize("D,other", [(64, 128), (128, 64)])
 def test_the_binding_checks_the_width_of_q_and_o(D, other):
     """Heads of another width than the cache's are refused before the C call, which sees pointers and
