@@ -186,12 +186,13 @@ def test_rows_of_o_lie_apart(P):
     for o_ld, o_head in ((1024, 128), (128, 640), (128, 648), (2048, 256), (1 << 30, 128), (128 * 8, 128 * 40), (256, 128 * 11)):
         assert attn(P, c, T=5, max_q=5, o_ld=o_ld, o_head_stride=o_head, workspace=None) == WORKSPACE, (o_ld, o_head)
     # by counting, for every small layout of both orders
+    at0 = P()
     for T in (1, 2, 3):
         for ld in range(0, 1200, 64):
             for hs in range(0, 1200, 64):
                 at = sorted(t * ld + h * hs for t in range(T) for h in range(4))
                 apart = all(b - a >= 128 for a, b in zip(at, at[1:]))
-                got = attn(P, c, T=T, max_q=T, num_q_heads=4, o_ld=ld, o_head_stride=hs, workspace=None)
+                got = attn(lambda: at0, c, T=T, max_q=T, num_q_heads=4, o_ld=ld, o_head_stride=hs, workspace=None)
                 assert got == (WORKSPACE if apart else INVALID), (T, ld, hs)
     assert attn(P, c, o_ld=0, workspace=None) == WORKSPACE, "one token: its stride is not used"
     big = 1 << 39
