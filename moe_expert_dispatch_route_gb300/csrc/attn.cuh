@@ -434,7 +434,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// 2^e as a float, 0 below its range.
+// 2^e as a float, 0 below its normal range.
 __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __int_as_float((min(e, 127) + 127) << 23); }
 
 // Four e4m3 codes as two fp16 pairs.
@@ -452,12 +452,50 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // [2^14, 2^15), at most 2^100 (a row of zeros, or of numbers so small that its scores are 0).
 __device__ __forceinline__ int f16_row_exp(uint32_t mx) { return min(14 - ((int)(mx >> 7) - 127), 100); }
 
-constexpr int kPBits = 7;       // e4m3: probabilities are multiplied by 2^7
+// An e4m3 cache's value scales.  A weight is its probability times 2^(b - ref) and 2^kPBits, b the value's
+// scale byte, ref a reference to which o refers as well.  In fp16 what a weight adds to o is off by 2^-11 of
+// itself or by 2^-32 of a value at the reference, whichever is more; so fp16 takes the keys whose
+// scales lie from the smallest one so far to 2^kNear above it, where the latter is 2^-20 of what any key
+// may add.  Keys with larger values, and those that come after much smaller ones were let go, take a way whose
+// weights keep their exponents: what a row gets from its keys does not depend on how large a value
+// beside them is, one that the row hardly weighs or does not see.
+constexpr int kPBits = 7;
+constexpr uint32_t kNear = 12;
+constexpr uint32_t kFarUp = 60;  // the most that a value's scale is above the reference: o stays in fp32's range
+struct Scales {
+    uint32_t lo, ref, top;  // smallest scale byte so far, reference, largest; top = 0: none yet
+    uint32_t span;          // bytes from ref - span to ref change nothing here and are near the reference
+};
+// Whether scale bytes from lo to top are multiplied in fp16.
+__device__ __forceinline__ bool near_ref(const Scales& w, uint32_t lo, uint32_t top) {
+    return top <= w.ref && w.ref - lo <= kNear;
+}
+// Takes the scale bytes from lo to top in.
+__device__ __forceinline__ void take_in(Scales& w, uint32_t lo, uint32_t top) {
+    if (lo > top) return;  // none
+    w.lo = w.top == 0 ? lo : min(w.lo, lo);
+    w.top = max(w.top, top);
+    w.ref = max(min(w.top, w.lo + kNear), w.top - min(w.top, kFarUp));
+    w.span = min(w.ref - w.lo, kNear);
+}
+// Two e4m3 codes as fp16 -> as bf16 (exact).
+__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_bf16x2(f.x, f.y);
+}
 constexpr float kLoose = 8.0f;  // log2 of how far a row's maximum may run ahead of the one in use
 
-// The value of a UE8M0 scale byte (255: NaN).
+// The exponent e by which a sum l of probabilities (relative to a maximum m that is followed loosely), o and m
+// change to l 2^-e, o 2^-e and m + e before o, whose values may be near the end of fp32's range, is added up with
+// others: l 2^-e is at most 2^-8, so 256 such o may be added.
+__device__ __forceinline__ int sum_exp(float l) {
+    const int e = (__float_as_int(l) >> 23) & 255;
+    return e == 0 || e == 255 ? 0 : e - 127 + 9;
+}
+
+// The value of a UE8M0 scale byte (0: 2^-127, 255: NaN).
 __device__ __forceinline__ float scale_of(uint8_t b) {
-    return b == 255 ? CUDART_NAN_F : __uint_as_float((uint32_t)b << 23);
+    return b == 255 ? CUDART_NAN_F : __uint_as_float(b == 0 ? 0x00400000u : (uint32_t)b << 23);
 }
 
 __device__ __forceinline__ float* part_o(const Params& p, int cta, int slot) {

@@ -19,8 +19,9 @@
 // range exactly:
 //   q   a row is multiplied by a power of two that brings its largest element into [2^14, 2^15);
 //       an element 2^29 below that becomes subnormal, an absolute error of 2^-40 of the largest
-//   p   2^7 p 2^(s - r), s the value's scale exponent, r the largest s so far: at most 2^15, and
-//       what falls below fp16's range is under 2^-31 of the largest weight a key can have
+//   p   2^7 p 2^(s - r), s the value's scale exponent, r a reference at most 2^12 above it: at most
+//       2^15, and where fp16's range ends what it adds to o is off by 2^-32 of a value at the reference
+// 32 keys among which a value's scale lies elsewhere take their weights and values in bf16 (attn.cuh).
 //
 // The running maximum is followed loosely: o and the sum stay relative to an older maximum
 // until a row's new one is 2^8 times as large (in the probabilities, which are then at most
@@ -32,6 +33,8 @@
 // of 64, 51 us (4.3 TB/s: start, joins and the consumers' latency); one request of 777 tokens 7.8 us,
 // a chain of dependent loads and barriers.
 #include "attn.cuh"
+
+#include <type_traits>
 
 namespace moe {
 namespace attn {
@@ -218,7 +221,8 @@ __device__ void stage_rows(const Params& p, const Item& it, RowLoads<kD, kRows>&
             uint8_t* at = row + (piece >> 1) * 32 + (piece & 1) * 8;
             *reinterpret_cast<uint2*>(at) = make_uint2(f[0], f[2]);
             *reinterpret_cast<uint2*>(at + 16) = make_uint2(f[1], f[3]);
-            if (piece == 0) info->row_scale[r] = p.scale_log2 * pow2(-u1) * pow2(-u2);
+            // not 0: a row whose scores are all but 0 must not make -inf * 0 of the mask
+            if (piece == 0) info->row_scale[r] = fmaxf(p.scale_log2 * pow2(-u1) * pow2(-u2), 0x1p-149f);
         }
     }
 }
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             }
         const int lo_all = info->lo_all, hi_all = info->hi_all, lo_any = info->it.s.lo, hi_any = info->it.s.hi;
         const int tile0 = info->it.k0, count = info->it.n;
-        uint32_t vref = 0;  // e4m3: the largest value scale byte so far
+        Scales vs = {0, 0, 0, 0};  // e4m3: of the values
         for (int kt = (tg + C::kTG - (int)(tiles % C::kTG)) % C::kTG; kt < count; kt += C::kTG) {
             const uint32_t at = tiles + kt, stage = at % C::kStages, parity = (at / C::kStages) & 1;
             const uint32_t k_addr = tc::smem_u32(ring + 2 * stage * C::kTileBytes), v_addr = k_addr + C::kTileBytes;
@@ -580,84 +584,107 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                 // keys of this chunk that no row sees hold anything, NaN among it: their values read as 0
                 const bool tail = key0 < lo_any || key0 + 16 * C::kStrips > hi_any;
                 float vscale = 1.0f;  // e4m3: of key `lane`
+                bool far = false;
                 if (kFp8) {
+                    const bool unseen = tail && (key0 + lane < lo_any || key0 + lane >= hi_any);
                     uint32_t vb = sc_at[kKeyTile + in0 + lane];
-                    if (tail && (key0 + lane < lo_any || key0 + lane >= hi_any)) vb = 0;
-                    if (__any_sync(0xffffffffu, vb > vref)) {
-                        const uint32_t to = max(vref, __reduce_max_sync(0xffffffffu, vb));
-                        const float f = pow2((int)vref - (int)to);
-                        vref = to;
+                    if (unseen) vb = vs.ref;  // its value reads as 0
+                    vscale = __uint_as_float((vb - vs.ref + kPBits + 127) << 23);
+                    if (__any_sync(0xffffffffu, vs.ref - vb > vs.span)) {
+                        const bool counts = !unseen && vb < 255;
+                        const uint32_t lo = __reduce_min_sync(0xffffffffu, counts ? vb : 255u);
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, counts ? vb : 0u), was = vs.ref;
+                        take_in(vs, lo, top);
+                        if (vs.ref != was) {
+                            const float f = pow2((int)was - (int)vs.ref);
 #pragma unroll
-                        for (int j = 0; j < kSteps; ++j)
+                            for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-                            for (int t = 0; t < kNT; ++t)
+                                for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) o[j][t][i] *= f;
-                    }
-                    const int ex = (int)vb - (int)vref + kPBits + 127;
-                    vscale = vb == 255 ? CUDART_NAN_F : vb == 0 || ex <= 0 ? 0.0f : __int_as_float(ex << 23);
-                }
-                uint32_t pb[C::kStrips][kNT][2];  // (row g, keys 2c, 2c + 1) and 8 keys further
-#pragma unroll
-                for (int st = 0; st < C::kStrips; ++st)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float f = kFp8 ? __shfl_sync(0xffffffffu, vscale, st * 16 + y * 8 + g) : 1.0f;
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) {
-                            const float p0 = exp2_fast(fmaf(s[st][t][2 * y], row_scale[t][0], base[t][0]));
-                            const float p1 = exp2_fast(fmaf(s[st][t][2 * y + 1], row_scale[t][1], base[t][1]));
-                            l[t][0] += p0;
-                            l[t][1] += p1;
-                            pb[st][t][y] = transpose8(kFp8 ? pack_f16x2(p0 * f, p1 * f) : pack_bf16x2(p0, p1));
+                                    for (int i = 0; i < 4; ++i) o[j][t][i] *= f;
                         }
+                        if (unseen) vb = vs.ref;
+                        far = !near_ref(vs, min(lo, top), top);
+                        vscale = vb == 255 ? CUDART_NAN_F : pow2((int)vb - (int)vs.ref + kPBits);
                     }
-                // ---- o += p v
+                }
+                auto weigh = [&](auto far_t) {
+                    constexpr bool kFar = decltype(far_t)::value;  // e4m3: weights and values in bf16
+                    uint32_t pb[C::kStrips][kNT][2];  // (row g, keys 2c, 2c + 1) and 8 keys further
 #pragma unroll
-                for (int st = 0; st < C::kStrips; ++st) {
-                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs 2c, 2c + 1 and 8 further
-                    if (tail) {
+                    for (int st = 0; st < C::kStrips; ++st)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
+                        for (int y = 0; y < 2; ++y) {
+                            const float f = kFp8 ? __shfl_sync(0xffffffffu, vscale, st * 16 + y * 8 + g) : 1.0f;
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int key = key0 + st * 16 + y * 8 + c * 2 + x;
-                                if (key < lo_any || key >= hi_any) keep[y] &= x ? 0x0000ffffu : 0xffff0000u;
+                            for (int t = 0; t < kNT; ++t) {
+                                const float p0 = exp2_fast(fmaf(s[st][t][2 * y], row_scale[t][0], base[t][0]));
+                                const float p1 = exp2_fast(fmaf(s[st][t][2 * y + 1], row_scale[t][1], base[t][1]));
+                                l[t][0] += p0;
+                                l[t][1] += p1;
+                                pb[st][t][y] = transpose8(!kFp8  ? pack_bf16x2(p0, p1)
+                                                          : kFar ? pack_bf16x2(p0 * f, p1 * f)
+                                                                 : pack_f16x2(p0 * f, p1 * f));
                             }
-                    }
-                    if (kFp8) {
+                        }
+                    // ---- o += p v
 #pragma unroll
-                        for (int j = 0; j < kSteps; j += 2) {
-                            uint32_t w[4];  // keys 0-7 and 8-15 of chunk j, then of chunk j + 1
-                            ldsm_x4_t(w, v_addr + swizzled<C::kRowBytes>(
-                                                      in0 + st * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), j + (lane >> 4)));
+                    for (int st = 0; st < C::kStrips; ++st) {
+                        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs 2c, 2c + 1 and 8 further
+                        if (tail) {
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                // bytes: a pair of keys of column 2 g, then of column 2 g + 1
-                                uint32_t w0 = __byte_perm(w[2 * u], 0, 0x3120), w1 = __byte_perm(w[2 * u + 1], 0, 0x3120);
-                                if (tail) {
-                                    w0 &= __byte_perm(keep[0], 0, 0x2020);
-                                    w1 &= __byte_perm(keep[1], 0, 0x2020);
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const int key = key0 + st * 16 + y * 8 + c * 2 + x;
+                                    if (key < lo_any || key >= hi_any) keep[y] &= x ? 0x0000ffffu : 0xffff0000u;
                                 }
-                                uint32_t a[4];
-                                e4m3x4_f16(w0, a[0], a[1]);
-                                e4m3x4_f16(w1, a[2], a[3]);
+                        }
+                        if (kFp8) {
 #pragma unroll
-                                for (int t = 0; t < kNT; ++t) mma16816<true>(o[j + u][t], a, pb[st][t][0], pb[st][t][1]);
+                            for (int j = 0; j < kSteps; j += 2) {
+                                uint32_t w[4];  // keys 0-7 and 8-15 of chunk j, then of chunk j + 1
+                                ldsm_x4_t(w, v_addr + swizzled<C::kRowBytes>(
+                                                          in0 + st * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), j + (lane >> 4)));
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    // bytes: a pair of keys of column 2 g, then of column 2 g + 1
+                                    uint32_t w0 = __byte_perm(w[2 * u], 0, 0x3120);
+                                    uint32_t w1 = __byte_perm(w[2 * u + 1], 0, 0x3120);
+                                    if (tail) {
+                                        w0 &= __byte_perm(keep[0], 0, 0x2020);
+                                        w1 &= __byte_perm(keep[1], 0, 0x2020);
+                                    }
+                                    uint32_t a[4];
+                                    e4m3x4_f16(w0, a[0], a[1]);
+                                    e4m3x4_f16(w1, a[2], a[3]);
+                                    if (kFar) {
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) a[i] = f16x2_bf16x2(a[i]);
+                                    }
+#pragma unroll
+                                    for (int t = 0; t < kNT; ++t)
+                                        mma16816<!kFar>(o[j + u][t], a, pb[st][t][0], pb[st][t][1]);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kSteps; ++j) {
+                                uint32_t a[4];
+                                ldsm_x4_t(a, v_addr + swizzled<C::kRowBytes>(in0 + st * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                                             2 * j + ((lane >> 3) & 1)));
+                                if (tail) a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
+#pragma unroll
+                                for (int t = 0; t < kNT; ++t) mma16816<false>(o[j][t], a, pb[st][t][0], pb[st][t][1]);
                             }
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kSteps; ++j) {
-                            uint32_t a[4];
-                            ldsm_x4_t(a, v_addr + swizzled<C::kRowBytes>(in0 + st * 16 + (lane >> 4) * 8 + (lane & 7),
-                                                                         2 * j + ((lane >> 3) & 1)));
-                            if (tail) a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
-#pragma unroll
-                            for (int t = 0; t < kNT; ++t) mma16816<false>(o[j][t], a, pb[st][t][0], pb[st][t][1]);
-                        }
                     }
-                }
+                };
+                if (kFp8 && far)
+                    weigh(std::true_type{});
+                else
+                    weigh(std::false_type{});
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[2 * stage + 1]);
@@ -677,15 +704,20 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], w);
                 }
-            if (kFp8) {  // back from 2^7 2^-r
-                const int e2 = (int)vref - 127 - kPBits;
-                const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
+            if (kFp8) {  // back from 2^7 2^-r, and relative to a maximum that keeps the sums of o in range
 #pragma unroll
-                for (int j = 0; j < kSteps; ++j)
+                for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                    for (int t = 0; t < kNT; ++t)
+                    for (int x = 0; x < 2; ++x) {
+                        const int up = sum_exp(l[t][x]), e2 = (int)vs.ref - 127 - kPBits - up;
+                        const float f1 = pow2(e2 / 2), f2 = pow2(e2 - e2 / 2);
+                        m[t][x] += (float)up;
+                        l[t][x] *= pow2(-up);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[j][t][i] = o[j][t][i] * f1 * f2;
+                        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                            for (int i = x; i < 4; i += 2) o[j][t][i] = o[j][t][i] * f1 * f2;
+                    }
             }
         }
         // where an element stands: column 16 j + g (+ 8), or 16 j + 2 g (+ 1) from e4m3 pairs
