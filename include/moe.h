@@ -469,8 +469,15 @@ MOE_API moe_status moe_kv_read(const moe_kv_cache* cache, int32_t B, int32_t T, 
  * lse = -inf.  What lies in tokens that no row of the request sees -- the rest of the last
  * page, pages before the window -- never reaches a result, whatever it holds.  (A NaN or an
  * infinity in a value that some of its rows see may make others of its rows NaN.)  Scores, the softmax's
- * maximum and sum, and o are held in fp32; the probabilities are rounded to bf16 for the
- * second product (the sum takes them before that), o once at the end.
+ * maximum and sum, and o are held in fp32 (scores past 2^24 are told apart no longer), o is rounded once
+ * at the end.  The probabilities are rounded for the second product, and the sum takes them before that:
+ *   bf16 cache  to bf16
+ *   e4m3 cache  to fp16, where the values' scales lie within 2^12 of the request's smallest: what a key adds to o
+ *               is off by 2^-11 of itself, or by 2^-20 of a value at that smallest scale for a key of little
+ *               weight.  Larger values go by a slower way, with each probability to bf16 or better, so what is
+ *               next to a row's keys, seen or not, does not change what it gets from them (down to 2^-100 of
+ *               it).  q is held in fp16 times a power of two: exactly, but for elements under 2^-29 of the
+ *               row's largest, which are off by up to 2^-40 of it.
  * Requests may be mixed freely: one new token, a draft, a prompt chunk. */
 typedef struct {
     const void* q;              /* device bf16: head h of row t at t*q_ld + h*q_head_stride */

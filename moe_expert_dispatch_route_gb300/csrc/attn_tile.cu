@@ -25,10 +25,13 @@
 //
 // An e4m3 cache is multiplied in fp16: a conversion instruction and a product turn two codes
 // into two elements (bf16 takes ten for four: shifts, masks and products).  What is multiplied is
-//   q   a row times a power of two that brings its largest element into [2^14, 2^15)
-//   k   code * 2^(s - r), s the key's scale exponent, r the largest in the tile; v likewise
-//   p   2^7 p 2^(r - R) for a V tile with reference r, R the largest so far, to which o refers
-// Each is exact but for what lies under 2^-31 of the largest number of its kind (2^-33 for k, v).
+//   q   a row times a power of two that brings its largest element into [2^14, 2^15); what lies
+//       2^29 below that is off by 2^-40 of the largest
+//   k   code * 2^(s - r), s the key's scale exponent, r a reference at most 2^15 above it: exact
+//   v   likewise, with a reference to which o refers and that is at most 2^12 above (attn.cuh)
+//   p   2^7 p
+// A tile whose scales lie elsewhere holds the codes as they are: its scores are multiplied by 2^s and its part
+// of o is added up in fp32 by the softmax's threads, several times as long.
 // The same chunk takes 1412 us: the conversion shares shared memory and issue slots with the rest
 // (left out, when this took 1540, it left 1250).
 //
@@ -44,7 +47,10 @@ namespace attn {
 namespace {
 
 constexpr int kHalfRows = 128;
-constexpr int kRefs = 8;  // tiles whose references are kept: more than the pipeline is deep
+// Tiles whose references and scales are kept.  The warps that come to tile t have had the ring's entry that the
+// values of tile t - 3 held (of 6 entries: t - 4), so those of at most four tiles are in use.
+constexpr int kRefs = 4;
+constexpr int kSpread = 15;  // fp16 holds an e4m3 code times 2^-15 exactly
 
 template <int kD, bool kFp8>
 struct Cfg {
@@ -56,8 +62,11 @@ struct Cfg {
     static constexpr int kRawBytes = kKeyTile * kD;                   // an e4m3 one
     static constexpr int kEntries = kFp8 ? (kD == 64 ? 6 : 4) : kD == 64 ? 8 : 5;
     static constexpr int kRaw = kFp8 ? (kD == 64 ? 6 : 2) : 0;
-    static constexpr int kFp8Bytes = kFp8 ? kRaw * (kRawBytes + kKeyTile) + 2 * kRefs : 0;
-    static constexpr int kSmem = 1024 + kQBytes + kEntries * kEntryBytes + kFp8Bytes + 512;
+    // e4m3: raw tiles, their scales; of kRefs tiles the keys' and values' scales and references
+    static constexpr int kFp8Bytes = kFp8 ? kRaw * (kRawBytes + kKeyTile) + kRefs * (2 * kKeyTile + 4) : 0;
+    static constexpr int kBars = 2 * (kEntries + kRaw) + 2 + 6 + 1 + kRefs + 2;  // 8 bytes each
+    static constexpr int kTail = (8 * kBars + 4 * (kEntries + kRaw) + 15) / 16 * 16;
+    static constexpr int kSmem = 1024 + kQBytes + kEntries * kEntryBytes + kFp8Bytes + kTail;
     static_assert(kSmem <= 232448 - 256, "");
     static_assert(kEntries * kEntryBytes >= (kMaxRequests + 32) * 4, "locate()'s scratch");
     // registers per thread after the redistribution: softmax, converters, the rest; their sum
@@ -76,6 +85,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -83,6 +97,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -298,8 +317,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     uint8_t* ring = qs + C::kQBytes;                          // bf16 tiles, as the MMAs read them
     uint8_t* raw = ring + C::kEntries * C::kEntryBytes;       // e4m3 tiles
     uint8_t* scales = raw + C::kRaw * C::kRawBytes;
-    uint8_t* k_ref = scales + C::kRaw * kKeyTile;  // e4m3: references of K and V tiles
-    uint8_t* v_ref = k_ref + kRefs;
+    // e4m3, of the last kRefs tiles: scale bytes of keys and values; references of both, bit 16: far apart
+    uint8_t* tile_scales = scales + C::kRaw * kKeyTile;
+    uint32_t* tile_refs = reinterpret_cast<uint32_t*>(tile_scales + kRefs * 2 * kKeyTile);
     uint64_t* full = reinterpret_cast<uint64_t*>(raw + C::kFp8Bytes);
     uint64_t* empty = full + C::kEntries;
     uint64_t* raw_full = empty + C::kEntries;
@@ -595,6 +615,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
         regs_dec<C::kRegsConv>();
         int re = 0, e = 0;
         uint32_t rturn = 0, turn = 0, tile = 0;
+        int k_ref = 1;  // of the last tile of keys
+        bool k_far = false;
+        Scales vs = {0, 8, 0, 0};  // of the query tile's values
         // A warp turns 32 keys, 8 at a time.  Eight lanes read four chunks of rows r and r ^ 5:
         // under the 128-byte swizzle both the 16-byte reads and the two 16-byte writes of each
         // lane fall into different banks.
@@ -606,19 +629,45 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             const bool values = i & 1;
             const int z0 = cmd >> kSeenLo & 255, z1 = cmd >> kSeenHi & 255;
             const uint8_t* sc = scales + re * kKeyTile;
-            // the tile's reference: the largest scale byte of a key that is seen, 255 (NaN) aside
-            uint32_t top = 0;
+            // the reference of the tile's scales, and whether they are too far from it
+            const bool edge = z0 > 0 || z1 < kKeyTile;
+            if (values && (cmd & kNewQ)) vs = {0, 8, 0, 0};
+            int ref = values ? (int)vs.ref : k_ref;
+            bool far = values && k_far;
             if (!(cmd & kStop)) {
-                const uint32_t four = reinterpret_cast<const uint32_t*>(sc)[lane];
+                uint32_t four = reinterpret_cast<const uint32_t*>(sc)[lane];
+                if (edge) {  // 255 for keys that are not seen: like NaN, it counts for nothing
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t b = four >> (8 * j) & 255;
-                    if (lane * 4 + j >= z0 && lane * 4 + j < z1 && b < 255) top = max(top, b);
+                    for (int j = 0; j < 4; ++j)
+                        if (lane * 4 + j < z0 || lane * 4 + j >= z1) four |= 255u << (8 * j);
                 }
-                top = __reduce_max_sync(0xffffffffu, top);
-                if (warp == 8 && lane == 0) {
-                    (values ? v_ref : k_ref)[tile % kRefs] = (uint8_t)top;
-                    if (values) tc::mbar_arrive(&ref_full[tile % kRefs]);
+                // the largest byte + 1, 255 wrapping to 0, and the smallest, two bytes at a time
+                const uint32_t even = four & 0xff00ffu, odd = four >> 8 & 0xff00ffu;
+                const uint32_t mx2 = __vmaxu2((even + 0x10001u) & 0xff00ffu, (odd + 0x10001u) & 0xff00ffu);
+                const uint32_t mn2 = __vminu2(even, odd), mx = max(mx2 & 255, mx2 >> 16), mn = min(mn2 & 255, mn2 >> 16);
+                if (__any_sync(0xffffffffu, (int)mx > ref + 1 || (int)mn < ref - (values ? (int)vs.span : kSpread))) {
+                    const int top = (int)__reduce_max_sync(0xffffffffu, mx) - 1;
+                    const int low = __reduce_min_sync(0xffffffffu, mn);
+                    if (!values) {
+                        k_ref = ref = max(top, 1);  // 2^(ref - 127) is a normal number
+                        far = top - low > kSpread;
+                    } else {
+                        take_in(vs, low, top);
+                        // 2^(ref - 127 - kPBits), the unit of o, is a normal number
+                        vs.ref = max(vs.ref, 8u);
+                        ref = vs.ref;
+                        far |= !near_ref(vs, low, top);
+                    }
+                }
+                if (!values) k_far = far;
+                if (warp == 8) {  // for the softmax
+                    const uint32_t known = values || far ? four : ref * 0x01010101u;
+                    reinterpret_cast<uint32_t*>(tile_scales)[(tile % kRefs * 2 + values) * 32 + lane] = known;
+                    __syncwarp();
+                    if (values && lane == 0) {
+                        tile_refs[tile % kRefs] = k_ref | ref << 8 | (far ? 1u << 16 : 0u);
+                        tc::mbar_arrive(&ref_full[tile % kRefs]);
+                    }
                 }
             }
             if (turn > 0) wait(&empty[e], (turn - 1) & 1);
@@ -638,7 +687,8 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             // lane i: the factor of key 32 * (warp - 8) + i: 2^ex in fp16, subnormal below 2^-14
             uint32_t factor;
             {
-                const int key = (warp - 8) * 32 + lane, b = sc[key], ex = b - (int)top;
+                const int key = (warp - 8) * 32 + lane, b = sc[key];
+                const int ex = far ? 0 : b - ref;  // far: the codes as they are
                 factor = (b == 255    ? 0x7e00u
                           : ex >= -14 ? (uint32_t)(ex + 15) << 10
                           : ex >= -24 ? 1u << (ex + 24)
@@ -646,7 +696,6 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                          0x10001u;
                 if (key < z0 || key >= z1) factor = 0;
             }
-            const bool edge = z0 > 0 || z1 < kKeyTile;
             const int first = (warp - 8) * 32 + row8;
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
@@ -755,13 +804,13 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             for (int kt = v.k0[h]; kt < k1; ++kt, ++n) {
                 const int key0 = kt * kKeyTile;
                 float scale = row_scale;
-                int v_exp = 0;
-                if (kFp8) {  // the references of this tile's V, and of its K, which come before
+                uint32_t refs = 0;
+                if (kFp8) {  // what is known of this tile once its V has come, after its K
                     const uint32_t t = tiles + (uint32_t)(kt - it.k0);
                     wait(&ref_full[t % kRefs], t / kRefs & 1);
+                    refs = tile_refs[t % kRefs];
                     // a row whose scores are all but 0 must not make -inf * 0 of the mask
-                    scale = fmaxf(row_scale * pow2((int)k_ref[t % kRefs] - 127), 0x1p-120f);
-                    v_exp = v_ref[t % kRefs];
+                    scale = fmaxf(row_scale * pow2((int)(refs & 255) - 127), 0x1p-120f);
                 }
                 wait(&s_full[h], n & 1);
                 tc::tc_fence_after();
@@ -791,16 +840,105 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 }
                 const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
                 const bool move = mn - m > kLoose;  // also from -inf
-                if (kt == v.k0[h]) {
+                const int v_ref = refs >> 8;  // 256 and more: far
+                if (kt == v.k0[h] && (!kFp8 || v_ref < 256)) {
                     m = mn;
-                    o_ref = v_exp;
-                } else if (__any_sync(0xffffffffu, move || (kFp8 && v_exp > o_ref))) {
+                    o_ref = v_ref;
+                } else if (__any_sync(0xffffffffu, move || (kFp8 && v_ref != o_ref))) {
+                    if (kFp8 && v_ref >= 256) {
+                        // Scales far from each other: each thread does its row alone, in fp32, every key with its own
+                        // scale.  Here, where few tiles come, and in little code: the loops around it lose by
+                        // every instruction between them (a form on the MMAs, with bf16 values, from a branch of
+                        // its own: 166 us for ragged chunks whose scales are near, 162 with this).
+                        const uint32_t t = tiles + (uint32_t)(kt - it.k0), entry = 2 * t + 1;
+                        const uint8_t* sc = tile_scales + t % kRefs * (2 * kKeyTile);
+                        const uint8_t* values = ring + entry % C::kEntries * C::kEntryBytes;
+                        auto score = [&](uint32_t x, int j) {
+                            const int key = key0 + j;
+                            return key < lo || key >= hi ? -CUDART_INF_F : __uint_as_float(x) * row_scale * scale_of(sc[j]);
+                        };
+                        uint32_t x[8];
+                        float top = m;
+#pragma unroll 1
+                        for (int i = 0; i < 16; ++i) {
+                            tmem_ld8(ts + i * 8, x);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) top = fmaxf(top, score(x[j], i * 8 + j));
+                        }
+                        const bool first = kt == v.k0[h];
+                        float f = m == -CUDART_INF_F ? 1.0f : exp2_fast(m - top);
+                        m = top;
+                        l *= f;
+                        if (!first) f *= pow2(o_ref - (v_ref & 255));
+                        o_ref = v_ref & 255;
+                        // the weights, in the place of the scores
+                        const float from = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll 1
+                        for (int i = 0; i < 16; ++i) {
+                            tmem_ld8(ts + i * 8, x);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float w = exp2_fast(score(x[j], i * 8 + j) - from);
+                                l += w;
+                                x[j] = __float_as_uint(w * pow2((int)sc[kKeyTile + i * 8 + j] - o_ref + kPBits));
+                            }
+                            tmem_st8(ts + i * 8, x);
+                        }
+                        tmem_wait_st();
+                        wait(&full[entry % C::kEntries], entry / C::kEntries & 1);
+                        float add[kD];  // not in registers: indexed in a loop
+#pragma unroll 1
+                        for (int c = 0; c < kD / 8; ++c) {
+                            float2 sum[4] = {};
+#pragma unroll 1
+                            for (int i = 0; i < 16; ++i) {
+                                tmem_ld8(ts + i * 8, x);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint4 q = *reinterpret_cast<const uint4*>(
+                                        values + (c >> 3) * C::kBlockBytes + (i * 8 + j) * 128 + (((c & 7) ^ j) << 4));
+                                    const uint32_t codes[4] = {q.x, q.y, q.z, q.w};
+                                    const float2 w = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j]));
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y)
+                                        sum[y] = fma2(w, __half22float2(*reinterpret_cast<const __half2*>(&codes[y])), sum[y]);
+                                }
+                            }
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) add[c * 8 + 2 * y] = sum[y].x, add[c * 8 + 2 * y + 1] = sum[y].y;
+                        }
+                        // the MMA adds nothing (or makes o zeros, if this tile is the first)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = 0;
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) tmem_st8(ts + i * 8, x);
+                        tmem_wait_st();
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&p_full[h]);
+                        wait(&pv_done[h], n & 1);
+                        tc::tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < kD / 8; ++i) {
+                            tmem_ld8(to + i * 8, x);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f, add[i * 8 + j]));
+                            tmem_st8(to + i * 8, x);
+                        }
+                        tmem_wait_st();
+                        continue;
+                    }
                     float f = move ? exp2_fast(m - mn) : 1.0f;
                     if (move) m = mn;
                     l *= f;
-                    if (kFp8 && v_exp > o_ref) {
-                        f *= pow2(o_ref - v_exp);
-                        o_ref = v_exp;
+                    if (kFp8) {
+                        f *= pow2(o_ref - v_ref);
+                        o_ref = v_ref;
                     }
                     wait(&pv_done[h], (n - 1) & 1);
                     tc::tc_fence_after();
@@ -814,12 +952,8 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                         tmem_st16(to + i * 16, o);
                     }
                 }
-                float base = m == -CUDART_INF_F ? 0.0f : m, back = 1.0f;
-                if (kFp8) {  // probabilities come out times 2^shift; the sum takes that back
-                    const int shift = max(v_exp - o_ref, -60) + kPBits;  // below 2^-60 fp16 has 0 anyway
-                    base -= (float)shift;
-                    back = pow2(-shift);
-                }
+                // e4m3: probabilities come out times 2^kPBits; the sum takes that back
+                const float base = (m == -CUDART_INF_F ? 0.0f : m) - (kFp8 ? (float)kPBits : 0.0f);
                 const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(-base, -base);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -842,7 +976,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&p_full[h]);
                 sum[0] = add2(sum[0], sum[1]);
-                l += kFp8 ? (sum[0].x + sum[0].y) * back : sum[0].x + sum[0].y;
+                l += (sum[0].x + sum[0].y) * (kFp8 ? 1.0f / (1 << kPBits) : 1.0f);
             }
             // the item again, from the cursor: its fields would cost registers throughout the loop above
             __syncwarp();
@@ -858,7 +992,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
             tiles += it.n;
             const float o_unit = kFp8 ? pow2(o_ref - 127 - kPBits) : 1.0f;
             if (it.whole) {
-                const float inv = l > 0.0f ? o_unit / l : (l == 0.0f ? 0.0f : l);
+                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
                 uint16_t* out = p.o + at.token * p.o_ld + at.head * p.o_head;
 #pragma unroll
                 for (int i = 0; i < kD / 32; ++i) {
@@ -873,9 +1007,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                             uint32_t w[4];
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                w[x] = l == 0.0f ? 0u
-                                                 : cvt_bf16x2(__uint_as_float(o[8 * j + 2 * x]) * inv,
-                                                              __uint_as_float(o[8 * j + 2 * x + 1]) * inv);
+                                w[x] = l == 0.0f ? 0u  // in two steps: the product of the factors may be subnormal
+                                                 : cvt_bf16x2(__uint_as_float(o[8 * j + 2 * x]) * inv * o_unit,
+                                                              __uint_as_float(o[8 * j + 2 * x + 1]) * inv * o_unit);
                             *reinterpret_cast<uint4*>(out + i * 32 + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
@@ -884,6 +1018,13 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     p.lse[(int64_t)at.token * p.heads * p.group + at.head] =
                         l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
             } else {
+                float down = 1.0f;
+                if (kFp8) {
+                    const int up = sum_exp(l);
+                    down = pow2(-up);
+                    m += (float)up;
+                    l *= down;
+                }
                 // parts: [four columns][row], so that a warp's rows lie side by side
                 const int slot = it.first ? 0 : 1, r = h * kHalfRows + row;
                 float4* out = reinterpret_cast<float4*>(part_o(p, blockIdx.x, slot)) + r;
@@ -894,14 +1035,12 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                         tc::tmem_ld32(to + i * 32, o);
                         tc::tmem_wait_ld();
                     }
+                    auto of = [&](int j) { return __uint_as_float(o[j]) * down * o_unit; };
                     if (valid) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            out[(i * 8 + j) * kMaxRows] =
-                                any ? make_float4(__uint_as_float(o[4 * j]) * o_unit, __uint_as_float(o[4 * j + 1]) * o_unit,
-                                                  __uint_as_float(o[4 * j + 2]) * o_unit,
-                                                  __uint_as_float(o[4 * j + 3]) * o_unit)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                            out[(i * 8 + j) * kMaxRows] = any ? make_float4(of(4 * j), of(4 * j + 1), of(4 * j + 2), of(4 * j + 3))
+                                                              : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 }
                 if (valid) part_ml(p, blockIdx.x, slot)[r] = make_float2(m, l);

@@ -76,7 +76,7 @@ class Ranges(Case):
 
 
 # rows a head: 4 * n.  Up to 32 are one kernel's, more another's.
-@pytest.mark.parametrize("n", [2, 8])
+@pytest.mark.parametrize("n", [2, 8, 20, 150])
 @pytest.mark.parametrize("what", [K, V])
 @pytest.mark.parametrize("gap", [12, 25, 40, 100])
 @pytest.mark.parametrize("D", [64, 128])
@@ -91,7 +91,7 @@ def test_scales_of_tokens_that_a_row_does_not_see(n, what, gap, D):
     c.check_o(skip=0 if what == K else None)
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 70])
 @pytest.mark.parametrize("weight", [0, 1, 2])
 @pytest.mark.parametrize("gap", [22, 30, 60, 100])
 def test_large_values_of_little_weight(n, weight, gap):
@@ -107,7 +107,7 @@ def test_large_values_of_little_weight(n, weight, gap):
         c.check_o()
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 70])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("max_ctas", [0, 3])
 def test_random_scales(n, D, max_ctas):
@@ -121,7 +121,7 @@ def test_random_scales(n, D, max_ctas):
     c.check_o(max_ctas=max_ctas)
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 70])
 @pytest.mark.parametrize("bytes_", [(60, 120, 180, 100), (180, 100, 60, 130), (110, 128, 118, 122), (40, 41, 240, 42)])
 @pytest.mark.parametrize("max_ctas", [0, 1])
 def test_columns_that_only_some_tokens_fill(n, bytes_, max_ctas):
@@ -166,7 +166,7 @@ def test_columns_that_only_some_tokens_fill(n, bytes_, max_ctas):
     c.check_o(max_ctas=max_ctas)
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 70])
 def test_the_smallest_scales(n):
     """A scale byte b stands for 2^(b - 127) down to b = 0; values of 2^-127 to 2^-111 come out as such."""
     c = Ranges([n, n], [200, 90])
@@ -191,7 +191,7 @@ def test_a_scale_near_the_smallest(n, dtype):
         c.check()
 
 
-@pytest.mark.parametrize("n", [1])
+@pytest.mark.parametrize("n", [1, 70])
 def test_weights_of_a_long_context(n):
     """One key with the weight of all the others together, each of which has 2^-14 of it: they add up."""
     kv = 16385
