@@ -38,8 +38,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
     // the same trips (shuffles below)
     const int runs = (H + kUnroll - 1) / kUnroll, items = T * 2 * runs;  // host: fits
     const int ngroups = gridDim.x * (kThreads / kLanes);
-    const int mine = (blockIdx.x * kThreads + threadIdx.x) / kLanes;
-    const int warp_first = (blockIdx.x * kThreads + (threadIdx.x & ~31)) / kLanes;
+    const int mine = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;  // threads may be more than 2^32
+    const int warp_first = blockIdx.x * (kThreads / kLanes) + (threadIdx.x & ~31) / kLanes;
     for (int i = mine, w0 = warp_first; w0 < items; i += ngroups, w0 += ngroups) {
         const int at = min(i, items - 1), h0 = at % runs * kUnroll, t = at / runs >> 1;
         const bool is_v = at / runs & 1;

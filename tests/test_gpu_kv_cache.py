@@ -123,6 +123,20 @@ def test_offsets_past_32_bits():
     assert torch.all((o[0].double() - mean).abs() <= 2.0**-8 * mean.abs() + 1e-6)
 
 
+def test_writes_of_more_than_32_bits_of_threads():
+    """2^27 + 8 tokens of one head, all but a few of them padding: the last ones are written."""
+    T = (1 << 27) + 8
+    (k, v), _, cache = pools(1, 1, 16, 128, "bf16")
+    x = torch.arange(2, dtype=torch.bfloat16, device=DEV)[:, None, None].expand(2, 1, 128).contiguous()
+    slots = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    slots[-5:] = torch.arange(5, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    # every token the same row: token stride 0
+    B.moe_kv_write(cache, x[0].expand(T, 1, 128), x[1].expand(T, 1, 128), slots, err_flag=err)
+    assert int(err.item()) == 0
+    assert torch.all(k[0, 0, :5] == 0) and torch.all(v[0, 0, :5] == 1) and torch.all(k[0, 0, 5:] == 1.5)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("H,page,order", [(1, 16, "hnd"), (3, 32, "nhd"), (8, 128, "hnd")])
