@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
     const int pieces = 2 * H * kLanes;  // of one row
     const int shift = __ffs(c.page_size) - 1;
     const int total = min(T, cu[B]);
-    const int warp = (blockIdx.x * kThreads + threadIdx.x) >> 5, nwarps = gridDim.x * (kThreads / 32);
+    const int warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), nwarps = gridDim.x * (kThreads / 32);
     for (int64_t first = (int64_t)warp * kRows; first < total; first += (int64_t)nwarps * kRows) {
         int64_t at = -1, sat = 0;  // lane i: element and scale offset of row i's head 0; -1: no such row
         if (lane < kRows && first + lane < total) {

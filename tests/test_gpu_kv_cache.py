@@ -137,6 +137,26 @@ def test_writes_of_more_than_32_bits_of_threads():
     assert torch.all(k[0, 0, :5] == 0) and torch.all(v[0, 0, :5] == 1) and torch.all(k[0, 0, 5:] == 1.5)
 
 
+def test_reads_of_more_than_32_bits_of_threads():
+    """2^29 + 40 rows of one head, the same cached tokens over and over: the last ones are written."""
+    if torch.cuda.mem_get_info()[0] < 180 << 30:
+        pytest.skip("needs 137 GB")
+    T, page = (1 << 29) + 40, 64
+    k = torch.randn(1, 1, page, 64, device=DEV).to(torch.bfloat16)
+    v = torch.randn(1, 1, page, 64, device=DEV).to(torch.bfloat16)
+    out = [torch.empty(T, 1, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for o in out:
+        o[-100:] = 9.0
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table = torch.zeros(1, T // page + 1, dtype=torch.int32, device=DEV)
+    B.moe_kv_read(B.kv_cache(k, v), table, i32([0]), i32([0, T - 3]), out[0], out[1], err_flag=err)
+    assert int(err.item()) == 0
+    at = torch.arange(T - 100, T - 3, device=DEV) % page
+    for o, pool in ((out[0], k), (out[1], v)):
+        assert torch.equal(o[-100:-3, 0], pool[0, 0, at]) and torch.all(o[-3:] == 9.0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("H,page,order", [(1, 16, "hnd"), (3, 32, "nhd"), (8, 128, "hnd")])
