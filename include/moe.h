@@ -533,12 +533,20 @@ MOE_API moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args
  * u, u_draw device fp32 [cu_draft[B]], [B], in [0, 1) (outside it is taken as the nearest).
  * out_ids  device int32 [B][max_draft + 1] (out): kept tokens, the drawn one, then -1.
  * out_len  device int32 [B] (out): c + 1.   max_draft <= 255.
- * max_ctas is rounded down to clusters of 8 CTAs, and up to one. */
+ * max_ctas is rounded down to clusters of 8 CTAs, and up to one.
+ * moe_draft_verify_ex knows how many drafted tokens there are room for: ids, u and draft have N rows, target
+ * N + B, and a request whose tokens are not all among them is refused like one with n > max_draft, so
+ * nothing past them is read.  moe_draft_verify takes cu_draft at its word. */
 MOE_API moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t dtype, const void* target,
                                     int64_t target_ld, const void* draft, int64_t draft_ld,
                                     const int32_t* cu_draft, const int32_t* ids, const float* u,
                                     const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err_flag,
                                     int32_t max_ctas, moe_stream_t stream);
+MOE_API moe_status moe_draft_verify_ex(int32_t B, int32_t N, int32_t vocab, int32_t max_draft, int32_t dtype,
+                                       const void* target, int64_t target_ld, const void* draft, int64_t draft_ld,
+                                       const int32_t* cu_draft, const int32_t* ids, const float* u,
+                                       const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err_flag,
+                                       int32_t max_ctas, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_debug_inject_wait -- test hook for the failure path of the bounded device

@@ -121,6 +121,8 @@ _SIGS = {
     "moe_attn_workspace_size": (_SZ, [_CACHE, _I32]),
     "moe_attn_paged": (_I32, [_CACHE, ctypes.POINTER(MoeAttnArgs), _I32, _P]),
     "moe_draft_verify": (_I32, [_I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
+    "moe_draft_verify_ex": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I32,
+                                   _P]),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -463,8 +465,8 @@ def moe_draft_verify(target, draft, cu_draft, ids, u, u_draw, out_ids, out_len, 
     if out_ids.dtype is not i32 or out_ids.dim() != 2 or out_ids.size(0) != B or not out_ids.is_contiguous():
         raise ValueError(f"moe_draft_verify: out_ids is packed int32 [{B}][max_draft + 1]")
     # the stride of a single row is not used, and may be any number
-    _check(lib().moe_draft_verify(B, V, out_ids.size(1) - 1, F32 if dtype is f32 else BF16, target.data_ptr(),
-                                  target_ld if rows > 1 else V, q, draft_ld if N > 1 else V, cu_draft.data_ptr(),
-                                  ids.data_ptr() if N else None, u.data_ptr() if N else None, u_draw.data_ptr(),
-                                  out_ids.data_ptr(), out_len.data_ptr(), _ptr(err_flag), max_ctas, _stream(stream)),
-           "moe_draft_verify")
+    _check(lib().moe_draft_verify_ex(B, N, V, out_ids.size(1) - 1, F32 if dtype is f32 else BF16, target.data_ptr(),
+                                     target_ld if rows > 1 else V, q, draft_ld if N > 1 else V, cu_draft.data_ptr(),
+                                     ids.data_ptr() if N else None, u.data_ptr() if N else None, u_draw.data_ptr(),
+                                     out_ids.data_ptr(), out_len.data_ptr(), _ptr(err_flag), max_ctas,
+                                     _stream(stream)), "moe_draft_verify")

@@ -131,7 +131,15 @@ moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t
                             int64_t target_ld, const void* draft, int64_t draft_ld, const int32_t* cu_draft,
                             const int32_t* ids, const float* u, const float* u_draw, int32_t* out_ids,
                             int32_t* out_len, int32_t* err_flag, int32_t max_ctas, moe_stream_t stream) {
-    if (B < 0 || vocab <= 0 || max_draft < 0 || target_ld < vocab || (draft && draft_ld < vocab))
+    return moe_draft_verify_ex(B, INT32_MAX, vocab, max_draft, dtype, target, target_ld, draft, draft_ld, cu_draft, ids, u,
+                               u_draw, out_ids, out_len, err_flag, max_ctas, stream);
+}
+
+moe_status moe_draft_verify_ex(int32_t B, int32_t N, int32_t vocab, int32_t max_draft, int32_t dtype, const void* target,
+                               int64_t target_ld, const void* draft, int64_t draft_ld, const int32_t* cu_draft,
+                               const int32_t* ids, const float* u, const float* u_draw, int32_t* out_ids,
+                               int32_t* out_len, int32_t* err_flag, int32_t max_ctas, moe_stream_t stream) {
+    if (B < 0 || N < 0 || vocab <= 0 || max_draft < 0 || target_ld < vocab || (draft && draft_ld < vocab))
         return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
     if (vocab > (1 << 23) || max_draft > 255) return MOE_ERR_UNSUPPORTED;
@@ -139,7 +147,7 @@ moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t
     if (!target || !cu_draft || !u_draw || !out_ids || !out_len) return MOE_ERR_INVALID_ARG;
     const uintptr_t el = dtype == MOE_F32 ? 4 : 2;
     if (!aligned_to(target, el) || !aligned_to(draft, el)) return MOE_ERR_ALIGNMENT;
-    return cuda_status(launch_draft_verify(B, vocab, max_draft, dtype == MOE_F32, target, target_ld, draft, draft_ld,
+    return cuda_status(launch_draft_verify(B, N, vocab, max_draft, dtype == MOE_F32, target, target_ld, draft, draft_ld,
                                            cu_draft, ids, u, u_draw, out_ids, out_len, err_flag,
                                            grid_cap_any(max_ctas), (cudaStream_t)stream));
 }

@@ -25,6 +25,7 @@ constexpr int kSegs = kCluster * kWarps;
 struct VerifyParams {
     int V, max_draft;
     int most;  // drafted tokens a request may have: max_draft, or 0 where there are no ids
+    int N;     // rows of drafted tokens that there are
     const void* target;
     int64_t target_ld;
     const void* draft;  // or null: q is 1 at the drafted token
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 8) __cluster_dims__(kCluster, 1, 1)
     // every CTA of a cluster walks the same requests: the cluster barriers below pair up
     for (int b = blockIdx.x / kCluster; b < B; b += gridDim.x / kCluster) {
         const int first = p.cu[b], n = p.cu[b + 1] - first;
-        const bool ok = first >= 0 && n >= 0 && n <= p.most;
+        const bool ok = first >= 0 && n >= 0 && n <= p.most && first <= p.N - n;
         if (warp == 0) {  // how many drafted tokens are kept, and whether an id is out of range
             int c = 0, bad = 0;
             for (int i0 = 0; ok && i0 < n; i0 += 32) {
@@ -282,11 +283,12 @@ __global__ void __launch_bounds__(kThreads, 8) __cluster_dims__(kCluster, 1, 1)
 
 }  // namespace
 
-cudaError_t launch_draft_verify(int B, int V, int max_draft, bool f32, const void* target, int64_t target_ld,
+cudaError_t launch_draft_verify(int B, int N, int V, int max_draft, bool f32, const void* target, int64_t target_ld,
                                 const void* draft, int64_t draft_ld, const int32_t* cu, const int32_t* ids,
                                 const float* u, const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err,
                                 int grid_cap, cudaStream_t st) {
-    VerifyParams p{V, max_draft, ids && u ? max_draft : 0, target, target_ld, draft, draft_ld, cu, ids, u, u_draw, out_ids, out_len, err};
+    VerifyParams p{V,  max_draft, ids && u ? max_draft : 0, N, target, target_ld, draft, draft_ld, cu, ids, u, u_draw,
+                   out_ids, out_len, err};
     // 16 bytes a load where every row starts on such a boundary and ends on one
     const int64_t lds = target_ld | (draft ? draft_ld : 0) | V;
     const bool vec = lds % (f32 ? 4 : 8) == 0 && aligned16(target) && aligned16(draft);

@@ -158,7 +158,7 @@ size_t attn_workspace_bytes();
 cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_cap, cudaStream_t st);
 
 // draft_verify.cu
-cudaError_t launch_draft_verify(int B, int V, int max_draft, bool f32, const void* target, int64_t target_ld,
+cudaError_t launch_draft_verify(int B, int N, int V, int max_draft, bool f32, const void* target, int64_t target_ld,
                                 const void* draft, int64_t draft_ld, const int32_t* cu, const int32_t* ids,
                                 const float* u, const float* u_draw, int32_t* out_ids, int32_t* out_len, int32_t* err,
                                 int grid_cap, cudaStream_t st);

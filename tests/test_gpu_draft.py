@@ -142,6 +142,42 @@ def test_too_many_drafts_for_a_row():
     assert int(err.item()) == 7 and n[0].item() == 0 and out[0].tolist() == [-1, -1, -1] and n[1].item() in (1, 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_past_the_inputs_are_not_read(dtype):
+    """cu_draft beyond the rows that there are (here: parts of larger buffers): those requests are refused, the
+    others are not touched by it."""
+    lens = [2, 1, 3, 1]
+    t, d, ids, u, ud = batch(lens, 200, 5)
+    dev = lambda a, ty: torch.tensor(np.asarray(a), dtype=ty, device=DEV)
+    f = torch.float32
+    full = dev(t, dtype), dev(d, dtype), dev(ids, torch.int32), dev(u, f), dev(ud, f)
+    cut = lambda n: (full[0][:n + 4], full[1][:n], full[2][:n], full[3][:n], full[4])
+
+    def call(n, cu):
+        out = torch.full((4, 4), 55, dtype=torch.int32, device=DEV)
+        length = torch.full((4,), 55, dtype=torch.int32, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        a = cut(n)
+        B.moe_draft_verify(a[0], a[1], dev(cu, torch.int32), a[2], a[3], a[4], out, length, err_flag=err)
+        return out.tolist(), length.tolist(), int(err.item())
+
+    out, length, err = call(7, [0, 2, 3, 6, 7])
+    assert err == 0 and min(length) >= 1
+    for n, refused in ((6, [3]), (5, [2, 3]), (2, [1, 2, 3])):
+        o, ln, e = call(n, [0, 2, 3, 6, 7])
+        assert e == 7
+        for b in range(4):
+            if b in refused:
+                assert ln[b] == 0 and o[b] == [-1] * 4
+            else:
+                assert (o[b], ln[b]) == (out[b], length[b])
+    # a descending one, and one that starts past the end
+    _, ln, e = call(7, [0, 9, 3, 6, 7])
+    assert e == 7 and ln[:2] == [0, 0] and ln[2:] == length[2:]
+    _, ln, e = call(7, [0, 2, 2**31 - 1, 2**31 - 1, -2**31])
+    assert e == 7 and ln[0] == length[0] and ln[1:] == [0, 0, 0]
+
+
 def test_distribution():
     """Kept and drawn tokens together follow the target: 40000 trials over 12 tokens, a chi-squared
     statistic of 11 degrees below 45 (probability of more: 5e-6)."""

@@ -132,6 +132,13 @@ def test_verify_arguments(P):
     assert v(mis=2) == ALIGNMENT
 
 
+def test_verify_with_a_row_count(P):
+    """moe_draft_verify_ex refuses a negative count, and otherwise what moe_draft_verify refuses."""
+    v = lambda N=3, V=100: B.lib().moe_draft_verify_ex(1, N, V, 3, B.F32, P(), 100, P(), 100, P(), P(), P(), P(), P(), None,
+                                                       None, 0, None)
+    assert v(N=-1) == v(V=0) == v() == INVALID  # the last: no out_len
+
+
 def test_the_binding_checks_tensors():
     z = torch.zeros
     bf, i32 = torch.bfloat16, torch.int32
