@@ -522,7 +522,10 @@ MOE_API moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args
  * token is the lowest v with w_0 + .. + w_v > floor(floor(2^24 * u) * W / 2^24), W the sum
  * over all v (at most 2^64 - 1 for vocab <= 2^23).  If W is 0 (p and q equal, or not finite)
  * the token is drawn from p_c; if that has no mass either, it is -1 and MOE_ERR_BAD_INDEX
- * is set.  The result is distributed as the target's own tokens for uniform u in [0, 1).
+ * is set.  The result is distributed as the target's own tokens for uniform u in [0, 1), as far as 24 bits of
+ * u_draw reach: of the 2^24 numbers that it can be, each stands for a share of 2^-24 of the sum and goes to
+ * the token at the start of that share, so a token's probability is off by less than 2^-24, and a token whose
+ * share is smaller may never be drawn.
  * target   device [cu_draft[B] + B][target_ld]: rows cu_draft[b] + b + i, i = 0 .. n; fp32 or
  *          bf16 by `dtype`.
  * draft    device [cu_draft[B]][draft_ld], the same type; or NULL: the draft was

@@ -178,6 +178,26 @@ def test_rows_past_the_inputs_are_not_read(dtype):
     assert e == 7 and ln[0] == length[0] and ln[1:] == [0, 0, 0]
 
 
+def test_every_number_of_the_draw():
+    """All 2^24 values of u_draw over one distribution of 300 tokens: how often a token comes is its
+    probability times 2^24, within one: those smaller than 2^-24 come once or never."""
+    V, n = 300, 1 << 24
+    p = softmax(np.random.default_rng(5).standard_normal((1, V)) * 6).astype(np.float32)
+    assert (p < 2.0**-24).sum() > 20
+    step = 1 << 20
+    t = torch.tensor(p, device=DEV).repeat(step, 1)
+    got = torch.zeros(V, dtype=torch.int64, device=DEV)
+    out = torch.empty(step, 1, dtype=torch.int32, device=DEV)
+    length = torch.empty(step, dtype=torch.int32, device=DEV)
+    cu = torch.zeros(step + 1, dtype=torch.int32, device=DEV)
+    for a in range(0, n, step):
+        u = torch.arange(a, a + step, device=DEV).float() * 2.0**-24
+        B.moe_draft_verify(t, None, cu, None, None, u, out, length)
+        got += torch.bincount(out[:, 0].long(), minlength=V)
+    w = np.floor(p[0].astype(np.float64) * 2.0**40)
+    assert np.abs(got.cpu().numpy() - w / w.sum() * n).max() < 1.0
+
+
 def test_distribution():
     """Kept and drawn tokens together follow the target: 40000 trials over 12 tokens, a chi-squared
     statistic of 11 degrees below 45 (probability of more: 5e-6)."""
