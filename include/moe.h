@@ -500,7 +500,8 @@ typedef struct {
     int32_t window;             /* 0 = none */
     int32_t* err_flag;          /* device int32 or NULL */
     void* workspace;            /* moe_attn_workspace_size bytes, 256-byte aligned.  Zero it once */
-    size_t workspace_bytes;     /* before its first use; every call leaves it ready for the next */
+    size_t workspace_bytes;     /* before its first use; every call leaves it ready for the next, */
+                                /* one that reports MOE_ERR_TIMEOUT too */
 } moe_attn_args;
 
 /* err_flag: MOE_ERR_BAD_INDEX for a page outside the pool (its tokens read as zeros), a
@@ -558,7 +559,7 @@ MOE_API moe_status moe_draft_verify_ex(int32_t B, int32_t N, int32_t vocab, int3
  * wait, limited to timeout_ns, on a barrier that nothing ever completes, before it
  * issues any copy: the wait runs out, the kernel stores MOE_ERR_TIMEOUT in err_flag,
  * skips its work, frees its tensor memory and returns normally, so the context stays
- * usable.  The attention kernels do the same.  The staged combine kernel takes the same
+ * usable.  So does the first CTA of an attention kernel, while the others do their work.  The staged combine kernel takes the same
  * path (its error goes to the layer's err_flag, or, called on its own, to the word
  * moe_comm_error reads).
  * enable = 0 (the default) turns it off.  Process-wide, host-side only;

@@ -314,14 +314,22 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
     }
     __syncthreads();
     pdl_begin();
-    if (p.inject_ns > 0) {  // test hook: the failure path of a bounded wait
+    locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
+    // one thread: counts a part that this CTA gives up, as if it had been stored
+    auto let_go = [&](const Item& it) {
+        if (it.whole) return;
+        const Parts parts = parts_of(p, it, start);
+        int last;
+        last_of(p.counters + parts.last, parts.last - parts.first + 1, 0, &last, [] {});
+    };
+    if (p.inject_ns > 0 && blockIdx.x == 0) {  // test hook: the failure path of a bounded wait
         if (threadIdx.x == 0) {
             tc::wait_on_nothing(never, (uint64_t)p.inject_ns);
             set_err(p.err, MOE_ERR_TIMEOUT);
+            for (Cursor cur = cursor(start); more(cur);) let_go(take(p, cur));
         }
         return;
     }
-    locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
     // a wait that runs out is reported and then passed, here and in every later wait, so that
     // each barrier is still met; the results are void
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -349,7 +357,16 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                     loads.load(p, it, 0);
                 }
                 // not cut short by an abort: the consumers meet for every query tile
-                if (n >= C::kInfos && !tc::mbar_wait_bounded(&info_empty[buf], (n / C::kInfos - 1) & 1)) break;
+                if (n >= C::kInfos && !tc::mbar_wait_bounded(&info_empty[buf], (n / C::kInfos - 1) & 1)) {
+                    // the consumers are told that there is no more, and the parts left are counted
+                    set_err(p.err, MOE_ERR_TIMEOUT);
+                    *abort = 1;
+                    if (lane == 0) {
+                        if (!stop) let_go(it);
+                        while (more(cur)) let_go(take(p, cur));
+                    }
+                    stop = true;
+                }
                 __syncwarp();
                 if (stop) {
                     if (lane == 0) info->stop = 1;
@@ -451,7 +468,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
         const int buf = n % C::kInfos;
         const Info* info = reinterpret_cast<const Info*>(infos + buf * C::kInfoBytes);
         const uint32_t q_addr = tc::smem_u32(info) + C::kInfoBytes - C::kRows * C::kQStride + rg * 8 * kNT * C::kQStride;
-        if (!tc::mbar_wait_bounded(&info_full[buf], (n / C::kInfos) & 1)) {
+        // (twice as long as the warp that fills it may wait before it says that there is no more)
+        if (!tc::mbar_wait_bounded(&info_full[buf], (n / C::kInfos) & 1) &&
+            !tc::mbar_wait_bounded(&info_full[buf], (n / C::kInfos) & 1)) {
             set_err(p.err, MOE_ERR_TIMEOUT);
             *abort = 1;
             return;  // every consumer waits here, and none past it

@@ -304,6 +304,15 @@ __device__ void join(const Params& p, const Item& it, const Start& st, const Row
         join_row<kD, true>(p, parts, parts.first, step, members, at, r);
 }
 
+// One thread: counts the parts of a CTA that gives up, as if they had been stored.
+template <int kD>
+__device__ __noinline__ void let_go(const Params& p, const Start& st, int* flag) {
+    for (Cursor cur = cursor(st); more(cur);) {
+        const Item it = take(p, cur);
+        if (!it.whole) join<kD>(p, it, st, RowAt{0, 0}, 0, false, flag, [] {});
+    }
+}
+
 template <int kD, bool kFp8>
 __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
@@ -371,13 +380,6 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     }
     __syncthreads();
     pdl_begin();
-    if (p.inject_ns > 0) {  // test hook: the failure path of a bounded wait
-        if (threadIdx.x == 0) {
-            tc::wait_on_nothing(never, (uint64_t)p.inject_ns);
-            set_err(p.err, MOE_ERR_TIMEOUT);
-        }
-        return;
-    }
     if (warp == kMmaWarp) {
         tc::tmem_alloc(&tmem_s, 512);
         tc::tmem_relinquish();
@@ -386,6 +388,16 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
     locate<C::kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
     tc::tc_fence_after();
     const uint32_t tmem = tmem_s;
+    if (p.inject_ns > 0 && blockIdx.x == 0) {  // test hook: the failure path of a bounded wait
+        if (threadIdx.x == 0) {
+            tc::wait_on_nothing(never, (uint64_t)p.inject_ns);
+            set_err(p.err, MOE_ERR_TIMEOUT);
+            let_go<kD>(p, start, &last_s);
+        }
+        __syncthreads();
+        if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+        return;
+    }
     Cursor cur = cursor(start);
     if (threadIdx.x == 0 || threadIdx.x == 128) cursors[threadIdx.x >> 7] = cur;
     __syncthreads();
