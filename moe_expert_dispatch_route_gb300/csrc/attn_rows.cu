@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
         }
         const int box_keys = min(p.page_size, kKeyTile), npg = kKeyTile / box_keys;
         int stage = 0;
-        uint32_t turn = 0;
+        uint32_t turn = 0, sent = 0;
         bool more_now = more(cur);
         Item it, after;
         Pages pages, pages_after;
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want)) * (box_keys * C::kRowBytes);
                 if (turn > 0) wait(&empty[2 * stage + role], (turn - 1) & 1);
                 if (!*abort) {
+                    ++sent;
                     if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
                     __syncwarp();
                     if (want)
@@ -452,9 +453,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8, kNT, kRW>::kThreads, 1)
             }
         }
         if (*abort)  // copies still in flight land (or a bounded wait gives up) before the CTA ends
-            for (int i = 0; i < 2 * C::kStages; ++i) {
-                const uint32_t issued = turn + (i / 2 < stage ? 1 : 0);
-                if (issued > 0 && i % 2 == role) tc::mbar_wait_bounded(&full[i], (issued - 1) & 1);
+            for (int i = 0; i < C::kStages; ++i) {
+                const uint32_t times = (sent + C::kStages - 1 - i) / C::kStages;  // that stage i has been copied to
+                if (times > 0) tc::mbar_wait_bounded(&full[2 * i + role], (times - 1) & 1);
             }
         return;
     }

@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
         if (warp == kCopyWarp) {
             // -------------------------------------------------------- copies
             int e = 0;
-            uint32_t turn = 0, items = 0;
+            uint32_t turn = 0, items = 0, sent = 0, q_sent = 0;
             const int box_keys = min(p.page_size, kKeyTile), npg = kKeyTile / box_keys;
             constexpr int kBoxes = kFp8 ? 1 : C::kCols;  // column blocks of a K or V tile as copied
             constexpr int kRing = kFp8 ? C::kRaw : C::kEntries;
@@ -444,7 +444,9 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                 }
                 const Halves v = halves(p, it);
                 if (items > 0) wait(q_empty, (items - 1) & 1);
-                if (!*abort && lane == 0) {
+                const bool go = !*abort;
+                if (go) ++q_sent;
+                if (go && lane == 0) {
                     const int count = it.tokens > half_tokens ? 2 : 1;
                     tc::mbar_arrive_expect_tx(q_full, count * C::kCols * half_tokens * p.group * 128);
                     for (int h = 0; h < count; ++h)
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                         if (kFp8 && want && !scaled)  // a page outside the pool: its tokens read as zeros
                             for (int i = 0; i < box_keys; ++i) scales[e * kKeyTile + pg * box_keys + i] = 0;
                         if (!*abort) {
+                            ++sent;
                             __syncwarp();
                             if (lane == 0) tc::mbar_arrive_expect_tx(&to_full[e], bytes);
                             __syncwarp();
@@ -501,17 +504,17 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     if (k == 0) ahead();
                 }
             }
+            if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
+                for (int i = 0; i < kRing; ++i) {
+                    const uint32_t times = (sent + kRing - 1 - i) / kRing;  // that entry i has been copied to
+                    if (times > 0) tc::mbar_wait_bounded(&to_full[i], (times - 1) & 1);
+                }
+                if (q_sent > 0) tc::mbar_wait_bounded(q_full, (q_sent - 1) & 1);
+            }
             if (turn > 0) wait(&to_empty[e], (turn - 1) & 1);
             if (lane == 0) {
                 (kFp8 ? raw_cmds : cmds)[e] = kStop;
                 tc::mbar_arrive(&to_full[e]);
-            }
-            if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
-                for (int i = 0; i < kRing; ++i) {
-                    const uint32_t issued = turn + (i < e ? 1 : 0);
-                    if (issued > 0) tc::mbar_wait_bounded(&to_full[i], (issued - 1) & 1);
-                }
-                if (items > 0) tc::mbar_wait_bounded(q_full, (items - 1) & 1);
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMAs
