@@ -484,7 +484,8 @@ typedef struct {
     void* o;                    /* device bf16 (out), likewise */
     float* lse;                 /* device fp32 [T][num_q_heads] (out) or NULL */
     /* elements; rows 16-byte aligned, of the cache's head_dim.  o's rows lie apart from each other
-     * (else MOE_ERR_INVALID_ARG); a stride that is used is below 2^39 (MOE_ERR_UNSUPPORTED) */
+     * (else MOE_ERR_INVALID_ARG); a stride that is used is below 2^39 (MOE_ERR_UNSUPPORTED); q's may be
+     * 0: tokens or heads that share their rows */
     int64_t q_ld, q_head_stride, o_ld, o_head_stride;
     const int32_t* cu_q;        /* device int32 [B+1], not decreasing, cu_q[0] = 0, cu_q[B] <= T */
     const int32_t* kv_len;      /* device int32 [B] */

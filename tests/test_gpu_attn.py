@@ -347,3 +347,18 @@ def test_a_bounded_wait_that_runs_out(n):
     assert int(c.err.item()) == 8
     c.err.zero_()
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens", [[1, 3], [150, 33, 1]])
+@pytest.mark.parametrize("shared", ["heads", "tokens", "both"])
+def test_shared_query_rows(dtype, D, q_lens, shared):
+    """q with a stride of 0: one row for all heads of a token, for all tokens, or for everything."""
+    c = Case(q_lens, [300, 200, 64][:len(q_lens)], Hq=12, H=2, D=D, dtype=dtype)
+    one = c.qd[:1 if shared != "heads" else None, :1 if shared != "tokens" else None].clone()
+    c.qd = one.expand(*c.qd.shape)
+    assert 0 in c.qd.stride()[:2]
+    c.q = c.qd.cpu()
+    c.args = c.make_args()
+    c.check()
