@@ -362,3 +362,53 @@ def test_shared_query_rows(dtype, D, q_lens, shared):
     c.q = c.qd.cpu()
     c.args = c.make_args()
     c.check()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("order", ["hnd", "nhd", "head first"])
+def test_chunks_in_pages_and_orders(page, dtype, order):
+    Case([70, 150, 1], [300, 513, 700], page=page, dtype=dtype, order=order, q_pad=3).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("requests", [40, 600])
+def test_chunks_of_many_requests(dtype, requests):
+    """More requests than a warp's lanes, and than the CTA's threads: with several query tiles, with one, with no row
+    and with rows that stand before the first token."""
+    rng = np.random.default_rng(requests)
+    q = rng.choice([0, 1, 5, 40, 90], size=requests, p=[0.2, 0.3, 0.3, 0.15, 0.05])
+    q[0], q[requests // 2], q[-1] = 200, 0, 150
+    kv = [int(n + rng.integers(0, 60)) if rng.random() < 0.9 else int(rng.integers(0, n + 1)) for n in q]
+    Case([int(n) for n in q], kv, Hq=4, H=1, D=64, dtype=dtype).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [4, 1, 3], [40, 200, 1]])
+@pytest.mark.parametrize("window", [1, 5, 128, 150])
+def test_windows_of_64_columns(dtype, q_lens, window):
+    Case(q_lens, [300, 700, 129], D=64, window=window, dtype=dtype).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("bad", [-1, 10**6])
+def test_pages_outside_the_pool_read_as_zeros(dtype, D, n, bad):
+    """A page outside the pool sets the error flag, and its tokens have keys and values of 0."""
+    c = Case([n, n], [200, 300], D=D, dtype=dtype)
+    c.table[0, 2] = bad
+    c.k[0][32:48] = 0
+    c.v[0][32:48] = 0
+    c.run()
+    assert int(c.err.item()) == 7
+    c.err.zero_()
+    run = c.run
+
+    def no_error():
+        out = run()
+        c.err.zero_()
+        return out
+
+    c.run = no_error
+    c.check()
