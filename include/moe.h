@@ -469,8 +469,9 @@ MOE_API moe_status moe_kv_read(const moe_kv_cache* cache, int32_t B, int32_t T, 
  * lse = -inf.  What lies in tokens that no row of the request sees -- the rest of the last
  * page, pages before the window -- never reaches a result, whatever it holds.  (A NaN or an
  * infinity in a value that some of its rows see may make others of its rows NaN.)  Scores, the softmax's
- * maximum and sum, and o are held in fp32 (scores past 2^24 are told apart no longer), o is rounded once
- * at the end.  The probabilities are rounded for the second product, and the sum takes them before that:
+ * maximum and sum, and o are held in fp32 (scores past 2^24 are told apart no longer; the sum that o is
+ * divided from takes probabilities up to 2^8, so a bf16 cache's values are to be below about 2^100), o is
+ * rounded once at the end.  The probabilities are rounded for the second product, and the sum takes them before that:
  *   bf16 cache  to bf16
  *   e4m3 cache  to fp16, where the values' scales lie within 2^12 of the request's smallest: what a key adds to o
  *               is off by 2^-11 of itself, or by 2^-20 of a value at that smallest scale for a key of little

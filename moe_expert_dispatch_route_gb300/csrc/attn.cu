@@ -66,7 +66,8 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_
     // Few rows are bound by reading the cache, on mma.sync; many on tcgen05, whose tiles have 128
     // rows whether they are filled or not.  32 requests of up to 8191 tokens, 8 heads of 128 (64),
     // bf16, rows a head: 32: 97 us against 113 there (63 against 96), 64: 161 against 113 (118
-    // against 96); e4m3: 32: 129 against 147, 64: 189 against 148.
+    // against 96); e4m3: 32: 129 against 147, 64: 189 against 148.  One rule for the whole call: one chunk of 512
+    // tokens beside 127 single tokens takes 258 us here, 45 + 178 as two calls (e4m3: 354, 57 + 100).
     const int64_t rows = (int64_t)a.max_q * p.group;
     return rows <= kFewRows ? launch_rows(c, p, (int)rows, grid_cap, st) : launch_tiles(c, p, grid_cap, st);
 }

@@ -28,10 +28,10 @@
 // 2^8).  The quotient o / sum does not depend on the reference point.  With 16 rows a warp
 // the exact maximum of one of them moved with almost every chunk, and o with it.
 //
-// Measured: 128 requests of up to 16384 bf16 tokens, 32 / 4 heads of 128, 288 us (6.8 TB/s); 96 of up
-// to 20001 e4m3 tokens, 64 / 8 heads, 311 us (6.5 TB/s); drafts of 30 rows over a 4096 window, 8 heads
-// of 64, 51 us (4.3 TB/s: start, joins and the consumers' latency); one request of 777 tokens 7.8 us,
-// a chain of dependent loads and barriers.
+// Measured: 128 requests of up to 16384 bf16 tokens, 32 / 4 heads of 128, 285-289 us (6.8 TB/s); 96 of up
+// to 20001 e4m3 tokens, 64 / 8 heads, 304-313 us (6.5 TB/s; with scales 2^40 apart everywhere 377); drafts of
+// 30 rows over a 4096 window, 8 heads of 64, 52 us (4.2 TB/s: start, joins and the consumers' latency; e4m3
+// 62); one request of 777 tokens 7.8 us, a chain of dependent loads and barriers.
 #include "attn.cuh"
 
 #include <type_traits>

@@ -14,8 +14,8 @@
 // in part; a pair of tiles (both halves, 128 keys, head_dim 128) takes 3400 cycles.  Its 32 MMAs
 // last 2070 (64.7 each), during which they read 192 KB of operands and the copies write 64 KB at
 // 128 bytes a cycle, 2048: shared memory is as busy as the tensor cores, which stretches them to
-// 2450.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1120 us, 1470 TFLOP/s (64 columns:
-// 977 us, bound by the softmax, which is the same for half the products).
+// 2450.  8192 rows over 16384 tokens, 32 / 4 heads of 128, bf16: 1100-1165 us from box to box, 1420-1500
+// TFLOP/s (64 columns: 974 us for half the products; the softmax is the same).
 //
 // The running maximum is followed loosely: o and the sum stay relative to an older maximum
 // until a row's new one is 2^8 times as large (in the probabilities), and only then are they
@@ -32,7 +32,7 @@
 //   p   2^7 p
 // A tile whose scales lie elsewhere holds the codes as they are: its scores are multiplied by 2^s and its part
 // of o is added up in fp32 by the softmax's threads, several times as long.
-// The same chunk takes 1412 us: the conversion shares shared memory and issue slots with the rest
+// The same chunk takes 1456 us: the conversion shares shared memory and issue slots with the rest
 // (left out, when this took 1540, it left 1250).
 //
 //   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row; e4m3: its row of Q too)

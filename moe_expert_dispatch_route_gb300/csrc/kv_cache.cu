@@ -20,7 +20,7 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // The e4m3 form is bound by issue slots before it is by HBM, so its scale comes from the bits of
 // the largest bf16 magnitude and scaling is one product.
 // 16384 tokens of 8 heads of 128 into e4m3, 101 MB, in random slots: 21.4 us (4.7 TB/s; 20.2 without
-// the scales, which are single bytes); 64 tokens of 4 bf16 heads 1.5 us.
+// the scales, which are single bytes); into bf16, 134 MB, 22.3 us (6.0 TB/s); 64 tokens of 4 bf16 heads 1.5 us.
 constexpr int kUnroll = 4;
 
 template <int kLanes, bool kFp8>
