@@ -456,9 +456,9 @@ __device__ __forceinline__ int f16_row_exp(uint32_t mx) { return min(14 - ((int)
 // scale byte, ref a reference to which o refers as well.  In fp16 what a weight adds to o is off by 2^-11 of
 // itself or by 2^-32 of a value at the reference, whichever is more; so fp16 takes the keys whose
 // scales lie from the smallest one so far to 2^kNear above it, where the latter is 2^-20 of what any key
-// may add.  Keys with larger values, and those that come after much smaller ones were let go, take a way whose
-// weights keep their exponents: what a row gets from its keys does not depend on how large a value
-// beside them is, one that the row hardly weighs or does not see.
+// may add.  Keys with larger values (and all of them, once values 2^60 larger have held the reference up) take
+// a way whose weights keep their exponents: what a row gets from its keys does not depend on how
+// large a value beside them is, one that the row hardly weighs or does not see.
 constexpr int kPBits = 7;
 constexpr uint32_t kNear = 12;
 constexpr uint32_t kFarUp = 60;  // the most that a value's scale is above the reference: o stays in fp32's range
