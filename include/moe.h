@@ -14,7 +14,12 @@
  *
  *   moe_kv_write, moe_kv_read  a paged key/value cache (bf16, or e4m3 quantised as written)
  *   moe_attn_paged             attention of new tokens (one, a draft, a prompt chunk) over it
+ *   moe_attn_tree              the same for a tree of drafted tokens
  *   moe_draft_verify           drafted tokens against the target's probabilities
+ *   moe_latent_write           a paged cache of one latent vector a token
+ *   moe_attn_latent            attention over it, absorbed form (every head reads the latent vectors)
+ *   moe_attn_expanded          the same attention of prompts, keys and values of every head written out
+ *   moe_block_norm             norm, gate, residual and the next norm between two blocks
  *
  * The operations follow the problem statement of the vLLM Dual-Batch Overlap pages:
  *   [A] "[Core/DBO][1/N] Add Dual-Batch Overlap mechanism to VLLM", Purpose
@@ -515,6 +520,131 @@ MOE_API moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args
                                   moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * moe_attn_tree -- moe_attn_paged for new tokens that are a tree of drafts: several continuations
+ * of each request, verified in one pass.  The request's n new tokens are the last n of its kv_len cached
+ * tokens (written with moe_kv_write in any order of the tree's nodes, a slot each); its new token i sees
+ *   every token before the new ones, itself, and new token j where bit j of tree[cu_q[b] + i] is set
+ * (its ancestors, for a tree; any set will do).  Bits from n on count for nothing.  Everything else is as
+ * for moe_attn_paged; what a sibling holds is multiplied by zero, so it has to be finite.
+ * tree     device uint64 [T].  A request has at most 64 new tokens (max_q <= 64, else
+ *          MOE_ERR_UNSUPPORTED); args->causal is 1 and args->window 0 (else MOE_ERR_INVALID_ARG). */
+MOE_API moe_status moe_attn_tree(const moe_kv_cache* cache, const moe_attn_args* args, const uint64_t* tree,
+                                 int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged cache for latent attention (the DeepSeek-V3 and -V2-Lite shapes): a token has one latent vector c
+ * of 512 numbers, from which every head's key and value are projected, and one rotary key of 64 that all heads
+ * share, side by side.
+ *   kv       device, element (page, token, d) at page*stride_page + token*stride_token + d (in
+ *            elements): c at d < latent, the rotary key behind it.  Strides and pool are multiples of 16
+ *            bytes (MOE_ERR_ALIGNMENT).
+ *   dtype    MOE_BF16 (else MOE_ERR_UNSUPPORTED).
+ * latent is 512, rope 64, page_size a power of two >= 16; else MOE_ERR_UNSUPPORTED. */
+typedef struct {
+    void* kv;
+    int32_t dtype; /* moe_dtype */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t latent;
+    int32_t rope;
+    int64_t stride_page;
+    int64_t stride_token;
+} moe_latent_cache;
+
+/* ---------------------------------------------------------------------------
+ * moe_latent_write -- stores T tokens' latent vectors and rotary keys into their slots, the latent
+ * vectors normed on the way where a weight w is given:
+ *   c'_d = c_d * w_d / sqrt(mean(c^2) + eps)      in fp32, rounded once
+ * c, k_rope device bf16: token t at t*ld_c, t*ld_rope (elements), so both may be parts of one
+ *          projection's output; 16-byte aligned rows.
+ * weight   device bf16 [latent] or NULL (c is stored as it is).  eps >= 0.
+ * slots    device int64 [T]: page*page_size + offset of each token, all different.  A
+ *          negative slot is skipped (padding); one past the pool sets MOE_ERR_BAD_INDEX.
+ * err_flag device int32 or NULL. */
+MOE_API moe_status moe_latent_write(const moe_latent_cache* cache, int32_t T, const void* c, int64_t ld_c,
+                                    const void* k_rope, int64_t ld_rope, const void* weight, float eps,
+                                    const int64_t* slots, int32_t* err_flag, int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_attn_latent -- latent attention in its absorbed form: q has been multiplied by each head's key
+ * projection (a matrix product upstream), so that every head's scores are products with the cached numbers
+ * themselves, and o is what each head's value projection is applied to downstream.
+ *   s_j = scale * q . [c_j, rope_j]  (576 numbers)   o = sum_j softmax(s)_j c_j  (512)   lse = ln sum_j e^(s_j)
+ * over the tokens j that the row sees: as for moe_attn_paged, or as for moe_attn_tree where tree is
+ * given (same conditions).  args is moe_attn_paged's: q [T][num_q_heads][576], o [T][num_q_heads][512],
+ * num_q_heads from 1 to 128 (else MOE_ERR_UNSUPPORTED), rows, lengths, table, bounds, empty rows, err_flag and
+ * workspace (of moe_attn_latent_workspace_size bytes) as there.  Scores, the softmax's maximum and sum, and o
+ * are held in fp32, the probabilities rounded to bf16 for the second product (the sum takes them before), o
+ * rounded once at the end.  The cached numbers are to be below about 2^100. */
+MOE_API size_t moe_attn_latent_workspace_size(const moe_latent_cache* cache, int32_t num_q_heads);
+MOE_API moe_status moe_attn_latent(const moe_latent_cache* cache, const moe_attn_args* args, const uint64_t* tree,
+                                   int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_attn_expanded -- latent attention in its expanded form, for prompts: keys and values of every head
+ * have been projected from the latent vectors (a matrix product upstream).  3.4 times fewer operations a
+ * pair of tokens than the absorbed form, for 2 * 256 bytes more a key and head.
+ *   s_j = scale * (q_n . k_j + q_r . rope_j)      q = [q_n, q_r] (128 + 64 numbers)
+ *   o   = sum_j softmax(s)_j v_j  (128),   lse = ln sum_j e^(s_j)
+ * Request b has query rows cu_q[b] .. and keys cu_kv[b] .. of k, k_rope and v; with n and m of them, its row i
+ * stands at position p = m - n + i and sees keys j < m, and j <= p if causal.  (Keys before the rows': a prefix
+ * expanded again, or in an earlier part of the prompt.)  A row that sees no key gets o = 0 and lse = -inf.  Precision as for
+ * moe_attn_latent; a NaN or an infinity in a key's value may make any row of its request NaN that shares
+ * a tile of 128 keys with it, and no row of another request. */
+typedef struct {
+    const void* q;      /* device bf16 [T][num_heads][192]: head h of row t at t*q_ld + h*q_head_stride */
+    const void* k;      /* device bf16 [S][num_heads][128], likewise */
+    const void* k_rope; /* device bf16 [S][64]: row t at t*rope_ld */
+    const void* v;      /* device bf16 [S][num_heads][128] */
+    void* o;            /* device bf16 [T][num_heads][128] (out) */
+    float* lse;         /* device fp32 [T][num_heads] (out) or NULL */
+    /* elements; rows 16-byte aligned.  Those of o lie apart from each other (else MOE_ERR_INVALID_ARG); a
+     * stride that is used is below 2^39 (MOE_ERR_UNSUPPORTED); the others may be 0 */
+    int64_t q_ld, q_head_stride, k_ld, k_head_stride, rope_ld, v_ld, v_head_stride, o_ld, o_head_stride;
+    const int32_t* cu_q;  /* device int32 [B+1], not decreasing, cu_q[0] = 0, cu_q[B] <= T */
+    const int32_t* cu_kv; /* device int32 [B+1], likewise, cu_kv[B] <= S */
+    int32_t T;            /* rows of q and o, at most 2^30 */
+    int32_t S;            /* rows of k, k_rope and v, at most 2^30 */
+    int32_t B;            /* requests, at most 8192 */
+    int32_t max_q;        /* upper bounds of the requests' rows and keys; they size the launch, and a */
+    int32_t max_kv;       /* request above one sets MOE_ERR_BAD_INDEX (its rows are not written) */
+    int32_t num_heads;
+    float scale;          /* > 0 */
+    int32_t causal;       /* 0 or 1 */
+    int32_t* err_flag;    /* device int32 or NULL */
+    void* workspace;      /* moe_attn_expanded_workspace_size bytes, as moe_attn_paged's */
+    size_t workspace_bytes;
+} moe_attn_expanded_args;
+MOE_API size_t moe_attn_expanded_workspace_size(int32_t num_heads);
+MOE_API moe_status moe_attn_expanded(const moe_attn_expanded_args* args, int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_block_norm -- what stands between two blocks: a block's output y is normed (post_weight), gated
+ * and scaled, added to the residual, and the next block's input is normed from the sum (pre_weight).
+ *   x  = y, or N(y; post_weight)            N(x; w)_d = x_d * w_d / sqrt(mean(x^2) + eps) over a row
+ *   r' = resid + scale * gate * x           (no resid: 0; no gate: 1)
+ *   out = N(r'; pre_weight)
+ * in fp32 from end to end, with one rounding each of r' and out (out is normed from r' before its rounding).
+ * resid_out may be resid, and out may be y; no other two buffers overlap. */
+typedef struct {
+    const void* y;           /* device [T][hidden] of `dtype` */
+    const void* post_weight; /* device [hidden] of `dtype` or NULL: y is taken as it is */
+    const void* gate;        /* device [gate_rows][hidden] of `dtype` or NULL */
+    const void* resid;       /* device [T][hidden] of `resid_dtype` or NULL */
+    void* resid_out;         /* device [T][hidden] of `resid_dtype` (out) or NULL: r' is not kept */
+    const void* pre_weight;  /* device [hidden] of `dtype`, with out */
+    void* out;               /* device [T][hidden] of `dtype` (out) or NULL: no second norm */
+    int32_t T;
+    int32_t hidden;          /* a multiple of 8, at most 16384 (else MOE_ERR_UNSUPPORTED) */
+    int32_t dtype;           /* MOE_F32 or MOE_BF16 */
+    int32_t resid_dtype;     /* MOE_F32 or MOE_BF16 */
+    int32_t gate_rows;       /* 1: one row for all tokens, or T */
+    float scale;             /* finite */
+    float eps;               /* >= 0 */
+} moe_norm_args;
+MOE_API moe_status moe_block_norm(const moe_norm_args* args, int32_t max_ctas, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * moe_draft_verify -- speculative decoding's acceptance test.  Request b drafted
  * n = cu_draft[b+1] - cu_draft[b] tokens x_i from the draft's distributions q_i; the target's
  * distributions at these places and at the one after them are p_0 .. p_n.
@@ -561,7 +691,7 @@ MOE_API moe_status moe_draft_verify_ex(int32_t B, int32_t N, int32_t vocab, int3
  * wait, limited to timeout_ns, on a barrier that nothing ever completes, before it
  * issues any copy: the wait runs out, the kernel stores MOE_ERR_TIMEOUT in err_flag,
  * skips its work, frees its tensor memory and returns normally, so the context stays
- * usable.  So does the first CTA of an attention kernel, while the others do their work.  The staged combine kernel takes the same
+ * usable.  So does the first CTA (pair) of an attention kernel, while the others do their work.  The staged combine kernel takes the same
  * path (its error goes to the layer's err_flag, or, called on its own, to the word
  * moe_comm_error reads).
  * enable = 0 (the default) turns it off.  Process-wide, host-side only;

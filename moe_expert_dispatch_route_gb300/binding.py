@@ -72,6 +72,28 @@ class MoeAttnArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class MoeLatentCache(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("latent", ctypes.c_int32), ("rope", ctypes.c_int32),
+                ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64)]
+
+
+class MoeAttnExpandedArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "k_rope", "v", "o", "lse")] + \
+               [(n, ctypes.c_int64) for n in ("q_ld", "q_head_stride", "k_ld", "k_head_stride", "rope_ld", "v_ld",
+                                              "v_head_stride", "o_ld", "o_head_stride")] + \
+               [("cu_q", ctypes.c_void_p), ("cu_kv", ctypes.c_void_p), ("T", ctypes.c_int32), ("S", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("err_flag", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class MoeNormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("y", "post_weight", "gate", "resid", "resid_out", "pre_weight", "out")] + \
+               [(n, ctypes.c_int32) for n in ("T", "hidden", "dtype", "resid_dtype", "gate_rows")] + \
+               [("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 def config(hidden, inter, num_experts, num_shared, top_k, gate=GATE_SOFTMAX, renormalize=1,
            n_group=1, topk_group=1, routed_scale=1.0, dtype=BF16) -> MoeConfig:
     return MoeConfig(hidden, inter, num_experts, num_shared, top_k, gate, int(renormalize), n_group,
@@ -89,6 +111,7 @@ def config_of(wl) -> MoeConfig:
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CFG = ctypes.POINTER(MoeConfig)
 _CACHE = ctypes.POINTER(MoeKvCache)
+_LATENT = ctypes.POINTER(MoeLatentCache)
 _SIGS = {
     "moe_route": (_I32, [_CFG, _I32, _P, _P, _P, _P, _I32, _P]),
     "moe_route_hash": (_I32, [_CFG, _I32, _P, _P, _P, _I32, _P, _P, _I32, _P]),
@@ -120,6 +143,13 @@ _SIGS = {
     "moe_kv_read": (_I32, [_CACHE, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P]),
     "moe_attn_workspace_size": (_SZ, [_CACHE, _I32]),
     "moe_attn_paged": (_I32, [_CACHE, ctypes.POINTER(MoeAttnArgs), _I32, _P]),
+    "moe_attn_tree": (_I32, [_CACHE, ctypes.POINTER(MoeAttnArgs), _P, _I32, _P]),
+    "moe_latent_write": (_I32, [_LATENT, _I32, _P, _I64, _P, _I64, _P, ctypes.c_float, _P, _P, _I32, _P]),
+    "moe_attn_latent_workspace_size": (_SZ, [_LATENT, _I32]),
+    "moe_attn_latent": (_I32, [_LATENT, ctypes.POINTER(MoeAttnArgs), _P, _I32, _P]),
+    "moe_attn_expanded_workspace_size": (_SZ, [_I32]),
+    "moe_attn_expanded": (_I32, [ctypes.POINTER(MoeAttnExpandedArgs), _I32, _P]),
+    "moe_block_norm": (_I32, [ctypes.POINTER(MoeNormArgs), _I32, _P]),
     "moe_draft_verify": (_I32, [_I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I32, _P]),
     "moe_draft_verify_ex": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I32,
                                    _P]),
@@ -414,16 +444,22 @@ def attn_args(q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal=True
               workspace=None, err_flag=None) -> MoeAttnArgs:
     """MoeAttnArgs from tensors: q, o bf16 [T][heads][head_dim] (any token and head strides), lse
     fp32 [T][heads]; workspace: moe_attn_workspace_size bytes, zeroed once before its first use."""
+    _same("attn_args: o", (o.shape, q.shape))
+    return _attn_args("attn_args", q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal, window, lse,
+                      workspace, err_flag)
+
+
+def _attn_args(where, q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal, window, lse, workspace, err_flag):
     T, H, D = q.shape
     B = kv_len.shape[0]
-    _same("attn_args: o", (o.shape, q.shape), (o.dtype, torch.bfloat16), (q.dtype, torch.bfloat16))
+    _same(f"{where}: q, o", (o.dtype, torch.bfloat16), (q.dtype, torch.bfloat16))
     if q.stride(2) != 1 or o.stride(2) != 1:
-        raise ValueError("attn_args: head_dim is contiguous in q and o")
-    _vector("attn_args: cu_q", cu_q, torch.int32, B + 1)
-    _vector("attn_args: kv_len", kv_len, torch.int32, B)
-    _table_ok("attn_args", block_table, B)
+        raise ValueError(f"{where}: head_dim is contiguous in q and o")
+    _vector(f"{where}: cu_q", cu_q, torch.int32, B + 1)
+    _vector(f"{where}: kv_len", kv_len, torch.int32, B)
+    _table_ok(where, block_table, B)
     if lse is not None:
-        _same("attn_args: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
+        _same(f"{where}: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
     size = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = MoeAttnArgs(_ptr(q), _ptr(o), _ptr(lse), q.stride(0), q.stride(1), o.stride(0), o.stride(1), _ptr(cu_q),
                        _ptr(kv_len), _ptr(block_table), block_table.shape[1], T, B, max_q, max_kv, H, float(scale),
@@ -437,6 +473,143 @@ def moe_attn_paged(cache: MoeKvCache, args: MoeAttnArgs, max_ctas=0, stream=None
         raise ValueError(f"moe_attn_paged: q and o have heads of {args.head_dim}, the cache of {cache.head_dim}")
     _check(lib().moe_attn_paged(ctypes.byref(cache), ctypes.byref(args), max_ctas, _stream(stream)),
            "moe_attn_paged")
+
+
+def _branches(where, tree, args):
+    if tree.dtype not in (torch.int64, torch.uint64) or tree.shape != (args.T,) or not tree.is_contiguous():
+        raise ValueError(f"{where}: tree is a packed vector of {args.T} 64-bit integers, got {tree.dtype} "
+                         f"{tuple(tree.shape)}")
+    return tree.data_ptr()
+
+
+def moe_attn_tree(cache: MoeKvCache, args: MoeAttnArgs, tree, max_ctas=0, stream=None):
+    """moe_attn_paged for trees of drafted tokens: tree int64 (or uint64) [T], bit j of a row's for its
+    request's j-th new token (at most 64), itself included or not; args with causal, without a window."""
+    if getattr(args, "head_dim", cache.head_dim) != cache.head_dim:
+        raise ValueError(f"moe_attn_tree: q and o have heads of {args.head_dim}, the cache of {cache.head_dim}")
+    _check(lib().moe_attn_tree(ctypes.byref(cache), ctypes.byref(args), _branches("moe_attn_tree", tree, args), max_ctas,
+                               _stream(stream)), "moe_attn_tree")
+
+
+# ---------------------------------------------------------------- latent attention
+LATENT, ROPE, HEAD = 512, 64, 128  # numbers of a latent vector, of a rotary key, of an expanded key or value
+
+
+def latent_cache(pool) -> MoeLatentCache:
+    """The cache in a bf16 pool [pages][page_size][576] (any strides, the 576 numbers contiguous: 512 of the
+    latent vector, 64 of the rotary key).  The pool must outlive the cache."""
+    if pool.dtype != torch.bfloat16 or pool.dim() != 3 or pool.shape[2] != LATENT + ROPE or pool.stride(2) != 1:
+        raise ValueError(f"latent_cache: a bf16 pool [pages][page_size][{LATENT + ROPE}] with contiguous rows is "
+                         f"expected, got {pool.dtype} {tuple(pool.shape)}")
+    return MoeLatentCache(_ptr(pool), BF16, pool.shape[0], pool.shape[1], LATENT, ROPE, pool.stride(0), pool.stride(1))
+
+
+def moe_latent_write(cache: MoeLatentCache, c, k_rope, slots, weight=None, eps=1e-6, err_flag=None, max_ctas=0,
+                     stream=None):
+    """Stores c [T][512] (normed with weight [512] where given) and k_rope [T][64] (bf16, any row strides) at
+    slots int64 [T]."""
+    T = c.size(0)
+    bf16 = torch.bfloat16
+    if c.shape != (T, cache.latent) or k_rope.shape != (T, cache.rope) or not (c.dtype is k_rope.dtype is bf16):
+        raise ValueError(f"moe_latent_write: c and k_rope are bf16 [{T}][{cache.latent}] and [{T}][{cache.rope}], got "
+                         f"{c.dtype} {tuple(c.shape)} and {k_rope.dtype} {tuple(k_rope.shape)}")
+    c0, c1 = c.stride()
+    r0, r1 = k_rope.stride()
+    if c1 != 1 or r1 != 1:
+        raise ValueError("moe_latent_write: the rows of c and k_rope are contiguous")
+    if weight is not None:
+        _vector("moe_latent_write: weight", weight, bf16, cache.latent)
+    _vector("moe_latent_write: slots", slots, torch.int64, T)
+    # the stride of a single row is not used, and may be any number
+    _check(lib().moe_latent_write(ctypes.byref(cache), T, c.data_ptr(), c0 if T > 1 else cache.latent,
+                                  k_rope.data_ptr(), r0 if T > 1 else cache.rope, _ptr(weight), eps, slots.data_ptr(),
+                                  _ptr(err_flag), max_ctas, _stream(stream)), "moe_latent_write")
+
+
+def moe_attn_latent_workspace_size(cache: MoeLatentCache, num_q_heads: int) -> int:
+    return int(lib().moe_attn_latent_workspace_size(ctypes.byref(cache), num_q_heads))
+
+
+def attn_latent_args(q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal=True, window=0, lse=None,
+                     workspace=None, err_flag=None) -> MoeAttnArgs:
+    """attn_args of moe_attn_latent: q bf16 [T][heads][576], o bf16 [T][heads][512]; workspace:
+    moe_attn_latent_workspace_size bytes, zeroed once before its first use."""
+    _same("attn_latent_args: q, o", (q.dim(), 3), (q.shape[2:], (LATENT + ROPE,)), (o.shape, (*q.shape[:2], LATENT)))
+    return _attn_args("attn_latent_args", q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, causal, window, lse,
+                      workspace, err_flag)
+
+
+def moe_attn_latent(cache: MoeLatentCache, args: MoeAttnArgs, tree=None, max_ctas=0, stream=None):
+    """Absorbed latent attention; tree as for moe_attn_tree."""
+    width = cache.latent + cache.rope
+    if getattr(args, "head_dim", width) != width:  # a structure filled by hand has none
+        raise ValueError(f"moe_attn_latent: q has rows of {args.head_dim}, the cache of {width} (attn_latent_args)")
+    _check(lib().moe_attn_latent(ctypes.byref(cache), ctypes.byref(args),
+                                 None if tree is None else _branches("moe_attn_latent", tree, args), max_ctas,
+                                 _stream(stream)), "moe_attn_latent")
+
+
+def moe_attn_expanded_workspace_size(num_heads: int) -> int:
+    return int(lib().moe_attn_expanded_workspace_size(num_heads))
+
+
+def attn_expanded_args(q, k, k_rope, v, o, cu_q, cu_kv, max_q, max_kv, scale, causal=True, lse=None, workspace=None,
+                       err_flag=None) -> MoeAttnExpandedArgs:
+    """MoeAttnExpandedArgs from bf16 tensors q [T][heads][192], k and v [S][heads][128], k_rope [S][64],
+    o [T][heads][128] (any row and head strides); lse fp32 [T][heads]; workspace:
+    moe_attn_expanded_workspace_size bytes, zeroed once before its first use."""
+    T, H, _ = q.shape
+    S, B = k_rope.shape[0], cu_q.shape[0] - 1
+    _same("attn_expanded_args: shapes", (q.shape, (T, H, HEAD + ROPE)), (k.shape, (S, H, HEAD)),
+          (k_rope.shape, (S, ROPE)), (v.shape, (S, H, HEAD)), (o.shape, (T, H, HEAD)))
+    for t in (q, k, k_rope, v, o):
+        _same("attn_expanded_args: types", (t.dtype, torch.bfloat16))
+        if t.stride(-1) != 1:
+            raise ValueError("attn_expanded_args: rows are contiguous")
+    _vector("attn_expanded_args: cu_q", cu_q, torch.int32, B + 1)
+    _vector("attn_expanded_args: cu_kv", cu_kv, torch.int32, B + 1)
+    if lse is not None:
+        _same("attn_expanded_args: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
+    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return MoeAttnExpandedArgs(_ptr(q), _ptr(k), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), q.stride(0), q.stride(1),
+                               k.stride(0), k.stride(1), k_rope.stride(0), v.stride(0), v.stride(1), o.stride(0),
+                               o.stride(1), _ptr(cu_q), _ptr(cu_kv), T, S, B, max_q, max_kv, H, float(scale),
+                               int(causal), _ptr(err_flag), _ptr(workspace), size)
+
+
+def moe_attn_expanded(args: MoeAttnExpandedArgs, max_ctas=0, stream=None):
+    _check(lib().moe_attn_expanded(ctypes.byref(args), max_ctas, _stream(stream)), "moe_attn_expanded")
+
+
+# ---------------------------------------------------------------- between two blocks
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def moe_block_norm(y, out=None, pre_weight=None, resid=None, resid_out=None, post_weight=None, gate=None, scale=1.0,
+                   eps=1e-6, max_ctas=0, stream=None):
+    """x = norm(y) with post_weight [H], or y; resid_out = resid + scale * gate * x; out = norm(resid_out) with
+    pre_weight [H].  y, out, weights and gate ([T][H], or [1][H] for all tokens) fp32 or bf16, the residual
+    either; packed rows.  resid_out may be resid, and out may be y."""
+    T, H = y.shape
+    dtype = y.dtype
+    stream_of = resid if resid is not None else resid_out
+    rdtype = dtype if stream_of is None else stream_of.dtype
+    if dtype not in _FLOATS or rdtype not in _FLOATS or not y.is_contiguous():
+        raise ValueError(f"moe_block_norm: packed rows of fp32 or bf16 are expected, got {dtype} and {rdtype}")
+    for t, d in ((out, dtype), (resid, rdtype), (resid_out, rdtype)):
+        if t is not None and (t.dtype is not d or t.shape != y.shape or not t.is_contiguous()):
+            raise ValueError(f"moe_block_norm: packed {d} rows {tuple(y.shape)} are expected, got {t.dtype} {tuple(t.shape)}")
+    for t in (post_weight, pre_weight):
+        if t is not None:
+            _vector("moe_block_norm: weight", t, dtype, H)
+    rows = 1
+    if gate is not None:
+        rows = gate.size(0)
+        if gate.dtype is not dtype or gate.shape != (rows, H) or rows not in (1, T) or not gate.is_contiguous():
+            raise ValueError(f"moe_block_norm: gate is packed {dtype} [1 or {T}][{H}], got {gate.dtype} {tuple(gate.shape)}")
+    args = MoeNormArgs(y.data_ptr(), _ptr(post_weight), _ptr(gate), _ptr(resid), _ptr(resid_out), _ptr(pre_weight),
+                       _ptr(out), T, H, _FLOATS[dtype], _FLOATS[rdtype], rows, scale, eps)
+    _check(lib().moe_block_norm(ctypes.byref(args), max_ctas, _stream(stream)), "moe_block_norm")
 
 
 def moe_draft_verify(target, draft, cu_draft, ids, u, u_draw, out_ids, out_len, err_flag=None, max_ctas=0,

@@ -10,6 +10,22 @@
 
 using namespace moe;
 
+namespace moe {
+
+bool rows_apart(int64_t T, int64_t H, int64_t ld, int64_t hs, int64_t width) {
+    if ((T > 1 && ld < width) || (H > 1 && hs < width)) return false;
+    if (T == 1 || H == 1) return true;
+    if (ld - width >= (H - 1) * hs || hs - width >= (T - 1) * ld) return true;  // one inside the other
+    // the tokens nearest to each head, before it and after it
+    for (int64_t h = 1; h < H; ++h) {
+        const int64_t t = h * hs / ld, past = h * hs - t * ld;
+        if ((t < T && past < width) || (t + 1 < T && ld - past < width)) return false;
+    }
+    return true;
+}
+
+}  // namespace moe
+
 namespace {
 
 // A call without an SM budget may have more CTAs than fit at once where they are short and alike.
@@ -44,17 +60,39 @@ moe_status check_cache(const moe_kv_cache* c) {
     return MOE_OK;
 }
 
-// Whether rows of `width` elements at t * ld + h * hs, t < T, h < H, lie apart from each other.
-bool rows_apart(int64_t T, int64_t H, int64_t ld, int64_t hs, int64_t width) {
-    if ((T > 1 && ld < width) || (H > 1 && hs < width)) return false;
-    if (T == 1 || H == 1) return true;
-    if (ld - width >= (H - 1) * hs || hs - width >= (T - 1) * ld) return true;  // one inside the other
-    // the tokens nearest to each head, before it and after it
-    for (int64_t h = 1; h < H; ++h) {
-        const int64_t t = h * hs / ld, past = h * hs - t * ld;
-        if ((t < T && past < width) || (t + 1 < T && ld - past < width)) return false;
-    }
-    return true;
+moe_status attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, const uint64_t* tree, int32_t max_ctas,
+                      moe_stream_t stream) {
+    const moe_status s = check_cache(cache);
+    if (s != MOE_OK) return s;
+    if (!a || a->T < 0 || a->B < 0 || a->max_q < 0 || a->max_kv < 0 || a->table_ld < 0 || a->window < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (a->num_q_heads <= 0 || a->num_q_heads % cache->num_heads || !isfinite(a->scale) || a->scale <= 0.0f)
+        return MOE_ERR_INVALID_ARG;
+    if (a->causal != 0 && a->causal != 1) return MOE_ERR_INVALID_ARG;
+    if (a->num_q_heads / cache->num_heads > 64 || a->B > kMaxRequests) return MOE_ERR_UNSUPPORTED;
+    if (a->T > kMaxTokens || a->max_kv > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+    if (a->T == 0 || a->B == 0 || a->max_q == 0) return MOE_OK;
+    if (!a->q || !a->o || !a->cu_q || !a->kv_len || (a->table_ld > 0 && !a->block_table)) return MOE_ERR_INVALID_ARG;
+    if (a->q_ld < 0 || a->q_head_stride < 0 || a->o_ld < 0 || a->o_head_stride < 0) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a->q) || !aligned16(a->o) || a->q_ld % 8 || a->q_head_stride % 8 || a->o_ld % 8 ||
+        a->o_head_stride % 8)
+        return MOE_ERR_ALIGNMENT;
+    // no stride that is used reaches past a tensor map's (below 2^40 bytes) or what 64 bits count
+    const int64_t T = a->T, H = a->num_q_heads, most = INT64_MAX / 2 / (T > H ? T : H), far = (int64_t)1 << 39;
+    const int64_t limit = most < far ? most : far;
+    if ((T > 1 && (a->q_ld >= limit || a->o_ld >= limit)) ||
+        (H > 1 && (a->q_head_stride >= limit || a->o_head_stride >= limit)))
+        return MOE_ERR_UNSUPPORTED;
+    // rows of o that overlap would be written by several threads at once
+    if (!rows_apart(T, H, a->o_ld, a->o_head_stride, cache->head_dim)) return MOE_ERR_INVALID_ARG;
+    // work is counted in 31 bits: tiles of as few tokens as any kernel takes, against tiles of keys
+    const int64_t group = a->num_q_heads / cache->num_heads, rows = a->max_q * group;
+    const int64_t tokens = rows > kFewRows ? 128 / group * 2 : (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) / group;
+    if ((a->T / tokens + a->B) * cache->num_heads > INT32_MAX / ((int64_t)a->max_kv / 128 + 16))
+        return MOE_ERR_UNSUPPORTED;
+    if (!a->workspace || a->workspace_bytes < attn_workspace_bytes()) return MOE_ERR_WORKSPACE;
+    if (!aligned_to(a->workspace, 256)) return MOE_ERR_ALIGNMENT;
+    return cuda_status(launch_attn(*cache, *a, tree, grid_cap_of(max_ctas), (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -94,37 +132,16 @@ size_t moe_attn_workspace_size(const moe_kv_cache* cache, int32_t num_q_heads) {
 }
 
 moe_status moe_attn_paged(const moe_kv_cache* cache, const moe_attn_args* a, int32_t max_ctas, moe_stream_t stream) {
-    const moe_status s = check_cache(cache);
-    if (s != MOE_OK) return s;
-    if (!a || a->T < 0 || a->B < 0 || a->max_q < 0 || a->max_kv < 0 || a->table_ld < 0 || a->window < 0)
-        return MOE_ERR_INVALID_ARG;
-    if (a->num_q_heads <= 0 || a->num_q_heads % cache->num_heads || !isfinite(a->scale) || a->scale <= 0.0f)
-        return MOE_ERR_INVALID_ARG;
-    if (a->causal != 0 && a->causal != 1) return MOE_ERR_INVALID_ARG;
-    if (a->num_q_heads / cache->num_heads > 64 || a->B > kMaxRequests) return MOE_ERR_UNSUPPORTED;
-    if (a->T > kMaxTokens || a->max_kv > kMaxTokens) return MOE_ERR_UNSUPPORTED;
-    if (a->T == 0 || a->B == 0 || a->max_q == 0) return MOE_OK;
-    if (!a->q || !a->o || !a->cu_q || !a->kv_len || (a->table_ld > 0 && !a->block_table)) return MOE_ERR_INVALID_ARG;
-    if (a->q_ld < 0 || a->q_head_stride < 0 || a->o_ld < 0 || a->o_head_stride < 0) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(a->q) || !aligned16(a->o) || a->q_ld % 8 || a->q_head_stride % 8 || a->o_ld % 8 ||
-        a->o_head_stride % 8)
-        return MOE_ERR_ALIGNMENT;
-    // no stride that is used reaches past a tensor map's (below 2^40 bytes) or what 64 bits count
-    const int64_t T = a->T, H = a->num_q_heads, most = INT64_MAX / 2 / (T > H ? T : H), far = (int64_t)1 << 39;
-    const int64_t limit = most < far ? most : far;
-    if ((T > 1 && (a->q_ld >= limit || a->o_ld >= limit)) ||
-        (H > 1 && (a->q_head_stride >= limit || a->o_head_stride >= limit)))
-        return MOE_ERR_UNSUPPORTED;
-    // rows of o that overlap would be written by several threads at once
-    if (!rows_apart(T, H, a->o_ld, a->o_head_stride, cache->head_dim)) return MOE_ERR_INVALID_ARG;
-    // work is counted in 31 bits: tiles of as few tokens as any kernel takes, against tiles of keys
-    const int64_t group = a->num_q_heads / cache->num_heads, rows = a->max_q * group;
-    const int64_t tokens = rows > kFewRows ? 128 / group * 2 : (rows <= 8 ? 8 : rows <= 16 ? 16 : 32) / group;
-    if ((a->T / tokens + a->B) * cache->num_heads > INT32_MAX / ((int64_t)a->max_kv / 128 + 16))
-        return MOE_ERR_UNSUPPORTED;
-    if (!a->workspace || a->workspace_bytes < attn_workspace_bytes()) return MOE_ERR_WORKSPACE;
-    if (!aligned_to(a->workspace, 256)) return MOE_ERR_ALIGNMENT;
-    return cuda_status(launch_attn(*cache, *a, grid_cap_of(max_ctas), (cudaStream_t)stream));
+    return attn_paged(cache, a, nullptr, max_ctas, stream);
+}
+
+moe_status moe_attn_tree(const moe_kv_cache* cache, const moe_attn_args* a, const uint64_t* tree, int32_t max_ctas,
+                         moe_stream_t stream) {
+    if (a && a->T > 0 && !tree) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(tree, 8)) return MOE_ERR_ALIGNMENT;
+    if (a && (a->causal != 1 || a->window != 0)) return MOE_ERR_INVALID_ARG;
+    if (a && a->max_q > kMaxTree) return MOE_ERR_UNSUPPORTED;
+    return attn_paged(cache, a, tree, max_ctas, stream);
 }
 
 moe_status moe_draft_verify(int32_t B, int32_t vocab, int32_t max_draft, int32_t dtype, const void* target,

@@ -1,4 +1,4 @@
-// moe_attn_paged: picks the kernel for a call and builds its tensor maps.
+// moe_attn_paged, moe_attn_tree: picks the kernel for a call and builds its tensor maps.
 #include "attn.cuh"
 
 #include <cudaTypedefs.h>
@@ -31,7 +31,8 @@ size_t attn_workspace_bytes() {
     return attn::kMaxCtas * sizeof(uint32_t) + ctas * 2 * attn::kPartBytes;
 }
 
-cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_cap, cudaStream_t st) {
+cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, const uint64_t* tree, int grid_cap,
+                        cudaStream_t st) {
     using namespace attn;
     Params p;
     p.q = static_cast<const uint16_t*>(a.q);
@@ -56,7 +57,8 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_
     p.page_shift = 0;
     while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.causal = a.causal;
+    p.causal = tree ? 0 : a.causal;
+    p.tree = tree;
     p.window = a.window < kMaxTokens ? a.window : kMaxTokens;  // no row is further from a token
     p.err = a.err_flag;
     p.counters = static_cast<uint32_t*>(a.workspace);
@@ -69,6 +71,8 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_
     // against 96); e4m3: 32: 129 against 147, 64: 189 against 148.  One rule for the whole call: one chunk of 512
     // tokens beside 127 single tokens takes 258 us here, 45 + 178 as two calls (e4m3: 354, 57 + 100).
     const int64_t rows = (int64_t)a.max_q * p.group;
+    if (tree)
+        return rows <= kFewRows ? launch_rows_tree(c, p, (int)rows, grid_cap, st) : launch_tiles_tree(c, p, grid_cap, st);
     return rows <= kFewRows ? launch_rows(c, p, (int)rows, grid_cap, st) : launch_tiles(c, p, grid_cap, st);
 }
 

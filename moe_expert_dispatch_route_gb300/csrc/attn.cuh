@@ -57,6 +57,91 @@ __device__ __forceinline__ bool elect_one() {
 
 namespace attn {
 
+// ---------------------------------------------------------------- PTX not shared with the FFN
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], A's row i in lane i, two 16-bit elements of K per column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an operand whose M/N index is contiguous (here V: columns contiguous, keys the
+// K index), 128-byte swizzle: blocks of 64 columns kBlock bytes apart (the leading byte
+// offset), groups of 8 keys 1024 bytes apart (the stride byte offset).
+__device__ __forceinline__ uint64_t desc_sw128_mnmajor(uint32_t saddr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(block_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+constexpr uint32_t kIdescBMn = 1u << 16;  // B with its N index contiguous
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+          "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 constexpr int kKeyTile = 128;
 constexpr int kMaxCtas = 1024;     // counters at the front of the workspace
 constexpr int kMaxRows = 256;      // rows of the largest query tile
@@ -84,6 +169,7 @@ struct Params {
     uint32_t* counters;       // [kMaxCtas], all zero between calls
     uint8_t* parts;           // [grid][2] parts: slot 0 the tile begun last, slot 1 the tile continued
     int64_t inject_ns;
+    const uint64_t* tree;     // of a tree of drafted tokens: a new token's branch, else null
 };
 
 // A request's lengths; n = 0 for one that is refused (its rows are not written).
@@ -98,6 +184,26 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
     r.kv = p.kv_len[b];
     const int64_t room = (int64_t)p.table_ld << p.page_shift;
     if (r.row0 < 0 || r.n < 0 || r.n > p.max_q || r.row0 > p.T - r.n || r.kv < 0 || r.kv > p.max_kv || r.kv > room) {
+        if (report) set_err(p.err, MOE_ERR_BAD_INDEX);
+        r.n = 0;
+    }
+    return r;
+}
+
+// Keys in packed rows (moe_attn_expanded) instead of pages: request b's are cu_kv[b] .. cu_kv[b+1].  kv_len
+// and the table are not used.
+struct DenseParams : Params {
+    const int32_t* cu_kv;
+    int S;  // rows of keys
+};
+__device__ __forceinline__ Request request(const DenseParams& p, int b, bool report) {
+    Request r;
+    r.row0 = p.cu_q[b];
+    r.n = p.cu_q[b + 1] - r.row0;
+    const int first = p.cu_kv[b];
+    r.kv = p.cu_kv[b + 1] - first;
+    if (r.row0 < 0 || r.n < 0 || r.n > p.max_q || r.row0 > p.T - r.n || first < 0 || r.kv < 0 || r.kv > p.max_kv ||
+        first > p.S - r.kv) {
         if (report) set_err(p.err, MOE_ERR_BAD_INDEX);
         r.n = 0;
     }
@@ -165,15 +271,17 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t v) {
 }
 
 // CTAs that get units, at least one each: no CTA has too few to be worth a part.
-__device__ __forceinline__ uint32_t ctas_for(const Params& p, uint32_t total) {
-    return total == 0 ? 0 : min((uint32_t)gridDim.x, max(total / (uint32_t)p.cta_units, 1u));
+__device__ __forceinline__ uint32_t ctas_for(const Params& p, uint32_t total, uint32_t ctas) {
+    return total == 0 ? 0 : min(ctas, max(total / (uint32_t)p.cta_units, 1u));
 }
 
-// Whole CTA (kThreads threads): the CTA's range of units and the query tile it begins in.
+// Whole CTA (kThreads threads): the range of units of CTA `me` of `ctas` (here the CTA itself of the grid, or
+// a team of CTAs that share a range) and the query tile it begins in.
 // scratch: shared, p.B + 32 uint32, free again for copies after it.  Ends with a barrier;
 // st->unit == st->end: nothing to do.
-template <int kThreads>
-__device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
+template <int kThreads, typename P>
+__device__ void locate(const P& p, uint32_t* scratch, Start* st, uint32_t me = blockIdx.x,
+                       uint32_t ctas = gridDim.x) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool single = p.max_q <= p.tokens_per_tile;  // one query tile a request
@@ -183,12 +291,12 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
             Request r = {0, 0, 0};
             uint32_t one = 0;
             if (lane < p.B) {
-                r = request(p, lane, blockIdx.x == 0);
+                r = request(p, lane, me == 0);
                 if (r.n > 0) one = cost_of(p, span(p, r, 0).units);
             }
             const uint32_t k = one * (uint32_t)p.heads, upto = warp_incl(k), at = upto - k;
             const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
-            const uint32_t n = ctas_for(p, total), me = blockIdx.x;
+            const uint32_t n = ctas_for(p, total, ctas);
             const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
             int moved[2];
             bool next = false;
@@ -232,14 +340,14 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     Request r = {0, 0, 0};
     if (single) {
         for (int b = b0; b < b1; ++b) {
-            r = request(p, b, blockIdx.x == 0);
+            r = request(p, b, me == 0);
             const uint32_t u = r.n > 0 ? cost_of(p, span(p, r, 0).units) : 0u;
             if (run > 1) per[b] = u;
             mine += u;
         }
     } else {
         for (int b = warp; b < p.B; b += kWarps) {
-            const Request q = request(p, b, blockIdx.x == 0 && lane == 0);
+            const Request q = request(p, b, me == 0 && lane == 0);
             const int n = tiles_of(p, q);
             uint32_t s = 0;
             for (int i = lane; i < n; i += 32) s += cost_of(p, span(p, q, i).units);
@@ -262,7 +370,7 @@ __device__ void locate(const Params& p, uint32_t* scratch, Start* st) {
     const uint32_t total = all * (uint32_t)p.heads;  // host: below 2^31
     // no CTA's range is empty (before boundaries move) but those of surplus CTAs: the CTAs of a
     // split tile are consecutive
-    const uint32_t n = ctas_for(p, total), me = blockIdx.x;
+    const uint32_t n = ctas_for(p, total, ctas);
     const uint32_t each = n ? total / n : 0, rest = n ? total - each * n : 0;
     const uint32_t u[2] = {me < n ? me * each + min(me, rest) : total,
                            me + 1 < n ? (me + 1) * each + min(me + 1, rest) : total};
@@ -366,7 +474,8 @@ __device__ __forceinline__ bool more(const Cursor& c) { return c.unit < c.end; }
 
 // The next item.  The cursor moves to it only now: the lengths of a request are not waited
 // for before its turn.
-__device__ __forceinline__ Item take(const Params& p, Cursor& c) {
+template <typename P>
+__device__ __forceinline__ Item take(const P& p, Cursor& c) {
     if (c.done) {
         c.skip = 0;
         if (++c.tile >= tiles_of(p, c.r)) {
@@ -426,6 +535,17 @@ __device__ __forceinline__ int page_of(const Params& p, const Item& it, Pages& g
         g.then = page_entry(p, it, g.first + 32 + (threadIdx.x & 31));
     }
     return __shfl_sync(0xffffffffu, g.now, (i0 - g.first + pg) & 31);
+}
+
+// A tree of drafted tokens (moe_attn_tree): a row sees the tokens before its request's new ones and, of
+// those, its branch: new token j stands at position first + j.
+struct Branch {
+    int first;
+    uint64_t bits;
+    __device__ __forceinline__ bool sees(int key) const { return key < first || (bits >> (key - first) & 1); }
+};
+__device__ __forceinline__ Branch branch_of(const Params& p, const Request& r, int token) {
+    return {r.kv - r.n, __ldg(p.tree + token) | 1ull << (token - r.row0)};
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -543,10 +663,13 @@ __device__ __forceinline__ int part_slot(const Parts& parts, int c) { return c =
 // Tensor map of a pool for boxes of up to kKeyTile tokens of one head: (d, token, head, page).
 bool make_pool_map(CUtensorMap* m, const moe_kv_cache& c, const void* base);
 
-// attn_rows.cu: requests of up to kFewRows rows a key/value head, on mma.sync, a tile's keys shared by warps
+// attn_rows.cuh: requests of up to kFewRows rows a key/value head, on mma.sync, a tile's keys shared by
+// warps; the second form is that for trees of drafted tokens (Params::tree)
 cudaError_t launch_rows(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st);
-// attn_tile.cu: query tiles of up to 256 rows on tcgen05
+cudaError_t launch_rows_tree(const moe_kv_cache& c, Params& p, int rows, int grid_cap, cudaStream_t st);
+// attn_tile.cuh: query tiles of up to 256 rows on tcgen05; likewise
 cudaError_t launch_tiles(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);
+cudaError_t launch_tiles_tree(const moe_kv_cache& c, Params& p, int grid_cap, cudaStream_t st);
 
 inline int64_t most_units(const Params& p) {
     return ((int64_t)p.T / p.tokens_per_tile + p.B) * p.heads * ((int64_t)p.max_kv / kKeyTile + 2 + p.item_cost);

@@ -19,6 +19,8 @@ struct DeviceInfo {
 const DeviceInfo& device_info();
 moe_status check_config(const moe_config* c);  // shape limits and row alignment
 bool aligned16(const void* p);
+// api_serve.cu: whether rows of `width` elements at t * ld + h * hs, t < T, h < H, lie apart from each other
+bool rows_apart(int64_t T, int64_t H, int64_t ld, int64_t hs, int64_t width);
 
 // Identity of the CUDA context current on the calling thread: unique for the life of
 // the process (a device reset followed by a new context gives a new id); 0 when it
@@ -153,9 +155,25 @@ cudaError_t launch_kv_read(const moe_kv_cache& c, int B, int T, const int32_t* t
 // attn.cu: paged attention (the kernels are in attn_rows.cu and attn_tile.cu)
 constexpr int kMaxRequests = 8192;
 constexpr int kMaxTokens = 1 << 30;  // rows, and cached tokens: positions less a window stay within 32 bits
-constexpr int kFewRows = 32;  // rows of a request and key/value head up to which attn_rows.cu takes the call
+constexpr int kFewRows = 32;  // rows of a request and key/value head up to which attn_rows.cuh takes the call
+constexpr int kMaxTree = 64;  // new tokens of a request in a tree
 size_t attn_workspace_bytes();
-cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, int grid_cap, cudaStream_t st);
+// tree: of moe_attn_tree, else null
+cudaError_t launch_attn(const moe_kv_cache& c, const moe_attn_args& a, const uint64_t* tree, int grid_cap,
+                        cudaStream_t st);
+
+// latent_cache.cu, attn_latent.cu, attn_expanded.cu: latent attention
+cudaError_t launch_latent_write(const moe_latent_cache& c, int T, const void* latent, int64_t ld_c, const void* rope,
+                                int64_t ld_rope, const void* weight, float eps, const int64_t* slots, int32_t* err,
+                                int grid_cap, cudaStream_t st);
+constexpr int kMaxLatentHeads = 128;
+cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a, const uint64_t* tree, int grid_cap,
+                               cudaStream_t st);
+cudaError_t launch_attn_expanded(const moe_attn_expanded_args& a, int grid_cap, cudaStream_t st);
+
+// norm.cu
+constexpr int kMaxNormWidth = 16384;
+cudaError_t launch_block_norm(const moe_norm_args& a, int grid_cap, cudaStream_t st);
 
 // draft_verify.cu
 cudaError_t launch_draft_verify(int B, int N, int V, int max_draft, bool f32, const void* target, int64_t target_ld,
