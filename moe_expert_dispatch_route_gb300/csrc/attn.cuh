@@ -538,14 +538,22 @@ __device__ __forceinline__ int page_of(const Params& p, const Item& it, Pages& g
 }
 
 // A tree of drafted tokens (moe_attn_tree): a row sees the tokens before its request's new ones and, of
-// those, its branch: new token j stands at position first + j.
+// those, its branch: new token j stands at position first + j.  No bits past the request's tokens.
 struct Branch {
     int first;
     uint64_t bits;
     __device__ __forceinline__ bool sees(int key) const { return key < first || (bits >> (key - first) & 1); }
+    // bit j: whether it sees key + j.  A tile's mask from these costs a test a key; from sees(), 64-bit shifts in
+    // both passes over the scores, trees of up to 64 nodes over 32 requests took 174 us instead of 106.
+    __device__ __forceinline__ uint32_t word(int key) const {
+        const int d = key - first;
+        if (d >= 0) return d < 64 ? (uint32_t)(bits >> d) : 0u;
+        return d > -32 ? (uint32_t)(bits << -d) | ((1u << -d) - 1) : 0xffffffffu;
+    }
 };
 __device__ __forceinline__ Branch branch_of(const Params& p, const Request& r, int token) {
-    return {r.kv - r.n, __ldg(p.tree + token) | 1ull << (token - r.row0)};
+    const uint64_t bits = __ldg(p.tree + token) | 1ull << (token - r.row0);
+    return {r.kv - r.n, r.n < 64 ? bits & ((1ull << r.n) - 1) : bits};
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

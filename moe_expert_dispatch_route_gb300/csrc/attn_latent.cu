@@ -19,8 +19,11 @@
 // The running maximum is followed loosely, as in attn_tile.cuh.
 //
 //   warps 0-3   softmax (16 rows each), rescaling and epilogue (a lane of tensor memory each)
-//   warp 4      issues the MMAs
-//   warp 5      copies
+//   warp 4      issues the scores' MMAs
+//   warp 5      issues the products' MMAs: from one warp, each product would wait for the copies of the scores
+//               behind it, which wait for the product to give their place back
+//   warps 6, 7  copies: the rotary blocks and half of the pieces, the other half (a copying warp issues
+//               a copy about every 100 cycles, and 16-token pages take 36 of them for 64 keys)
 #include <cudaTypedefs.h>
 
 #include "attn.cuh"
@@ -35,19 +38,20 @@ constexpr int kBlocks = kWidth / 64;           // 128-byte column blocks of a ro
 constexpr int kBlockBytes = kSub * 128;        // one of them
 constexpr int kPieceBytes = 2 * kBlockBytes;   // 128 columns, as the second product takes them
 constexpr int kPieces = kLatent / 128;
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
 
 template <int kN>
 struct Cfg {
     static constexpr int kQBytes = kBlocks * kN * 128;
     static constexpr int kPBytes = kN * 128;
     // rings of 128-column pieces (four a key tile) and of rotary blocks
-    static constexpr int kRing = kN == 64 ? 8 : kN == 32 ? 10 : 11;
+    static constexpr int kRing = kN == 64 ? 8 : 10;
     static constexpr int kRopes = kN == 64 ? 2 : 3;
-    static constexpr int kBars = 2 * kRing + 2 * kRopes + 2 + 2 + 2 + 2;
+    static constexpr int kBars = 2 * kRing + 2 * kRopes + 4 + 2 + 2 + 2;
     static constexpr int kTail = kBars * 8 + 4 * kRopes + 4 + kN * 20;
     static constexpr int kSmem = 1024 + kQBytes + kPBytes + kRing * kPieceBytes + kRopes * kBlockBytes + kTail;
     static_assert(kSmem <= 232448 - 512, "");
+    static_assert(kRing % 2 == 0, "the copying warps' halves of a tile");
     static_assert(kRing * kPieceBytes >= (kMaxRequests + 32) * 4, "locate()'s scratch");
     // the scores of rows past kN are of what lies behind Q in shared memory, and go nowhere
     static_assert((64 - kN) * 128 <= kPBytes + kRing * kPieceBytes, "");
@@ -88,75 +92,100 @@ __device__ __forceinline__ bool any_of_128(bool x) {
         : "memory");
     return r != 0;
 }
+// 16 lanes, 64 columns from taddr: of lane g = lane / 4 (r[4 i], r[4 i + 1]) and of lane g + 8 (r[4 i + 2], r[4 i + 3])
+// the columns 8 i + 2 (lane % 4) and the next.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ float max_of_4(float v) {  // of the lanes that share a row
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
 __device__ __forceinline__ void sync_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // The softmax warps: the sum of n parts of a split tile, those of CTAs first, first + step, ..., in this
-// order, a row at a time and four columns a thread.  kEnd: it goes to the output, otherwise to the place of
-// the first part.
+// order, four columns a thread.  kEnd: it goes to the output, otherwise to the place of the first part.
+// weights: shared, kFan * 64 floats.  kBatch rows of a part are loaded at a time, those of the next part (or of
+// the first one's next rows) while these are added: two rows of all parts at a time, a join of two parts of
+// 64 rows took 50 us.
 constexpr int kFan = 4;  // the most parts summed together
 template <bool kEnd>
-__device__ void join_rows(const LatentParams& lp, const Parts& parts, int first, int step, int n, int block, int rows,
-                          const int64_t* row_off, const int64_t* row_lse) {
+__device__ __noinline__ void join_rows(const LatentParams& lp, const Parts& parts, int first, int step, int n, int block,
+                                       int rows, const int64_t* row_off, const int64_t* row_lse, float* weights) {
     const Params& p = lp.p;
     auto cta = [&](int i) { return (first + i * step) * lp.team + block; };
     auto slot = [&](int i) { return part_slot(parts, first + i * step); };
-    constexpr int kUnroll = 2;  // rows under way together
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += kUnroll) {
-        float2 ml[kUnroll][kFan];
-        float4 x[kUnroll][kFan];
+    const int tid = threadIdx.x;
+    constexpr int kBatch = 8;
+    float4 next[kBatch];
+    int load_r = 0, load_i = 0;
+    auto load = [&] {
+        if (load_r >= rows) return;
+        const float4* from =
+            reinterpret_cast<const float4*>(part_o(p, cta(load_i), slot(load_i)) + load_r * kLatent) + tid;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int j = 0; j < kBatch; ++j)
+            if (load_r + j < rows) next[j] = __ldcg(from + j * (kLatent / 4));
+        if (++load_i == n) load_i = 0, load_r += kBatch;
+    };
+    load();
+    if (tid < rows) {
+        float2 ml[kFan];
+        float m = -CUDART_INF_F, l = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kFan; ++i) {
-                ml[u][i] = make_float2(-CUDART_INF_F, 0.0f);
-                x[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < n && r0 + u < rows) {
-                    ml[u][i] = __ldcg(part_ml(p, cta(i), slot(i)) + r0 + u);
-                    x[u][i] = __ldcg(reinterpret_cast<const float4*>(part_o(p, cta(i), slot(i)) + (r0 + u) * kLatent) +
-                                     threadIdx.x);
-                }
-            }
+        for (int i = 0; i < kFan; ++i)
+            ml[i] = i < n ? __ldcg(part_ml(p, cta(i), slot(i)) + tid) : make_float2(-CUDART_INF_F, 0.0f);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int r = r0 + u;
-            if (r >= rows) break;
-            float m = -CUDART_INF_F, l = 0.0f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kFan; ++i) m = fmaxf(m, ml[i].x);
+        const float to = m == -CUDART_INF_F ? 0.0f : m;
 #pragma unroll
-            for (int i = 0; i < kFan; ++i) m = fmaxf(m, ml[u][i].x);
-            const float to = m == -CUDART_INF_F ? 0.0f : m;
+        for (int i = 0; i < kFan; ++i) l += ml[i].y * exp2_fast(ml[i].x - to);
+        const float inv = !kEnd ? 1.0f : l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
-            for (int i = 0; i < kFan; ++i) {
-                const float w = exp2_fast(ml[u][i].x - to);
-                l += ml[u][i].y * w;
-                o.x += x[u][i].x * w, o.y += x[u][i].y * w;
-                o.z += x[u][i].z * w, o.w += x[u][i].w * w;
-            }
-            if (!kEnd) {
-                reinterpret_cast<float4*>(part_o(p, cta(0), slot(0)) + r * kLatent)[threadIdx.x] = o;
-                continue;
-            }
-            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-            if (row_off[r] >= 0)
-                *reinterpret_cast<uint2*>(p.o + row_off[r] + threadIdx.x * 4) =
-                    make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
-            if (p.lse && row_off[r] >= 0 && threadIdx.x == 0)
-                p.lse[row_lse[r]] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-        }
+        for (int i = 0; i < kFan; ++i) weights[i * 64 + tid] = exp2_fast(ml[i].x - to) * inv;
+        if (!kEnd)
+            part_ml(p, cta(0), slot(0))[tid] = make_float2(m, l);  // read by this thread alone before
+        else if (p.lse && row_off[tid] >= 0)
+            p.lse[row_lse[tid]] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
     }
-    if (!kEnd) {  // the sums' maxima and sums, once every thread has read the parts'
-        sync_128();
-        for (int r = threadIdx.x; r < rows; r += 128) {
-            float m = -CUDART_INF_F, l = 0.0f;
-            for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(part_ml(p, cta(i), slot(i)) + r).x);
-            const float to = m == -CUDART_INF_F ? 0.0f : m;
-            for (int i = 0; i < n; ++i) {
-                const float2 ml = __ldcg(part_ml(p, cta(i), slot(i)) + r);
-                l += ml.y * exp2_fast(ml.x - to);
-            }
-            part_ml(p, cta(0), slot(0))[r] = make_float2(m, l);
+    sync_128();
+    float4 o[kBatch];
+#pragma unroll 1
+    for (int r0 = 0, i = 0; r0 < rows;) {
+        float4 x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) x[j] = next[j];
+        load();
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float w = weights[i * 64 + min(r0 + j, rows - 1)];
+            if (i == 0) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w == 0.0f) continue;  // a part without keys, or a sum of 0: its numbers may be anything
+            o[j].x += x[j].x * w, o[j].y += x[j].y * w;
+            o[j].z += x[j].z * w, o[j].w += x[j].w * w;
         }
+        if (++i < n) continue;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int r = r0 + j;
+            if (r >= rows) break;
+            if (!kEnd)
+                reinterpret_cast<float4*>(part_o(p, cta(0), slot(0)) + r * kLatent)[tid] = o[j];
+            else if (row_off[r] >= 0)
+                *reinterpret_cast<uint2*>(p.o + row_off[r] + tid * 4) =
+                    make_uint2(cvt_bf16x2(o[j].x, o[j].y), cvt_bf16x2(o[j].z, o[j].w));
+        }
+        i = 0;
+        r0 += kBatch;
     }
 }
 
@@ -164,7 +193,8 @@ __device__ void join_rows(const LatentParams& lp, const Parts& parts, int first,
 // group by the last of its CTAs to arrive, and the sums again (attn_tile.cuh).
 template <typename Sync>
 __device__ void join(const LatentParams& lp, const Item& it, const Start& st, int me, int block, int rows,
-                     const int64_t* row_off, const int64_t* row_lse, int* flag, Sync sync) {
+                     const int64_t* row_off, const int64_t* row_lse, float* weights, int* flag,
+                     Sync sync) {
     const Params& p = lp.p;
     const Parts parts = parts_of(p, it, st);
     const int n = parts.last - parts.first + 1, mine = me - parts.first;
@@ -174,11 +204,11 @@ __device__ void join(const LatentParams& lp, const Item& it, const Start& st, in
         if (members == 1) continue;
         const int first = parts.first + head;
         if (!last_of(p.counters + (first + step) * lp.team + block, members, threadIdx.x, flag, sync)) return;
-        if (rows > 0) join_rows<false>(lp, parts, first, step, members, block, rows, row_off, row_lse);
+        if (rows > 0) join_rows<false>(lp, parts, first, step, members, block, rows, row_off, row_lse, weights);
     }
     const int members = (n + step - 1) / step;
     if (last_of(p.counters + (parts.first + step) * lp.team + block, members, threadIdx.x, flag, sync) && rows > 0)
-        join_rows<true>(lp, parts, parts.first, step, members, block, rows, row_off, row_lse);
+        join_rows<true>(lp, parts, parts.first, step, members, block, rows, row_off, row_lse, weights);
 }
 
 template <int kN, bool kTree>
@@ -199,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* rope_full = empty + C::kRing;
     uint64_t* rope_empty = rope_full + C::kRopes;
     uint64_t* s_full = rope_empty + C::kRopes;  // [2]
-    uint64_t* q_full = s_full + 2;
+    uint64_t* s_free = s_full + 2;              // [2]
+    uint64_t* q_full = s_free + 2;
     uint64_t* q_empty = q_full + 1;
     uint64_t* p_full = q_empty + 1;
     uint64_t* pv_done = p_full + 1;
@@ -214,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int me = blockIdx.x / lp.team, block = blockIdx.x % lp.team;
-    constexpr int kMmaWarp = 4, kCopyWarp = 5;
+    constexpr int kMmaWarp = 4, kValueWarp = 5, kCopyWarp = 6;
     if (threadIdx.x == 0) {
         abort_s = 0;
         for (int i = 0; i < C::kRing; ++i) {
@@ -225,8 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&rope_full[i], 1);
             tc::mbar_init(&rope_empty[i], 1);
         }
-        tc::mbar_init(&s_full[0], 1);
-        tc::mbar_init(&s_full[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s_full[i], 1);
+            tc::mbar_init(&s_free[i], 4);
+        }
         tc::mbar_init(q_full, 1);
         tc::mbar_init(q_empty, 1);
         tc::mbar_init(p_full, 4);
@@ -254,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             set_err(p.err, MOE_ERR_TIMEOUT);
             for (Cursor cur = cursor(start); more(cur);) {  // its parts are counted, as if they had been stored
                 const Item it = take(p, cur);
-                if (!it.whole) join(lp, it, start, me, block, 0, row_off, row_lse, &last_s, [] {});
+                if (!it.whole) join(lp, it, start, me, block, 0, row_off, row_lse, nullptr, &last_s, [] {});
             }
         }
         __syncthreads();
@@ -272,10 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     constexpr uint32_t kScores = 4 * kN;  // column of the score buffers, behind O^T
 
-    if (warp == kCopyWarp) {
+    if (warp >= kCopyWarp) {
         // ------------------------------------------------------------ copies
-        int e = 0, re = 0;
-        uint32_t turn = 0, rturn = 0, items = 0, sent = 0, rope_sent = 0, q_sent = 0;
+        const bool first_warp = warp == kCopyWarp;  // takes Q, the rotary blocks and pieces 0 and 1
+        int e = first_warp ? 0 : 2, re = 0;
+        uint32_t tiles = 0, items = 0, q_sent = 0, rope_sent = 0, sent = 0;  // sent: pairs of pieces
         const int box_keys = min(p.page_size, kSub), npg = kSub / box_keys;
         const bool wide = npg == 1;  // a copy takes both column blocks of a piece
         bool more_now = more(cur);
@@ -298,17 +332,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ahead();
                 continue;
             }
-            if (items > 0) wait(q_empty, (items - 1) & 1);
-            ++items;
-            if (!*abort) {
-                ++q_sent;
-                if (lane == 0) tc::mbar_arrive_expect_tx(q_full, kBlocks * p.tokens_per_tile * p.group * 128);
-                __syncwarp();
-                if (lane < kBlocks)
-                    tc::tma_load_3d(qs + lane * kN * 128, &qmap, q_full, lane * 64, block * p.group,
-                                    it.r.row0 + it.tile * p.tokens_per_tile);
+            if (first_warp) {
+                if (items > 0) wait(q_empty, (items - 1) & 1);
+                ++items;
+                if (!*abort) {
+                    ++q_sent;
+                    if (lane == 0) tc::mbar_arrive_expect_tx(q_full, kBlocks * p.tokens_per_tile * p.group * 128);
+                    __syncwarp();
+                    if (lane < kBlocks)
+                        tc::tma_load_3d(qs + lane * kN * 128, &qmap, q_full, lane * 64, block * p.group,
+                                        it.r.row0 + it.tile * p.tokens_per_tile);
+                }
             }
-            for (int k = s.first; k < s.last; ++k) {
+            for (int k = s.first; k < s.last; ++k, ++tiles) {
                 const int key0 = k * kSub;
                 // lane i: page i / (blocks a copy leaves) of the tile
                 const int pg = wide ? 0 : lane >> 1;
@@ -321,26 +357,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool want = in && (!wide || lane == 0), want1 = in && (wide ? lane == 0 : (lane & 1) == 0);
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, want1)) * (box_keys * 128);
-                // the rotary block, and the tile's command
-                if (rturn > 0) wait(&rope_empty[re], (rturn - 1) & 1);
-                if (lane == 0)
-                    cmds[re] = (k == s.first ? kNewQ : 0) | (k == s.last - 1 ? kLast : 0) |
-                               (uint32_t)max(it.s.lo - key0, 0) << kSeenLo |
-                               (uint32_t)min(it.s.hi - key0, kSub) << kSeenHi;
-                if (!*abort) {
-                    ++rope_sent;
-                    if (lane == 0) tc::mbar_arrive_expect_tx(&rope_full[re], bytes);
-                    __syncwarp();
-                    if (want1)
-                        tc::tma_load_4d(ropes + re * kBlockBytes + pg * box_keys * 128, &map1, &rope_full[re], 0, off,
-                                        kLatent / 64, page);
+                if (first_warp) {
+                    // the rotary block, and the tile's command
+                    const uint32_t turn = tiles / C::kRopes;
+                    if (turn > 0) wait(&rope_empty[re], (turn - 1) & 1);
+                    if (lane == 0)
+                        cmds[re] = (k == s.first ? kNewQ : 0) | (k == s.last - 1 ? kLast : 0) |
+                                   (uint32_t)max(it.s.lo - key0, 0) << kSeenLo |
+                                   (uint32_t)min(it.s.hi - key0, kSub) << kSeenHi;
+                    if (!*abort) {
+                        ++rope_sent;
+                        if (lane == 0) tc::mbar_arrive_expect_tx(&rope_full[re], bytes);
+                        __syncwarp();
+                        if (want1)
+                            tc::tma_load_4d(ropes + re * kBlockBytes + pg * box_keys * 128, &map1, &rope_full[re], 0,
+                                            off, kLatent / 64, page);
+                    }
+                    if (++re == C::kRopes) re = 0;
                 }
-                if (++re == C::kRopes) re = 0, ++rturn;
 #pragma unroll 1
-                for (int b = 0; b < kPieces; ++b) {
+                for (int b = first_warp ? 0 : 2, end = b + 2; b < end; ++b) {
+                    const uint32_t turn = (tiles * kPieces + b) / C::kRing;
                     if (turn > 0) wait(&empty[e], (turn - 1) & 1);
                     if (!*abort) {
-                        ++sent;
+                        sent = tiles + 1;
                         if (lane == 0) tc::mbar_arrive_expect_tx(&full[e], 2 * bytes);
                         __syncwarp();
                         uint8_t* dst = ring + e * kPieceBytes;
@@ -352,38 +392,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 0, off, 2 * b + (lane & 1), page);
                         }
                     }
-                    if (++e == C::kRing) e = 0, ++turn;
+                    if (++e >= C::kRing) e -= C::kRing;
                 }
+                e = e + 2 < C::kRing ? e + 2 : e + 2 - C::kRing;  // the other warp's
                 if (k == s.first) ahead();
             }
         }
         if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
-            auto landed = [](uint64_t* bars, int n, uint32_t count) {
-                for (int i = 0; i < n; ++i) {
-                    const uint32_t times = (count + n - 1 - i) / n;  // that entry i has been copied to
-                    if (times > 0) tc::mbar_wait_bounded(&bars[i], (times - 1) & 1);
+            for (int i = 0; i < C::kRopes; ++i) {
+                const uint32_t times = (rope_sent + C::kRopes - 1 - i) / C::kRopes;  // that entry i has been copied to
+                if (times > 0) tc::mbar_wait_bounded(&rope_full[i], (times - 1) & 1);
+            }
+            if (q_sent > 0) tc::mbar_wait_bounded(q_full, (q_sent - 1) & 1);
+            // this warp's pieces of the last tiles; those before lie in the same entries
+            for (uint32_t t = sent, i = 0; t-- > 0 && i < C::kRing / 2; ++i)
+                for (int b = first_warp ? 0 : 2, end = b + 2; b < end; ++b) {
+                    const uint32_t x = t * kPieces + b;
+                    tc::mbar_wait_bounded(&full[x % C::kRing], x / C::kRing & 1);
                 }
-            };
-            landed(full, C::kRing, sent);
-            landed(rope_full, C::kRopes, rope_sent);
-            landed(q_full, 1, q_sent);
         }
-        if (rturn > 0) wait(&rope_empty[re], (rturn - 1) & 1);
-        if (lane == 0) {
-            cmds[re] = kStop;
-            tc::mbar_arrive(&rope_full[re]);
-        }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMAs
+        if (first_warp) {
+            const uint32_t turn = tiles / C::kRopes;
+            if (turn > 0) wait(&rope_empty[re], (turn - 1) & 1);
+            if (lane == 0) {
+                cmds[re] = kStop;
+                tc::mbar_arrive(&rope_full[re]);
+            }
+        }    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ the scores' MMAs
         constexpr uint32_t kIdescS = tc::idesc_bf16_f32(64, kSub);
-        constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, kN) | kIdescAMn;
         int e = 0, re = 0;
-        uint32_t turn = 0, rturn = 0, queries = 0, tiles = 0, weighed = 0;
+        uint32_t turn = 0, rturn = 0, queries = 0, tiles = 0;
         const uint64_t q_desc = tc::desc_sw128_kmajor(tc::smem_u32(qs));
-        const uint64_t p_desc = tc::desc_sw128_kmajor(tc::smem_u32(ps));
         const uint64_t k_desc = tc::desc_sw128_kmajor(tc::smem_u32(ring));
         const uint64_t r_desc = tc::desc_sw128_kmajor(tc::smem_u32(ropes));
-        const uint64_t v_desc = desc_sw128_mnmajor(tc::smem_u32(ring), kBlockBytes);
         auto commit = [&](uint64_t* bar) {
             if (tc::elect_one()) tc::mma_commit(bar);
             __syncwarp();
@@ -393,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&rope_full[re], rturn & 1);
             return cmds[re];
         };
-        // its scores, as its pieces arrive; at: its first piece's entry
-        auto scores = [&](uint32_t cmd, int& at) {
+        // its scores, as its pieces arrive
+        auto scores = [&](uint32_t cmd) {
             if (cmd & kNewQ) wait(q_full, queries++ & 1);
             tc::tc_fence_after();
             const uint32_t to = tmem + kScores + (tiles & 1) * kSub;
@@ -408,7 +450,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (++re == C::kRopes) re = 0, ++rturn;
             const int z0 = cmd >> kSeenLo & 255, z1 = cmd >> kSeenHi & 255;
-            at = e;
 #pragma unroll 1
             for (int c = 0; c < kPieces; ++c) {
                 wait(&full[e], turn & 1);
@@ -438,117 +479,134 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (cmd & kLast) commit(q_empty);
             ++tiles;
         };
-        auto values = [&](uint32_t cmd, int at) {
-            wait(p_full, weighed++ & 1);
-            tc::tc_fence_after();
-            const uint32_t accumulate = cmd & kNewQ ? 0 : 1;
-            if (tc::elect_one()) {
-#pragma unroll 1
-                for (int b = 0; b < kPieces; ++b) {
-                    const uint64_t a = v_desc + (uint32_t)(at * (kPieceBytes >> 4));
-#pragma unroll
-                    for (int s = 0; s < kSub / 16; ++s)
-                        tc::mma_bf16(tmem + b * kN, a + s * (2048 >> 4), p_desc + s * 2, kIdescO, s > 0 ? 1u : accumulate);
-                    tc::mma_commit(&empty[at]);
-                    if (++at == C::kRing) at = 0;
-                }
-                tc::mma_commit(pv_done);
-            }
-            __syncwarp();
-        };
-        int at = 0;
-        uint32_t cmd = next();
-        if (!(cmd & kStop)) scores(cmd, at);
-        while (!(cmd & kStop)) {
-            // within a query tile the next scores go before this tile's product, which waits for its softmax;
-            // those of another query tile wait for its rows, and the product comes first
-            const int was = at;
-            uint32_t then;
-            if (cmd & kLast) {
-                values(cmd, was);
-                then = next();
-                if (!(then & kStop)) scores(then, at);
-            } else {
-                then = next();
-                scores(then, at);
-                values(cmd, was);
-            }
-            cmd = then;
+        for (;;) {
+            const uint32_t cmd = next();
+            if (cmd & kStop) break;
+            if (tiles > 1) wait(&s_free[tiles & 1], (tiles >> 1) - 1 & 1);  // the buffer's scores before have been read
+            scores(cmd);
         }
         commit(done);
         tc::mbar_wait_bounded(done, 0);
+    } else if (warp == kValueWarp) {
+        // ------------------------------------------------------------ the products' MMAs
+        constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, kN) | kIdescAMn;
+        const uint64_t p_desc = tc::desc_sw128_kmajor(tc::smem_u32(ps));
+        const uint64_t v_desc = desc_sw128_mnmajor(tc::smem_u32(ring), kBlockBytes);
+        int at = 0;
+        uint32_t n = 0;  // key tiles so far
+        while (more(cur)) {
+            const Item it = take(p, cur);
+            const Subs s = subs_of(it);
+            for (int k = s.first; k < s.last; ++k, ++n) {
+                wait(p_full, n & 1);
+                tc::tc_fence_after();
+                const uint32_t accumulate = k == s.first ? 0 : 1;
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int b = 0; b < kPieces; ++b) {
+                        const int e = at + b < C::kRing ? at + b : at + b - C::kRing;
+                        const uint64_t a = v_desc + (uint32_t)(e * (kPieceBytes >> 4));
+#pragma unroll
+                        for (int x = 0; x < kSub / 16; ++x)
+                            tc::mma_bf16(tmem + b * kN, a + x * (2048 >> 4), p_desc + x * 2, kIdescO,
+                                         x > 0 ? 1u : accumulate);
+                        tc::mma_commit(&empty[e]);
+                    }
+                    tc::mma_commit(pv_done);
+                }
+                __syncwarp();
+                at = at + kPieces < C::kRing ? at + kPieces : at + kPieces - C::kRing;
+            }
+        }
+        if (n > 0) tc::mbar_wait_bounded(pv_done, (n - 1) & 1);
     } else {
         // ------------------------------------------------------------ softmax and epilogue
         const uint32_t lanes = (uint32_t)warp << 21;  // this warp's quarter of the lanes
-        const int row = warp * 16 + lane;             // in lanes 0-15
-        const bool mine = lane < 16 && row < kN;
-        const bool rows_here = warp * 16 < kN;
+        // scores: rows g and g + 8 of the warp's 16, a quarter of the columns of each
+        const int row0 = warp * 16 + (lane >> 2);
+        const bool rows_here = warp * 16 < kN, speaks = rows_here && (lane & 3) == 0;
         uint32_t n = 0;  // key tiles so far
         while (more(cur)) {
             const Item it = take(p, cur);
             const Subs s = subs_of(it);
             const int rows = it.tokens * p.group;
-            int lo = 0, hi = 0;
-            Branch branch = {0, 0};
-            bool valid;
-            {
-                int64_t off = -1;
-                int token = 0, head = 0;
-                if (mine && row < rows) {
-                    const RowAt at = row_at(p, it, row);
-                    token = at.token;
-                    head = block * p.group + at.head;
-                    if (head < lp.q_heads) off = token * p.o_ld + head * p.o_head;
+            int lo[2] = {0, 0}, hi[2] = {0, 0};
+            Branch branch[2] = {{0, 0}, {0, 0}};
+            bool valid[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = row0 + 8 * i;
+                const RowAt at = row_at(p, it, min(row, rows - 1));
+                const int head = block * p.group + at.head;
+                valid[i] = row < rows && head < lp.q_heads;
+                if (valid[i]) {
+                    const int pos = it.r.kv - it.r.n + (at.token - it.r.row0);
+                    hi[i] = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
+                    lo[i] = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+                    if (kTree) branch[i] = branch_of(p, it.r, at.token);
                 }
-                valid = off >= 0;
-                if (valid) {
-                    const int pos = it.r.kv - it.r.n + (token - it.r.row0);
-                    hi = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
-                    lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-                    if (kTree) branch = branch_of(p, it.r, token);
-                }
-                if (mine) {
-                    row_off[row] = off;
-                    row_lse[row] = (int64_t)token * lp.q_heads + head;
+                if (speaks) {
+                    row_off[row] = valid[i] ? at.token * p.o_ld + head * p.o_head : -1;
+                    row_lse[row] = (int64_t)at.token * lp.q_heads + head;
                 }
             }
             // every row sees keys [lo_all, hi_all): no mask there
             const int pos0 = it.r.kv - it.r.n + it.tile * p.tokens_per_tile;
             const int hi_all = kTree ? max(it.r.kv - it.r.n, 0) : p.causal ? min(it.r.kv, pos0 + 1) : it.r.kv;
             const int lo_all = p.window > 0 ? max(0, pos0 + it.tokens - p.window) : 0;
-            float m = -CUDART_INF_F, l = 0.0f;  // m in powers of two
+            // m in powers of two, the same in the four lanes of a row; l of this lane's columns
+            float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f};
             for (int k = s.first; k < s.last; ++k, ++n) {
                 const int key0 = k * kSub;
-                const bool edge = key0 < lo_all || key0 + kSub > hi_all;
                 wait(&s_full[n & 1], n >> 1 & 1);
                 tc::tc_fence_after();
-                uint32_t x[kSub];
-                float mn = m;
+                uint32_t x[32];
+                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
                 if (rows_here) {
-                    const uint32_t ts = tmem + kScores + (n & 1) * kSub + lanes;
-                    tc::tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-                    tc::tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                    tmem_ld_16x64(tmem + kScores + (n & 1) * kSub + lanes, x);
                     tc::tmem_wait_ld();
-                    if (edge) {
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&s_free[n & 1]);
+                if (rows_here) {
+                    if (key0 < lo_all || key0 + kSub > hi_all) {
+                        const int col = (lane & 3) * 2;
+                        uint32_t seen[2][2];  // of a row, from this lane's first column on: 32 keys, and the next 32
 #pragma unroll
-                        for (int j = 0; j < kSub; ++j) {
-                            const int key = key0 + j;
-                            if (key < lo || key >= hi || (kTree && !branch.sees(key))) x[j] = 0xff800000u;
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                seen[i][u] = kTree && valid[i] ? branch[i].word(key0 + u * 32 + col) : 0u;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int at = (j >> 2) * 8 + (j & 1), key = key0 + col + at, i = j >> 1 & 1;
+                            if (kTree ? !(seen[i][at >> 5] >> (at & 31) & 1) : key < lo[i] || key >= hi[i])
+                                x[j] = 0xff800000u;
                         }
                     }
-                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                    for (int j = 0; j < kSub; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
-                    mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
+                    for (int j = 0; j < 32; ++j) mx[j >> 1 & 1] = fmaxf(mx[j >> 1 & 1], __uint_as_float(x[j]));
                 }
-                const bool move = valid && mn - m > kLoose;  // also from -inf
+                bool move = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mx[i] *= p.scale_log2;
+                    move |= valid[i] && mx[i] - m[i] > kLoose;  // also from -inf
+                }
                 if (k == s.first) {
-                    m = mn;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) m[i] = max_of_4(mx[i]);
                 } else if (any_of_128(move)) {
-                    const float f = move ? exp2_fast(m - mn) : 1.0f;
-                    if (move) m = mn;
-                    l *= f;
-                    if (mine) row_f[row] = f;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float mn = max_of_4(mx[i]);
+                        const bool up = valid[i] && mn - m[i] > kLoose;
+                        const float f = up ? exp2_fast(m[i] - mn) : 1.0f;
+                        if (up) m[i] = mn;
+                        l[i] *= f;
+                        if (speaks) row_f[row0 + 8 * i] = f;
+                    }
                     sync_128();
                     wait(pv_done, (n - 1) & 1);
                     tc::tc_fence_after();
@@ -565,28 +623,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
                 if (rows_here) {
-                    const float base = m == -CUDART_INF_F ? 0.0f : m;
-                    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+                    float2 nb2[2], sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int j = 0; j < kSub / 2; ++j) {
+                    for (int i = 0; i < 2; ++i) {
+                        const float base = m[i] == -CUDART_INF_F ? 0.0f : -m[i];
+                        nb2[i] = make_float2(base, base);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
                         float2 y = make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-                        y = fma2(y, sc2, nb2);
+                        y = fma2(y, sc2, nb2[j & 1]);
                         y.x = exp2_fast(y.x);
                         y.y = exp2_fast(y.y);
                         sum[j & 1] = add2(sum[j & 1], y);
                         x[j] = cvt_bf16x2(y.x, y.y);
                     }
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
+                    l[0] += sum[0].x + sum[0].y;
+                    l[1] += sum[1].x + sum[1].y;
                 }
                 if (n > 0) wait(pv_done, (n - 1) & 1);  // the probabilities before have been read
-                if (mine) {
-                    uint8_t* to = ps + row * 128;
+                if (rows_here) {
+                    uint8_t* to = ps + row0 * 128 + (lane & 3) * 4;  // (row0 + 8) & 7 is row0 & 7
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(to + ((c ^ (row & 7)) << 4)) =
-                            make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                    for (int c = 0; c < 8; ++c) {
+                        const int at = (c ^ (row0 & 7)) << 4;
+                        *reinterpret_cast<uint32_t*>(to + at) = x[2 * c];
+                        *reinterpret_cast<uint32_t*>(to + 1024 + at) = x[2 * c + 1];
+                    }
                     tc::fence_proxy_async_smem();
                 }
                 tc::tc_fence_before();
@@ -599,13 +663,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tc_fence_after();
             }
             const int slot = it.first ? 0 : 1;
-            if (mine) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                const int row = row0 + 8 * i;
+                if (!speaks) continue;
                 if (it.whole) {
-                    row_f[row] = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-                    if (p.lse && row_off[row] >= 0)
-                        p.lse[row_lse[row]] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+                    row_f[row] = l[i] > 0.0f ? 1.0f / l[i] : (l[i] == 0.0f ? 0.0f : l[i]);
+                    if (p.lse && valid[i])
+                        p.lse[row_lse[row]] = l[i] == 0.0f ? -CUDART_INF_F : (m[i] + log2f(l[i])) * 0.6931471805599453f;
                 } else if (row < rows) {
-                    part_ml(p, blockIdx.x, slot)[row] = make_float2(m, l);
+                    part_ml(p, blockIdx.x, slot)[row] = make_float2(m[i], l[i]);
                 }
             }
             sync_128();  // the rows' factors and places
@@ -642,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 lane & 1 ? cvt_bf16x2(got, v1) : cvt_bf16x2(v0, got);
                     }
                 }
-            if (!it.whole) join(lp, it, start, me, block, rows, row_off, row_lse, &last_s, sync_128);
+            if (!it.whole)  // (the probabilities have been read: their place is free)
+                join(lp, it, start, me, block, rows, row_off, row_lse, reinterpret_cast<float*>(ps), &last_s, sync_128);
             tc::tc_fence_before();  // o has been read: the next item's first arrival on p_full says so
             sync_128();             // and the rows' places may be written again
         }

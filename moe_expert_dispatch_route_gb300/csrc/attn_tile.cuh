@@ -761,10 +761,11 @@ __global__ void __launch_bounds__(Cfg<kD, kFp8>::kThreads, 1)
                     tc::tmem_ld32(ts + i * 32, s);
                     tc::tmem_wait_ld();
                     if (edge) {
+                        const uint32_t seen = kTree && valid ? branch.word(key0 + i * 32) : 0u;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int key = key0 + i * 32 + j;
-                            if (masked(key)) s[j] = 0xff800000u;
+                            if (kTree ? !(seen >> j & 1) : key < lo || key >= hi) s[j] = 0xff800000u;
                         }
                     }
                 };
