@@ -112,103 +112,154 @@ __device__ __forceinline__ float max_of_4(float v) {  // of the lanes that share
 }
 __device__ __forceinline__ void sync_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// The softmax warps: the sum of n parts of a split tile, those of CTAs first, first + step, ..., in this
-// order, four columns a thread.  kEnd: it goes to the output, otherwise to the place of the first part.
-// weights: shared, kFan * 64 floats.  kBatch rows of a part are loaded at a time, those of the next part (or of
-// the first one's next rows) while these are added: two rows of all parts at a time, a join of two parts of
-// 64 rows took 50 us.
-constexpr int kFan = 4;  // the most parts summed together
-template <bool kEnd>
-__device__ __noinline__ void join_rows(const LatentParams& lp, const Parts& parts, int first, int step, int n, int block,
-                                       int rows, const int64_t* row_off, const int64_t* row_lse, float* weights) {
-    const Params& p = lp.p;
-    auto cta = [&](int i) { return (first + i * step) * lp.team + block; };
-    auto slot = [&](int i) { return part_slot(parts, first + i * step); };
-    const int tid = threadIdx.x;
-    constexpr int kBatch = 8;
-    float4 next[kBatch];
-    int load_r = 0, load_i = 0;
-    auto load = [&] {
-        if (load_r >= rows) return;
-        const float4* from =
-            reinterpret_cast<const float4*>(part_o(p, cta(load_i), slot(load_i)) + load_r * kLatent) + tid;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (load_r + j < rows) next[j] = __ldcg(from + j * (kLatent / 4));
-        if (++load_i == n) load_i = 0, load_r += kBatch;
-    };
-    load();
-    if (tid < rows) {
-        float2 ml[kFan];
-        float m = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kFan; ++i)
-            ml[i] = i < n ? __ldcg(part_ml(p, cta(i), slot(i)) + tid) : make_float2(-CUDART_INF_F, 0.0f);
-#pragma unroll
-        for (int i = 0; i < kFan; ++i) m = fmaxf(m, ml[i].x);
-        const float to = m == -CUDART_INF_F ? 0.0f : m;
-#pragma unroll
-        for (int i = 0; i < kFan; ++i) l += ml[i].y * exp2_fast(ml[i].x - to);
-        const float inv = !kEnd ? 1.0f : l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-        for (int i = 0; i < kFan; ++i) weights[i * 64 + tid] = exp2_fast(ml[i].x - to) * inv;
-        if (!kEnd)
-            part_ml(p, cta(0), slot(0))[tid] = make_float2(m, l);  // read by this thread alone before
-        else if (p.lse && row_off[tid] >= 0)
-            p.lse[row_lse[tid]] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-    }
-    sync_128();
-    float4 o[kBatch];
-#pragma unroll 1
-    for (int r0 = 0, i = 0; r0 < rows;) {
-        float4 x[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) x[j] = next[j];
-        load();
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const float w = weights[i * 64 + min(r0 + j, rows - 1)];
-            if (i == 0) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w == 0.0f) continue;  // a part without keys, or a sum of 0: its numbers may be anything
-            o[j].x += x[j].x * w, o[j].y += x[j].y * w;
-            o[j].z += x[j].z * w, o[j].w += x[j].w * w;
-        }
-        if (++i < n) continue;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int r = r0 + j;
-            if (r >= rows) break;
-            if (!kEnd)
-                reinterpret_cast<float4*>(part_o(p, cta(0), slot(0)) + r * kLatent)[tid] = o[j];
-            else if (row_off[r] >= 0)
-                *reinterpret_cast<uint2*>(p.o + row_off[r] + tid * 4) =
-                    make_uint2(cvt_bf16x2(o[j].x, o[j].y), cvt_bf16x2(o[j].z, o[j].w));
-        }
-        i = 0;
-        r0 += kBatch;
-    }
+// What the second kernel has to know of a part, behind its sums in the workspace.  Every CTA writes those of
+// its two slots in every call.
+struct PartHead {
+    int n;        // parts of the tile, 0: no part in this slot
+    int rank;     // of this one among them
+    int first;    // the CTA with the first one (in its slot 0; the others are in slot 1)
+    int rows;     // of the tile
+    int token;    // its first row of q
+    int block;    // which of the heads' blocks
+};
+__device__ __forceinline__ PartHead* part_head(const Params& p, int cta, int slot) {
+    return reinterpret_cast<PartHead*>(part_ml(p, cta, slot) + 64);
 }
 
-// The softmax warps of a CTA whose part of a split tile is stored: parts are summed kFan at a time, each
-// group by the last of its CTAs to arrive, and the sums again (attn_tile.cuh).
-template <typename Sync>
-__device__ void join(const LatentParams& lp, const Item& it, const Start& st, int me, int block, int rows,
-                     const int64_t* row_off, const int64_t* row_lse, float* weights, int* flag,
-                     Sync sync) {
+// Split tiles, put together: the CTAs of a slot each take a share of their tile's output, so that a long context's
+// many parts are read by as many CTAs.  (Joined by the last CTA to arrive, as in attn_tile.cuh, a tile of 64 rows took
+// its CTA 15 to 30 us, 128 KB a part from a busy memory, and one request of 100000 tokens three times that.)
+// A thread takes four columns of a row; a small share with many parts is shared by several groups of
+// threads, whose sums are added in order.
+constexpr int kJoinThreads = 512;
+constexpr int kMostParts = 160;  // of a tile, and CTAs of a call
+__global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __grid_constant__ LatentParams lp) {
     const Params& p = lp.p;
-    const Parts parts = parts_of(p, it, st);
-    const int n = parts.last - parts.first + 1, mine = me - parts.first;
-    int step = 1;
-    for (; step * kFan < n; step *= kFan) {
-        const int head = mine / (step * kFan) * (step * kFan), members = min(kFan, (n - head + step - 1) / step);
-        if (members == 1) continue;
-        const int first = parts.first + head;
-        if (!last_of(p.counters + (first + step) * lp.team + block, members, threadIdx.x, flag, sync)) return;
-        if (rows > 0) join_rows<false>(lp, parts, first, step, members, block, rows, row_off, row_lse, weights);
+    __shared__ float weights[64 + 2 * kMostParts];  // [row of the share][part]
+    __shared__ float4 sums[kJoinThreads];
+    pdl_begin();
+    const int cta = blockIdx.x >> 1, slot = blockIdx.x & 1, tid = threadIdx.x;
+    const PartHead h = *part_head(p, cta, slot);
+    if (h.n == 0) return;
+    constexpr int kPer = kLatent / 4;
+    const int total = h.rows * kPer, e0 = (int)((int64_t)total * h.rank / h.n);
+    const int count = (int)((int64_t)total * (h.rank + 1) / h.n) - e0;
+    if (count == 0) return;
+    const uint8_t* base = p.parts + ((size_t)h.first * 2 + 1) * kPartBytes;
+    const size_t stride = (size_t)lp.team * 2 * kPartBytes;
+    auto part_at = [&](int i) { return base + i * stride - (i == 0 ? kPartBytes : 0); };
+    auto ml_at = [&](int i, int r) {
+        return __ldcg(reinterpret_cast<const float2*>(part_at(i) + (size_t)kMaxRows * 128 * 4) + r);
+    };
+    const int r0 = e0 / kPer, nrows = (e0 + count - 1) / kPer - r0 + 1;
+    auto load = [&](int i, int e) { return __ldcg(reinterpret_cast<const float4*>(part_at(i)) + e); };
+    int groups = 1;
+    while (groups * 2 * count <= kJoinThreads && groups * 4 <= h.n) groups *= 2;
+    // the first numbers are on their way while the weights are found: a chain of two loads in all
+    constexpr int kE = 8, kI = 2;  // elements and parts under way together
+    float4 x[kE][kI];
+    auto fetch = [&](int at, int i0) {
+#pragma unroll
+        for (int u = 0; u < kE; ++u)
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+                if (at + u * kJoinThreads < count && i0 + i < h.n) x[u][i] = load(i0 + i, e0 + at + u * kJoinThreads);
+    };
+    if (groups == 1) fetch(tid, 0);
+    // a warp a row, a lane a part (or several): its weight
+    constexpr int kPerLane = kMostParts / 32, kPerWarp = 64 / (kJoinThreads / 32);
+    const int lane = tid & 31;
+    auto weigh = [&](int row, const float2 (&ml)[kPerLane], int parts) {
+        float m = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) m = i < parts ? fmaxf(m, ml[i].x) : m;
+        m = warp_max(m);
+        const float to = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) l += i < parts ? ml[i].y * exp2_fast(ml[i].x - to) : 0.0f;
+        l = warp_sum(l);
+        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (i < parts) weights[(row - r0) * h.n + i * 32 + lane] = exp2_fast(ml[i].x - to) * inv;
+        const int token = h.token + row / p.group, head = h.block * p.group + row % p.group;
+        if (lane == 0 && p.lse && head < lp.q_heads && row * kPer >= e0 && row * kPer < e0 + count)
+            p.lse[(int64_t)token * lp.q_heads + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+    };
+    const int parts = h.n > lane ? (h.n - lane + 31) / 32 : 0;  // of this lane
+    if (h.n <= 32) {
+        float2 ml[kPerWarp];
+#pragma unroll
+        for (int k = 0; k < kPerWarp; ++k) {
+            const int r = (tid >> 5) + k * (kJoinThreads / 32);
+            if (r < nrows && parts > 0) ml[k] = ml_at(lane, r0 + r);
+        }
+#pragma unroll
+        for (int k = 0; k < kPerWarp; ++k) {
+            const int r = (tid >> 5) + k * (kJoinThreads / 32);
+            if (r < nrows) {
+                const float2 one[kPerLane] = {ml[k]};
+                weigh(r0 + r, one, min(parts, 1));
+            }
+        }
+    } else if (tid >> 5 < nrows) {  // a share of at most 3 rows
+        float2 ml[kPerLane];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (i < parts) ml[i] = ml_at(i * 32 + lane, r0 + (tid >> 5));
+        weigh(r0 + (tid >> 5), ml, parts);
     }
-    const int members = (n + step - 1) / step;
-    if (last_of(p.counters + (parts.first + step) * lp.team + block, members, threadIdx.x, flag, sync) && rows > 0)
-        join_rows<true>(lp, parts, parts.first, step, members, block, rows, row_off, row_lse, weights);
+    __syncthreads();
+    auto out = [&](int e, float4 o) {
+        const int row = e / kPer, token = h.token + row / p.group, head = h.block * p.group + row % p.group;
+        if (head < lp.q_heads)
+            *reinterpret_cast<uint2*>(p.o + token * p.o_ld + head * p.o_head + e % kPer * 4) =
+                make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
+    };
+    auto add = [](float4& o, float4 x, float w) {
+        if (w == 0.0f) return;  // a part without keys for this row: its numbers may be anything
+        o.x += x.x * w, o.y += x.y * w, o.z += x.z * w, o.w += x.w * w;
+    };
+    if (groups == 1) {
+        for (int at = tid; at < count; at += kE * kJoinThreads) {
+            float4 o[kE];
+#pragma unroll
+            for (int u = 0; u < kE; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < h.n; i0 += kI) {
+                if (at >= kE * kJoinThreads || i0 > 0) fetch(at, i0);
+#pragma unroll
+                for (int u = 0; u < kE; ++u)
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+                        if (at + u * kJoinThreads < count && i0 + i < h.n)
+                            add(o[u], x[u][i], weights[((e0 + at + u * kJoinThreads) / kPer - r0) * h.n + i0 + i]);
+            }
+#pragma unroll
+            for (int u = 0; u < kE; ++u)
+                if (at + u * kJoinThreads < count) out(e0 + at + u * kJoinThreads, o[u]);
+        }
+        return;
+    }
+    const int per = kJoinThreads / groups, g = tid / per, at = tid % per;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (at < count) {
+        const float* w = weights + ((e0 + at) / kPer - r0) * h.n;
+        for (int i0 = g; i0 < h.n; i0 += kE * groups) {
+            float4 y[kE];
+#pragma unroll
+            for (int i = 0; i < kE; ++i)
+                if (i0 + i * groups < h.n) y[i] = load(i0 + i * groups, e0 + at);
+#pragma unroll
+            for (int i = 0; i < kE; ++i)
+                if (i0 + i * groups < h.n) add(o, y[i], w[i0 + i * groups]);
+        }
+    }
+    sums[tid] = o;
+    __syncthreads();
+    if (g == 0 && at < count) {
+        for (int i = 1; i < groups; ++i) add(o, sums[i * per + at], 1.0f);
+        out(e0 + at, o);
+    }
 }
 
 template <int kN, bool kTree>
@@ -239,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* row_f = reinterpret_cast<float*>(never + 1);  // a row's factor
     uint32_t* cmds = reinterpret_cast<uint32_t*>(row_f + kN);
     __shared__ Start start;
-    __shared__ int abort_s, last_s;
+    __shared__ int abort_s;
     __shared__ uint32_t tmem_s;
     volatile int* abort = &abort_s;
 
@@ -281,14 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     locate<kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start, me, gridDim.x / lp.team);
     tc::tc_fence_after();
     const uint32_t tmem = tmem_s;
+    if (threadIdx.x < 2) part_head(p, blockIdx.x, threadIdx.x)->n = 0;
+    __syncthreads();
     if (p.inject_ns > 0 && blockIdx.x == 0) {  // test hook: the failure path of a bounded wait
         if (threadIdx.x == 0) {
             tc::wait_on_nothing(never, (uint64_t)p.inject_ns);
             set_err(p.err, MOE_ERR_TIMEOUT);
-            for (Cursor cur = cursor(start); more(cur);) {  // its parts are counted, as if they had been stored
-                const Item it = take(p, cur);
-                if (!it.whole) join(lp, it, start, me, block, 0, row_off, row_lse, nullptr, &last_s, [] {});
-            }
         }
         __syncthreads();
         if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
@@ -312,6 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t tiles = 0, items = 0, q_sent = 0, rope_sent = 0, sent = 0;  // sent: pairs of pieces
         const int box_keys = min(p.page_size, kSub), npg = kSub / box_keys;
         const bool wide = npg == 1;  // a copy takes both column blocks of a piece
+        // parts of split tiles stay in L2 until they are joined, beside the keys that stream through it
+        const uint64_t once = tc::policy_evict_first();
         bool more_now = more(cur);
         Item it, after;
         Pages pages, pages_after;
@@ -370,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) tc::mbar_arrive_expect_tx(&rope_full[re], bytes);
                         __syncwarp();
                         if (want1)
-                            tc::tma_load_4d(ropes + re * kBlockBytes + pg * box_keys * 128, &map1, &rope_full[re], 0,
-                                            off, kLatent / 64, page);
+                            tc::tma_load_4d_hint(ropes + re * kBlockBytes + pg * box_keys * 128, &map1, &rope_full[re],
+                                                 0, off, kLatent / 64, page, once);
                     }
                     if (++re == C::kRopes) re = 0;
                 }
@@ -386,10 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint8_t* dst = ring + e * kPieceBytes;
                         if (want) {
                             if (wide)
-                                tc::tma_load_4d(dst, &map2, &full[e], 0, off, 2 * b, page);
+                                tc::tma_load_4d_hint(dst, &map2, &full[e], 0, off, 2 * b, page, once);
                             else
-                                tc::tma_load_4d(dst + (lane & 1) * kBlockBytes + pg * box_keys * 128, &map1, &full[e],
-                                                0, off, 2 * b + (lane & 1), page);
+                                tc::tma_load_4d_hint(dst + (lane & 1) * kBlockBytes + pg * box_keys * 128, &map1,
+                                                     &full[e], 0, off, 2 * b + (lane & 1), page, once);
                         }
                     }
                     if (++e >= C::kRing) e -= C::kRing;
@@ -711,8 +762,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 lane & 1 ? cvt_bf16x2(got, v1) : cvt_bf16x2(v0, got);
                     }
                 }
-            if (!it.whole)  // (the probabilities have been read: their place is free)
-                join(lp, it, start, me, block, rows, row_off, row_lse, reinterpret_cast<float*>(ps), &last_s, sync_128);
+            if (!it.whole && threadIdx.x == 0) {
+                const Parts parts = parts_of(p, it, start);
+                *part_head(p, blockIdx.x, slot) = {parts.last - parts.first + 1, me - parts.first,
+                                                   parts.first * lp.team + block, rows,
+                                                   it.r.row0 + it.tile * p.tokens_per_tile, block};
+            }
             tc::tc_fence_before();  // o has been read: the next item's first arrival on p_full says so
             sync_128();             // and the rows' places may be written again
         }
@@ -757,7 +812,8 @@ cudaError_t launch_as(const moe_latent_cache& c, const LatentParams& lp, int gri
     auto kern = attn_latent_kernel<kN, kTree>;
     cudaError_t e = ensure_max_dynamic_smem(kern, Cfg<kN>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid, kThreads, Cfg<kN>::kSmem, st, lp, qm, m1, m2);
+    e = launch_pdl(kern, grid, kThreads, Cfg<kN>::kSmem, st, lp, qm, m1, m2);
+    return e == cudaSuccess ? launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp) : e;
 }
 template <bool kTree>
 cudaError_t launch_of(const moe_latent_cache& c, const LatentParams& lp, int rows, int grid, cudaStream_t st) {
@@ -811,7 +867,7 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
     p.item_cost = 2;
     p.item_slack = 1;
     p.cta_units = 2;
-    if (grid_cap > kMaxCtas) grid_cap = kMaxCtas;
+    if (grid_cap > kMostParts) grid_cap = kMostParts;
     const int teams = grid_cap / lp.team < 1 ? 1 : grid_cap / lp.team;
     int grid = grid_for(p, teams);
     const int fit = device_info().num_sms / lp.team;
