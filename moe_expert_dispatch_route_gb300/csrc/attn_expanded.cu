@@ -6,12 +6,18 @@
 // Scores, probabilities and output fill tensor memory as there (S0 | S1 | O0 | O1, P over S).
 //
 // Q takes 96 KB, so the ring holds 128 KB, less than two key tiles (80 KB).  Its entries are 16 KB pieces, each
-// copied and given back by itself: a key tile's three blocks of 64 columns, and the halves of 64 keys of
-// its values.
+// given back by itself: a key tile's three blocks of 64 columns, and the halves of 64 keys of its values.  They
+// arrive on one barrier for a tile's keys and one for its values: the issuing warp's waits, even those for what
+// is there already, stand between the MMAs.
+//
+// The softmax reads the scores once, 32 keys at a time: their maximum, then their probabilities relative to the
+// maximum in use, which is a whole power of two.  Where a maximum is 2^8 times above that one, what refers to it
+// already (o, the sum, and the tile's probabilities so far) is multiplied by a power of two, which rounds nothing.
 //
 //   warps 0-3, 4-7   softmax and epilogue of half 0, 1 (a thread owns a row)
 //   warp 8           issues the MMAs
-//   warp 9           copies
+//   warps 9-11       copies: keys, values, shared keys and Q (one warp took 800 cycles a piece, 4000 a key tile, and
+//                    bounded the kernel: 2166 us)
 #include "attn_tile.cuh"
 
 namespace moe {
@@ -23,8 +29,8 @@ constexpr int kXThreads = 384;
 constexpr int kPieceBytes = 16384;
 constexpr int kHalfBytes = 3 * kHalfRows * 128;  // of Q
 constexpr int kRingPieces = 8;
-constexpr int kXBars = 2 * kRingPieces + 2 + 6 + 2;
-constexpr int kXSmem = 1024 + 2 * kHalfBytes + kRingPieces * kPieceBytes + 8 * kXBars + 4 * kRingPieces;
+constexpr int kXBars = kRingPieces + 4 + 2 + 6 + 2;
+constexpr int kXSmem = 1024 + 2 * kHalfBytes + kRingPieces * kPieceBytes + 8 * kXBars + 8;
 static_assert(kXSmem <= 232448 - 512, "");
 
 __global__ void __launch_bounds__(kXThreads, 1)
@@ -34,16 +40,17 @@ __global__ void __launch_bounds__(kXThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* qs = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);  // by an offset: accesses keep 32-bit addresses
     uint8_t* ring = qs + 2 * kHalfBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + kRingPieces * kPieceBytes);
-    uint64_t* empty = full + kRingPieces;
-    uint64_t* q_full = empty + kRingPieces;
+    uint64_t* empty = reinterpret_cast<uint64_t*>(ring + kRingPieces * kPieceBytes);  // of each piece
+    uint64_t* k_full = empty + kRingPieces;  // [2] of a tile's keys, by the tile's parity
+    uint64_t* v_full = k_full + 2;           // [2] of its values
+    uint64_t* q_full = v_full + 2;
     uint64_t* q_empty = q_full + 1;
     uint64_t* s_full = q_empty + 1;  // [2] scores of a half are in tensor memory
     uint64_t* p_full = s_full + 2;   // [2] its probabilities are
     uint64_t* pv_done = p_full + 2;  // [2] they have been multiplied into o
     uint64_t* done = pv_done + 2;
     uint64_t* never = done + 1;
-    uint32_t* cmds = reinterpret_cast<uint32_t*>(never + 1);  // of a key tile, beside its first piece
+    uint32_t* cmds = reinterpret_cast<uint32_t*>(never + 1);  // [2] of a key tile
     __shared__ Start start;
     __shared__ Cursor cursors[2];  // where the two softmax groups stand: not held in registers
     __shared__ int abort_s, last_s;
@@ -54,13 +61,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
     constexpr int kMmaWarp = 8, kCopyWarp = 9;
     if (threadIdx.x == 0) {
         abort_s = 0;
-        for (int i = 0; i < kRingPieces; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
-        }
+        for (int i = 0; i < kRingPieces; ++i) tc::mbar_init(&empty[i], 1);
         tc::mbar_init(q_full, 1);
         tc::mbar_init(q_empty, 1);
         for (int h = 0; h < 2; ++h) {
+            tc::mbar_init(&k_full[h], 2);
+            tc::mbar_init(&v_full[h], 1);
             tc::mbar_init(&s_full[h], 1);
             tc::mbar_init(&p_full[h], 4);
             tc::mbar_init(&pv_done[h], 1);
@@ -107,59 +113,60 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
     if (warp >= kMmaWarp) {
         regs_dec<120>();
-        if (warp == kCopyWarp) {
+        if (warp >= kCopyWarp) {
             // -------------------------------------------------------- copies
-            uint32_t at = 0;  // pieces so far
-            uint32_t items = 0, sent = 0, q_sent = 0;
-            // the next piece's place, once it is free; `bytes` are announced
-            auto piece = [&](uint32_t bytes) -> uint8_t* {
-                const uint32_t e = at % kRingPieces;
-                if (at >= kRingPieces) wait(&empty[e], (at / kRingPieces - 1) & 1);
-                if (*abort) return nullptr;
-                ++sent;
-                if (lane == 0) tc::mbar_arrive_expect_tx(&full[e], bytes);
-                return ring + e * kPieceBytes;
-            };
+            // of a key tile's five pieces: 0 and 1 (keys), 3 and 4 (values), 2 (shared keys) and Q
+            const int role = warp - kCopyWarp, b0 = role == 0 ? 0 : role == 1 ? 3 : 2, b1 = role == 2 ? 3 : b0 + 2;
+            uint32_t tiles = 0, sent = 0, items = 0, q_sent = 0;
             while (more(cur)) {
                 const Item it = take(p, cur);
                 if (it.n == 0) continue;
                 const Halves v = halves(p, it);
                 const int row0 = it.r.row0 + it.tile * p.tokens_per_tile, key_row0 = p.cu_kv[it.b];
-                if (items > 0) wait(q_empty, (items - 1) & 1);
-                ++items;
-                if (!*abort) {
-                    ++q_sent;
-                    if (lane == 0) {
-                        tc::mbar_arrive_expect_tx(q_full, v.count * kHalfBytes);
-                        for (int h = 0; h < v.count; ++h)
-                            for (int b = 0; b < 3; ++b)
-                                tc::tma_load_3d(qs + (h * 3 + b) * kHalfRows * 128, &qmap, q_full, b * 64, it.head,
-                                                row0 + h * kHalfRows);
+                if (role == 2) {
+                    if (items > 0) wait(q_empty, (items - 1) & 1);
+                    ++items;
+                    if (!*abort) {
+                        ++q_sent;
+                        if (lane == 0) {
+                            tc::mbar_arrive_expect_tx(q_full, v.count * kHalfBytes);
+                            for (int h = 0; h < v.count; ++h)
+                                for (int b = 0; b < 3; ++b)
+                                    tc::tma_load_3d(qs + (h * 3 + b) * kHalfRows * 128, &qmap, q_full, b * 64, it.head,
+                                                    row0 + h * kHalfRows);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
-                for (int k = 0; k < it.n; ++k) {
+                for (int k = 0; k < it.n; ++k, ++tiles) {
                     const int kt = it.k0 + k, key0 = kt * kKeyTile, row = key_row0 + key0;
-                    uint32_t cmd = (uint32_t)min(it.s.hi - key0, kKeyTile) << kSeenHi;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (active(v, h, kt)) cmd |= kAct0 << h | (kt == v.k0[h] ? kFirst0 << h : 0);
-                    if (k == 0) cmd |= kNewQ;
-                    if (k == it.n - 1) cmd |= kLastK;
                     // (rows past the last key's are the next request's, or past the tensor: zeros)
 #pragma unroll 1
-                    for (int b = 0; b < 5; ++b, ++at) {
-                        const uint32_t e = at % kRingPieces;
-                        uint8_t* dst = piece(kPieceBytes);
-                        if (lane == 0 && b == 0) cmds[e] = cmd;
-                        if (dst && lane == 0) {
+                    for (int b = b0; b < b1; ++b) {
+                        const uint32_t at = tiles * 5 + b, e = at % kRingPieces;
+                        if (at >= kRingPieces) wait(&empty[e], (at / kRingPieces - 1) & 1);
+                        if (b == 0) {
+                            uint32_t cmd = (uint32_t)min(it.s.hi - key0, kKeyTile) << kSeenHi;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (active(v, h, kt)) cmd |= kAct0 << h | (kt == v.k0[h] ? kFirst0 << h : 0);
+                            if (k == 0) cmd |= kNewQ;
+                            if (k == it.n - 1) cmd |= kLastK;
+                            if (lane == 0) cmds[tiles & 1] = cmd;
+                        }
+                        if (*abort) continue;
+                        sent = tiles + 1;
+                        if (lane == 0) {
+                            uint8_t* dst = ring + e * kPieceBytes;
+                            uint64_t* bar = role == 1 ? &v_full[tiles & 1] : &k_full[tiles & 1];
+                            if (b == b0) tc::mbar_arrive_expect_tx(bar, (b1 - b0) * kPieceBytes);
                             if (b < 2) {
-                                tc::tma_load_3d(dst, &kmap, &full[e], b * 64, it.head, row);
+                                tc::tma_load_3d(dst, &kmap, bar, b * 64, it.head, row);
                             } else if (b == 2) {
-                                tc::tma_load_2d(dst, &rmap, &full[e], 0, row);
+                                tc::tma_load_2d(dst, &rmap, bar, 0, row);
                             } else {
-                                tc::tma_load_3d(dst, &vmap, &full[e], 0, it.head, row + (b - 3) * 64);
-                                tc::tma_load_3d(dst + kPieceBytes / 2, &vmap, &full[e], 64, it.head, row + (b - 3) * 64);
+                                tc::tma_load_3d(dst, &vmap, bar, 0, it.head, row + (b - 3) * 64);
+                                tc::tma_load_3d(dst + kPieceBytes / 2, &vmap, bar, 64, it.head, row + (b - 3) * 64);
                             }
                         }
                         __syncwarp();
@@ -167,33 +174,33 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             if (*abort) {  // copies still in flight land (or a bounded wait gives up) before the CTA ends
-                for (uint32_t i = 0; i < kRingPieces; ++i) {
-                    const uint32_t times = (sent + kRingPieces - 1 - i) / kRingPieces;  // that entry i has been copied to
-                    if (times > 0) tc::mbar_wait_bounded(&full[i], (times - 1) & 1);
-                }
+                for (uint32_t t = sent, i = 0; t-- > 0 && i < 2; ++i)
+                    tc::mbar_wait_bounded(role == 1 ? &v_full[t & 1] : &k_full[t & 1], t >> 1 & 1);
                 if (q_sent > 0) tc::mbar_wait_bounded(q_full, (q_sent - 1) & 1);
             }
-            const uint32_t e = at % kRingPieces;
-            if (at >= kRingPieces) wait(&empty[e], (at / kRingPieces - 1) & 1);
-            if (lane == 0) {
-                cmds[e] = kStop;
-                tc::mbar_arrive(&full[e]);
+            if (role != 1) {
+                const uint32_t at = tiles * 5;
+                if (at >= kRingPieces) wait(&empty[at % kRingPieces], (at / kRingPieces - 1) & 1);
+                if (lane == 0) {
+                    if (role == 0) cmds[tiles & 1] = kStop;
+                    tc::mbar_arrive(&k_full[tiles & 1]);
+                }
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMAs
             constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, kKeyTile);
             constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, kValueCols) | kIdescBMn;
             uint32_t at = 0;  // the next piece
-            uint32_t queries = 0, np0 = 0, np1 = 0;
+            uint32_t tiles = 0, queries = 0, np0 = 0, np1 = 0;  // tiles: key tiles begun
             const uint64_t q_desc = tc::desc_sw128_kmajor(tc::smem_u32(qs));
             const uint64_t k_desc = tc::desc_sw128_kmajor(tc::smem_u32(ring));
             const uint64_t v_desc = desc_sw128_mnmajor(tc::smem_u32(ring), kPieceBytes / 2);
-            auto arrived = [&](uint32_t i) { wait(&full[i % kRingPieces], i / kRingPieces & 1); };
             auto commit = [&](uint64_t* bar) {
                 if (tc::elect_one()) tc::mma_commit(bar);
                 __syncwarp();
             };
-            auto scores = [&](int h, uint32_t first) {  // S_h = Q_h K^T from the pieces at `first`
+            // S_h = Q_h K^T from the pieces at `first`; the last half to use them gives each back as it goes
+            auto scores = [&](int h, uint32_t first, bool release) {
                 if (tc::elect_one()) {
                     const uint64_t a = q_desc + (uint32_t)(h * (kHalfBytes >> 4));
 #pragma unroll
@@ -203,53 +210,49 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         for (int s = 0; s < 4; ++s)
                             tc::mma_bf16(tmem + h * 128, a + b * (kHalfRows * 128 >> 4) + s * 2, k + s * 2, kIdescS,
                                          b + s > 0);
+                        if (release) tc::mma_commit(&empty[(first + b) % kRingPieces]);
                     }
                     tc::mma_commit(&s_full[h]);
                 }
                 __syncwarp();
             };
-            auto values = [&](int h, uint32_t first, uint32_t accumulate) {  // O_h (+)= P_h V
+            auto values = [&](int h, uint32_t first, uint32_t accumulate, bool release) {  // O_h (+)= P_h V
                 if (tc::elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < kKeyTile / 16; ++s)
+                    for (int s = 0; s < kKeyTile / 16; ++s) {
                         mma_bf16_ta(tmem + 256 + h * 128, tmem + h * 128 + s * 8,
                                     v_desc + (first + s / 4) % kRingPieces * (kPieceBytes >> 4) + s % 4 * (2048 >> 4),
                                     kIdescO, s > 0 ? 1u : accumulate);
+                        if (release && s % 4 == 3) tc::mma_commit(&empty[(first + s / 4) % kRingPieces]);
+                    }
                     tc::mma_commit(&pv_done[h]);
                 }
                 __syncwarp();
             };
             // the key tile at `at` is there: its command, with Q there too
             auto keys = [&]() -> uint32_t {
-                arrived(at);
-                const uint32_t cmd = cmds[at % kRingPieces];
+                wait(&k_full[tiles & 1], tiles >> 1 & 1);
+                const uint32_t cmd = cmds[tiles & 1];
                 if (cmd & kStop) return cmd;
-                arrived(at + 1);
-                arrived(at + 2);
                 if (cmd & kNewQ) wait(q_full, queries++ & 1);
                 tc::tc_fence_after();
                 return cmd;
             };
             auto keys_done = [&](uint32_t cmd) {
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) tc::mma_commit(&empty[(at + b) % kRingPieces]);
-                    if (cmd & kLastK) tc::mma_commit(q_empty);
-                }
-                __syncwarp();
+                if (cmd & kLastK) commit(q_empty);
+                ++tiles;
                 at += 3;
             };
             uint32_t cmd = keys();
             if (!(cmd & kStop)) {
-                if (cmd & kAct0) scores(0, at);
-                if (cmd & (kAct0 << 1)) scores(1, at);
+                if (cmd & kAct0) scores(0, at, !(cmd & (kAct0 << 1)));
+                if (cmd & (kAct0 << 1)) scores(1, at, true);
                 keys_done(cmd);
             }
             while (!(cmd & kStop)) {
                 const uint32_t va = at;
                 at += 2;
-                arrived(va);
-                arrived(va + 1);
+                wait(&v_full[(tiles - 1) & 1], (tiles - 1) >> 1 & 1);
                 const int z1 = cmd >> kSeenHi & 255;
                 if (z1 < kKeyTile) {
                     // what lies behind the request's keys may be anything, NaN among it: 0 * NaN would reach o
@@ -269,27 +272,22 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 if (cmd & kAct0) {
                     wait(&p_full[0], np0++ & 1);
                     tc::tc_fence_after();
-                    values(0, va, cmd & kFirst0 ? 0 : 1);
+                    values(0, va, cmd & kFirst0 ? 0 : 1, !(cmd & (kAct0 << 1)));
                 }
                 if (!last) {
                     then = keys();
-                    if (then & kAct0) scores(0, at);
+                    if (then & kAct0) scores(0, at, !(then & (kAct0 << 1)));
                 }
                 if (cmd & (kAct0 << 1)) {
                     wait(&p_full[1], np1++ & 1);
                     tc::tc_fence_after();
-                    values(1, va, cmd & (kFirst0 << 1) ? 0 : 1);
+                    values(1, va, cmd & (kFirst0 << 1) ? 0 : 1, true);
                 }
-                if (tc::elect_one()) {
-                    tc::mma_commit(&empty[va % kRingPieces]);
-                    tc::mma_commit(&empty[(va + 1) % kRingPieces]);
-                }
-                __syncwarp();
                 if (last) {
                     then = keys();
-                    if (then & kAct0) scores(0, at);
+                    if (then & kAct0) scores(0, at, !(then & (kAct0 << 1)));
                 }
-                if (then & (kAct0 << 1)) scores(1, at);
+                if (then & (kAct0 << 1)) scores(1, at, true);
                 if (!(then & kStop)) keys_done(then);
                 cmd = then;
             }
@@ -321,10 +319,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 const int key0 = kt * kKeyTile;
                 wait(&s_full[h], n & 1);
                 tc::tc_fence_after();
-                // read twice, in rolled loops, as in attn_tile.cuh
                 const bool edge = key0 + kKeyTile > hi_all;
-                uint32_t s[32];
-                auto load = [&](int i) {
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t s[32], out[16];
                     tc::tmem_ld32(ts + i * 32, s);
                     tc::tmem_wait_ld();
                     if (edge) {
@@ -332,41 +331,43 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             if (key0 + i * 32 + j >= hi) s[j] = 0xff800000u;
                     }
-                };
-                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    load(i);
+                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                     for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
-                }
-                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
-                const bool move = valid && mn - m > kLoose;  // also from -inf
-                if (kt == v.k0[h]) {
-                    m = mn;
-                } else if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? exp2_fast(m - mn) : 1.0f;
-                    if (move) m = mn;
-                    l *= f;
-                    wait(&pv_done[h], (n - 1) & 1);
-                    tc::tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < kValueCols / 16; ++i) {
-                        uint32_t o[16];
-                        tmem_ld16(to + i * 16, o);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st16(to + i * 16, o);
-                    }
-                }
-                const float base = m == -CUDART_INF_F ? 0.0f : m;
-                const float2 nb2 = make_float2(-base, -base);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    const bool move = valid && top - m > kLoose;  // also from -inf
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float mn = move ? ceilf(top) : m;
+                        const float f = move ? exp2_fast(m - mn) : 1.0f;
+                        m = mn;
+                        sum[0] = add2(sum[0], sum[1]);
+                        l = (l + sum[0].x + sum[0].y) * f;
+                        sum[0] = sum[1] = make_float2(0.f, 0.f);
+                        tmem_wait_st();
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    load(i);
-                    uint32_t out[16];
+                        for (int c = 0; c < i; ++c) {
+                            tmem_ld16(ts + c * 16, out);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                out[j] = cvt_bf16x2(__uint_as_float(out[j] << 16) * f, __uint_as_float(out[j] & 0xffff0000u) * f);
+                            tmem_st16(ts + c * 16, out);
+                        }
+                        if (kt != v.k0[h]) {
+                            wait(&pv_done[h], (n - 1) & 1);
+                            tc::tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < kValueCols / 16; ++c) {
+                                tmem_ld16(to + c * 16, out);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) out[j] = __float_as_uint(__uint_as_float(out[j]) * f);
+                                tmem_st16(to + c * 16, out);
+                            }
+                        }
+                    }
+                    const float base = m == -CUDART_INF_F ? 0.0f : -m;
+                    const float2 nb2 = make_float2(base, base);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         float2 x = make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));

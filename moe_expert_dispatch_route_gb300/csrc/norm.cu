@@ -2,16 +2,19 @@
 //   x = N(y; post) or y,   r' = resid + scale * gate * x,   out = N(r'; pre)
 // Every row is read once and kept in registers as fp32 through both norms, so HBM bounds it: y and the
 // residual in, both out.  A row is shared by kWarps warps, a thread holding kChunks times 8 consecutive
-// elements; a norm is one sum over them and one exchange through shared memory.  8 / kWarps rows are
-// under way in a CTA, so that narrow rows fill it too.
-// 16384 tokens of 7168 (bf16, fp32 residual): see the launch for the rule and its figures.
+// elements; a norm is one sum over them and one exchange through shared memory.  A CTA of 256 threads (512
+// for wide rows) takes as many rows as it has warps for, so that narrow rows fill it too.
+// 16384 rows of 7168, bf16 with an fp32 residual, both norms and a gate, 1.41 GB: 234 us (6.0 TB/s; a copy of as many
+// bytes reaches 6.8); 64 rows of 2048 2.2 us.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+// Rows of up to 4096 elements a CTA, 256 threads; wider ones 512.
+template <int kWarps>
+constexpr int kCtaThreads = kWarps > 8 ? 512 : 256;
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -63,7 +66,9 @@ __device__ __forceinline__ float inv_rms(float part, float* sums, int warp, floa
 }
 
 template <typename T, typename R, int kWarps, int kChunks>
-__global__ void __launch_bounds__(kThreads) block_norm_kernel(const __grid_constant__ moe_norm_args a) {
+__global__ void __launch_bounds__(kCtaThreads<kWarps>, kChunks <= 2 ? 3 : 1)
+    block_norm_kernel(const __grid_constant__ moe_norm_args a) {
+    constexpr int kThreads = kCtaThreads<kWarps>;
     __shared__ float sums[2][kThreads / 32];
     pdl_begin();
     constexpr int kRows = kThreads / 32 / kWarps, kLanes = 32 * kWarps;
@@ -143,12 +148,14 @@ __global__ void __launch_bounds__(kThreads) block_norm_kernel(const __grid_const
 
 template <typename T, typename R, int kWarps, int kChunks>
 cudaError_t launch_as(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
-    constexpr int kRows = kThreads / 32 / kWarps;
+    constexpr int kThreads = kCtaThreads<kWarps>, kRows = kThreads / 32 / kWarps;
     int grid = (a.T - 1) / kRows + 1;
     if (grid > grid_cap) grid = grid_cap;
     return launch_pdl(block_norm_kernel<T, R, kWarps, kChunks>, grid, kThreads, 0, st, a);
 }
-// A row goes to as few warps as hold it with 8 elements a thread, wide ones to 8 warps with more.
+// A row goes to as few warps as hold it with 8 elements a thread, wide ones to 8 or 16 warps with more.  Three CTAs
+// an SM keep enough loads under way: the rows above with 8 warps and 32 elements a thread take 242 us, 299 where the
+// registers leave two CTAs; 32 warps 264.
 template <typename T, typename R>
 cudaError_t launch_of(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     const int n = (a.hidden / 8 + 31) / 32;  // warps' worth of chunks
@@ -157,8 +164,8 @@ cudaError_t launch_of(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     if (n <= 4) return launch_as<T, R, 4, 1>(a, grid_cap, st);
     if (n <= 8) return launch_as<T, R, 8, 1>(a, grid_cap, st);
     if (n <= 16) return launch_as<T, R, 8, 2>(a, grid_cap, st);
-    if (n <= 32) return launch_as<T, R, 8, 4>(a, grid_cap, st);
-    return launch_as<T, R, 8, 8>(a, grid_cap, st);
+    if (n <= 32) return launch_as<T, R, 16, 2>(a, grid_cap, st);
+    return launch_as<T, R, 16, 4>(a, grid_cap, st);
 }
 
 }  // namespace
