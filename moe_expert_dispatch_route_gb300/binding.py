@@ -590,26 +590,37 @@ def moe_block_norm(y, out=None, pre_weight=None, resid=None, resid_out=None, pos
     """x = norm(y) with post_weight [H], or y; resid_out = resid + scale * gate * x; out = norm(resid_out) with
     pre_weight [H].  y, out, weights and gate ([T][H], or [1][H] for all tokens) fp32 or bf16, the residual
     either; packed rows.  resid_out may be resid, and out may be y."""
-    T, H = y.shape
-    dtype = y.dtype
-    stream_of = resid if resid is not None else resid_out
-    rdtype = dtype if stream_of is None else stream_of.dtype
-    if dtype not in _FLOATS or rdtype not in _FLOATS or not y.is_contiguous():
+    shape, dtype = y.shape, y.dtype
+    T, H = shape
+    rdtype = dtype if resid is None and resid_out is None else (resid if resid is not None else resid_out).dtype
+    kind, rkind = _FLOATS.get(dtype), _FLOATS.get(rdtype)
+    if kind is None or rkind is None or not y.is_contiguous():
         raise ValueError(f"moe_block_norm: packed rows of fp32 or bf16 are expected, got {dtype} and {rdtype}")
-    for t, d in ((out, dtype), (resid, rdtype), (resid_out, rdtype)):
-        if t is not None and (t.dtype is not d or t.shape != y.shape or not t.is_contiguous()):
-            raise ValueError(f"moe_block_norm: packed {d} rows {tuple(y.shape)} are expected, got {t.dtype} {tuple(t.shape)}")
-    for t in (post_weight, pre_weight):
-        if t is not None:
-            _vector("moe_block_norm: weight", t, dtype, H)
+    y_at, out_at, resid_at = y.data_ptr(), _rows_at(out, shape, dtype), _rows_at(resid, shape, rdtype)
+    resid_out_at = resid_at if resid_out is resid else _rows_at(resid_out, shape, rdtype)
+    post_at = pre_at = gate_at = None
+    if post_weight is not None:
+        _vector("moe_block_norm: post_weight", post_weight, dtype, H)
+        post_at = post_weight.data_ptr()
+    if pre_weight is not None:
+        _vector("moe_block_norm: pre_weight", pre_weight, dtype, H)
+        pre_at = pre_weight.data_ptr()
     rows = 1
     if gate is not None:
         rows = gate.size(0)
         if gate.dtype is not dtype or gate.shape != (rows, H) or rows not in (1, T) or not gate.is_contiguous():
             raise ValueError(f"moe_block_norm: gate is packed {dtype} [1 or {T}][{H}], got {gate.dtype} {tuple(gate.shape)}")
-    args = MoeNormArgs(y.data_ptr(), _ptr(post_weight), _ptr(gate), _ptr(resid), _ptr(resid_out), _ptr(pre_weight),
-                       _ptr(out), T, H, _FLOATS[dtype], _FLOATS[rdtype], rows, scale, eps)
+        gate_at = gate.data_ptr()
+    args = MoeNormArgs(y_at, post_at, gate_at, resid_at, resid_out_at, pre_at, out_at, T, H, kind, rkind, rows, scale, eps)
     _check(lib().moe_block_norm(ctypes.byref(args), max_ctas, _stream(stream)), "moe_block_norm")
+
+
+def _rows_at(t, shape, dtype):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"moe_block_norm: packed {dtype} rows {tuple(shape)} are expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def moe_draft_verify(target, draft, cu_draft, ids, u, u_draw, out_ids, out_len, err_flag=None, max_ctas=0,

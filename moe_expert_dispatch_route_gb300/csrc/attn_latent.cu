@@ -813,7 +813,8 @@ cudaError_t launch_as(const moe_latent_cache& c, const LatentParams& lp, int gri
     cudaError_t e = ensure_max_dynamic_smem(kern, Cfg<kN>::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, grid, kThreads, Cfg<kN>::kSmem, st, lp, qm, m1, m2);
-    return e == cudaSuccess ? launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp) : e;
+    if (e != cudaSuccess || lp.p.max_kv <= kKeyTile) return e;  // a tile of one unit is never split
+    return launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp);
 }
 template <bool kTree>
 cudaError_t launch_of(const moe_latent_cache& c, const LatentParams& lp, int rows, int grid, cudaStream_t st) {
@@ -864,9 +865,10 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
     // a request's rows in as few tiles as hold them, of 64 at most; a narrow tile where they are few
     const int most = 64 / p.group;
     p.tokens_per_tile = a.max_q < most ? a.max_q : most;
-    p.item_cost = 2;
+    // what a query tile costs beside its key tiles (1.7 us each 64 keys) is about 4 us
+    p.item_cost = 1;
     p.item_slack = 1;
-    p.cta_units = 2;
+    p.cta_units = 1;
     if (grid_cap > kMostParts) grid_cap = kMostParts;
     const int teams = grid_cap / lp.team < 1 ? 1 : grid_cap / lp.team;
     int grid = grid_for(p, teams);
