@@ -24,20 +24,12 @@
 //               behind it, which wait for the product to give their place back
 //   warps 6, 7  copies: the rotary blocks and half of the pieces, the other half (a copying warp issues
 //               a copy about every 100 cycles, and 16-token pages take 36 of them for 64 keys)
-#include <cudaTypedefs.h>
-
-#include "attn.cuh"
+#include "attn_latent.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kLatent = 512, kRope = 64, kWidth = kLatent + kRope;
-constexpr int kSub = 64;                       // keys at a time
-constexpr int kBlocks = kWidth / 64;           // 128-byte column blocks of a row
-constexpr int kBlockBytes = kSub * 128;        // one of them
-constexpr int kPieceBytes = 2 * kBlockBytes;   // 128 columns, as the second product takes them
-constexpr int kPieces = kLatent / 128;
 constexpr int kThreads = 256;
 
 template <int kN>
@@ -56,22 +48,6 @@ struct Cfg {
     // the scores of rows past kN are of what lies behind Q in shared memory, and go nowhere
     static_assert((64 - kN) * 128 <= kPBytes + kRing * kPieceBytes, "");
 };
-
-struct LatentParams {
-    Params p;      // heads = 1; group = the heads of one CTA
-    int q_heads;   // of a token
-    int team;      // CTAs that share a range of keys
-};
-
-// Key tiles of kSub keys of an item: [first, last), none for a tile that sees no key.
-struct Subs {
-    int first, last;
-};
-__device__ __forceinline__ Subs subs_of(const Item& it) {
-    if (it.n == 0) return {0, 0};
-    const int lo = max(it.s.lo, it.k0 * kKeyTile), hi = min(it.s.hi, (it.k0 + it.n) * kKeyTile);
-    return {lo / kSub, (hi + kSub - 1) / kSub};
-}
 
 // What the MMA warp has to know of a key tile, put beside it by the copying warp.
 enum : uint32_t {
@@ -111,20 +87,6 @@ __device__ __forceinline__ float max_of_4(float v) {  // of the lanes that share
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 __device__ __forceinline__ void sync_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// What the second kernel has to know of a part, behind its sums in the workspace.  Every CTA writes those of
-// its two slots in every call.
-struct PartHead {
-    int n;        // parts of the tile, 0: no part in this slot
-    int rank;     // of this one among them
-    int first;    // the CTA with the first one (in its slot 0; the others are in slot 1)
-    int rows;     // of the tile
-    int token;    // its first row of q
-    int block;    // which of the heads' blocks
-};
-__device__ __forceinline__ PartHead* part_head(const Params& p, int cta, int slot) {
-    return reinterpret_cast<PartHead*>(part_ml(p, cta, slot) + 64);
-}
 
 // Split tiles, put together: the CTAs of a slot each take a share of their tile's output, so that a long context's
 // many parts are read by as many CTAs.  (Joined by the last CTA to arrive, as in attn_tile.cuh, a tile of 64 rows took
@@ -776,8 +738,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
-// q as (d, head, token): a box holds the rows of a query tile in (token, head) order.
-bool make_q_map(CUtensorMap* m, const Params& p, int q_heads) {
+template <int kN, bool kTree>
+cudaError_t launch_as(const moe_latent_cache& c, const LatentParams& lp, int grid, cudaStream_t st) {
+    CUtensorMap qm, m1, m2;
+    const int tokens = c.page_size < kSub ? c.page_size : kSub;
+    if (!make_latent_q_map(&qm, lp) || !make_latent_map(&m1, c, 1, tokens) || !make_latent_map(&m2, c, 2, tokens))
+        return cudaErrorInvalidValue;
+    auto kern = attn_latent_kernel<kN, kTree>;
+    cudaError_t e = ensure_max_dynamic_smem(kern, Cfg<kN>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, kThreads, Cfg<kN>::kSmem, st, lp, qm, m1, m2);
+}
+template <bool kTree>
+cudaError_t launch_of(const moe_latent_cache& c, const LatentParams& lp, int rows, int grid, cudaStream_t st) {
+    return rows <= 16   ? launch_as<16, kTree>(c, lp, grid, st)
+           : rows <= 32 ? launch_as<32, kTree>(c, lp, grid, st)
+                        : launch_as<64, kTree>(c, lp, grid, st);
+}
+
+}  // namespace
+
+bool make_latent_q_map(CUtensorMap* m, const LatentParams& lp) {
+    const Params& p = lp.p;
+    const int q_heads = lp.q_heads;
     auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encode_fn());
     if (!enc) return false;
     cuuint64_t dims[3] = {kWidth, (cuuint64_t)q_heads, (cuuint64_t)p.T};
@@ -790,40 +773,18 @@ bool make_q_map(CUtensorMap* m, const Params& p, int q_heads) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The pool as (d within a block, token, column block, page): a box holds `blocks` column blocks of up to
-// kSub tokens.
-bool make_latent_map(CUtensorMap* m, const moe_latent_cache& c, int blocks) {
+bool make_latent_map(CUtensorMap* m, const moe_latent_cache& c, int blocks, int tokens) {
     auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tma_encode_fn());
     if (!enc) return false;
     cuuint64_t dims[4] = {64, (cuuint64_t)c.page_size, kBlocks, (cuuint64_t)c.num_pages};
     cuuint64_t strides[3] = {(cuuint64_t)c.stride_token * 2, 128, (cuuint64_t)c.stride_page * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)(c.page_size < kSub ? c.page_size : kSub), (cuuint32_t)blocks, 1};
+    cuuint32_t box[4] = {64, (cuuint32_t)tokens, (cuuint32_t)blocks, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
 
-template <int kN, bool kTree>
-cudaError_t launch_as(const moe_latent_cache& c, const LatentParams& lp, int grid, cudaStream_t st) {
-    CUtensorMap qm, m1, m2;
-    if (!make_q_map(&qm, lp.p, lp.q_heads) || !make_latent_map(&m1, c, 1) || !make_latent_map(&m2, c, 2))
-        return cudaErrorInvalidValue;
-    auto kern = attn_latent_kernel<kN, kTree>;
-    cudaError_t e = ensure_max_dynamic_smem(kern, Cfg<kN>::kSmem);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, grid, kThreads, Cfg<kN>::kSmem, st, lp, qm, m1, m2);
-    if (e != cudaSuccess || lp.p.max_kv <= kKeyTile) return e;  // a tile of one unit is never split
-    return launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp);
-}
-template <bool kTree>
-cudaError_t launch_of(const moe_latent_cache& c, const LatentParams& lp, int rows, int grid, cudaStream_t st) {
-    return rows <= 16   ? launch_as<16, kTree>(c, lp, grid, st)
-           : rows <= 32 ? launch_as<32, kTree>(c, lp, grid, st)
-                        : launch_as<64, kTree>(c, lp, grid, st);
-}
-
-}  // namespace
 }  // namespace attn
 
 cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a, const uint64_t* tree, int grid_cap,
@@ -875,7 +836,12 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
     const int fit = device_info().num_sms / lp.team;
     if (grid > fit) grid = fit;
     const int rows = p.tokens_per_tile * p.group;
-    return tree ? launch_of<true>(c, lp, rows, grid * lp.team, st) : launch_of<false>(c, lp, rows, grid * lp.team, st);
+    grid *= lp.team;
+    const cudaError_t e = lp.team == 2 ? launch_latent_pair(c, lp, grid, st)
+                          : tree       ? launch_of<true>(c, lp, rows, grid, st)
+                                       : launch_of<false>(c, lp, rows, grid, st);
+    if (e != cudaSuccess || p.max_kv <= kKeyTile) return e;  // a tile of one unit is never split
+    return launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp);
 }
 
 }  // namespace moe
