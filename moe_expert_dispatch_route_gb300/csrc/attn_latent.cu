@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
     };
     const int r0 = e0 / kPer, nrows = (e0 + count - 1) / kPer - r0 + 1;
     auto load = [&](int i, int e) { return __ldcg(reinterpret_cast<const float4*>(part_at(i)) + e); };
+    const bool wide = count > kJoinThreads;  // several numbers a thread, of few parts
     int groups = 1;
     while (groups * 2 * count <= kJoinThreads && groups * 4 <= h.n) groups *= 2;
     // the first numbers are on their way while the weights are found: a chain of two loads in all
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
             for (int i = 0; i < kI; ++i)
                 if (at + u * kJoinThreads < count && i0 + i < h.n) x[u][i] = load(i0 + i, e0 + at + u * kJoinThreads);
     };
-    if (groups == 1) fetch(tid, 0);
+    if (wide) fetch(tid, 0);
     // a warp a row, a lane a part (or several): its weight
     constexpr int kPerLane = kMostParts / 32, kPerWarp = 64 / (kJoinThreads / 32);
     const int lane = tid & 31;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
         if (w == 0.0f) return;  // a part without keys for this row: its numbers may be anything
         o.x += x.x * w, o.y += x.y * w, o.z += x.z * w, o.w += x.w * w;
     };
-    if (groups == 1) {
+    if (wide) {
         for (int at = tid; at < count; at += kE * kJoinThreads) {
             float4 o[kE];
 #pragma unroll
@@ -323,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t tiles = 0, items = 0, q_sent = 0, rope_sent = 0, sent = 0;  // sent: pairs of pieces
         const int box_keys = min(p.page_size, kSub), npg = kSub / box_keys;
         const bool wide = npg == 1;  // a copy takes both column blocks of a piece
-        // parts of split tiles stay in L2 until they are joined, beside the keys that stream through it
-        const uint64_t once = tc::policy_evict_first();
+        const uint64_t policy = tc::policy_of(one_tile(p));
         bool more_now = more(cur);
         Item it, after;
         Pages pages, pages_after;
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (want1)
                             tc::tma_load_4d_hint(ropes + re * kBlockBytes + pg * box_keys * 128, &map1, &rope_full[re],
-                                                 0, off, kLatent / 64, page, once);
+                                                 0, off, kLatent / 64, page, policy);
                     }
                     if (++re == C::kRopes) re = 0;
                 }
@@ -399,10 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint8_t* dst = ring + e * kPieceBytes;
                         if (want) {
                             if (wide)
-                                tc::tma_load_4d_hint(dst, &map2, &full[e], 0, off, 2 * b, page, once);
+                                tc::tma_load_4d_hint(dst, &map2, &full[e], 0, off, 2 * b, page, policy);
                             else
                                 tc::tma_load_4d_hint(dst + (lane & 1) * kBlockBytes + pg * box_keys * 128, &map1,
-                                                     &full[e], 0, off, 2 * b + (lane & 1), page, once);
+                                                     &full[e], 0, off, 2 * b + (lane & 1), page, policy);
                         }
                     }
                     if (++e >= C::kRing) e -= C::kRing;

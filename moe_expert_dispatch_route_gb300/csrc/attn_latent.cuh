@@ -21,6 +21,11 @@ struct LatentParams {
     int team;      // CTAs that share a range of keys
 };
 
+// Whether no request of the call has more than one query tile: then its keys are read once, and leave L2 to the
+// parts of split tiles (64 requests with 16 heads 104 us, 108 without; but two chunks of 64 tokens with 128
+// heads, whose tiles read the same keys, 173, 150 without).
+__device__ __forceinline__ bool one_tile(const Params& p) { return p.max_q <= p.tokens_per_tile; }
+
 // Key tiles of kSub keys of an item: [first, last), none for a tile that sees no key.
 struct Subs {
     int first, last;

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (warp == kKeyCopies || warp == kValueCopies) {
         // ------------------------------------------------------------ copies
         const bool is_k = warp == kKeyCopies;
-        const uint64_t once = tc::policy_evict_first();
+        const uint64_t policy = tc::policy_of(one_tile(p));
         const int span_keys = is_k ? kSub / 2 : kSub;             // of a tile that this CTA copies
         const int box_keys = min(p.page_size, span_keys), npg = span_keys / box_keys;
         const int blks = is_k ? kBlocks : 4;                      // column blocks
@@ -274,12 +274,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (want) {
                     if (is_k)
                         tc::tma_load_4d_pair(keys + st * kKeyBytes + part * kKeyBlock + pg * box_keys * 128, &kmap,
-                                             tc::map_to_rank(&full[st], 0), 0, off, part * per_box, page, once);
+                                             tc::map_to_rank(&full[st], 0), 0, off, part * per_box, page, policy);
                     else {
                         // this CTA's blocks: 2 and 2 of the two halves of 256 columns
                         const int blk = part * per_box;
                         tc::tma_load_4d_hint(vals + st * kValueBytes + blk * kBlockBytes + pg * box_keys * 128, &vmap,
-                                             &full[st], 0, off, (blk >> 1) * 4 + block * 2 + (blk & 1), page, once);
+                                             &full[st], 0, off, (blk >> 1) * 4 + block * 2 + (blk & 1), page, policy);
                     }
                 }
             }
