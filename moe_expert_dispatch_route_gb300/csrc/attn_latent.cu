@@ -10,8 +10,7 @@
 // contiguous.  Two score buffers let the tensor cores work on the next keys' scores while the softmax of
 // these runs; probabilities go through shared memory as the second product's B operand.
 //
-// 65 to 128 heads take two CTAs side by side, each with half of the heads and the same range of
-// keys, which the second one to ask finds in L2.
+// Requests of more rows go to attn_latent_pair.cu.
 //
 // What bounds it: few rows, HBM; 64 rows, the tensor cores: the 36 instructions of a score tile take as
 // long with 64 rows as with 128, and the 16 of the product read 6 KB of shared memory each.
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
     const int count = (int)((int64_t)total * (h.rank + 1) / h.n) - e0;
     if (count == 0) return;
     const uint8_t* base = p.parts + ((size_t)h.first * 2 + 1) * kPartBytes;
-    const size_t stride = (size_t)lp.team * 2 * kPartBytes;
+    const size_t stride = (size_t)h.step * 2 * kPartBytes;
     auto part_at = [&](int i) { return base + i * stride - (i == 0 ? kPartBytes : 0); };
     auto ml_at = [&](int i, int r) {
         return __ldcg(reinterpret_cast<const float2*>(part_at(i) + (size_t)kMaxRows * 128 * 4) + r);
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i)
             if (i < parts) weights[(row - r0) * h.n + i * 32 + lane] = exp2_fast(ml[i].x - to) * inv;
-        const int token = h.token + row / p.group, head = h.block * p.group + row % p.group;
+        const int token = h.token + row / p.group, head = h.head + row % p.group;
         if (lane == 0 && p.lse && head < lp.q_heads && row * kPer >= e0 && row * kPer < e0 + count)
             p.lse[(int64_t)token * lp.q_heads + head] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
     };
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
     }
     __syncthreads();
     auto out = [&](int e, float4 o) {
-        const int row = e / kPer, token = h.token + row / p.group, head = h.block * p.group + row % p.group;
+        const int row = e / kPer, token = h.token + row / p.group, head = h.head + row % p.group;
         if (head < lp.q_heads)
             *reinterpret_cast<uint2*>(p.o + token * p.o_ld + head * p.o_head + e % kPer * 4) =
                 make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
@@ -258,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort = &abort_s;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int me = blockIdx.x / lp.team, block = blockIdx.x % lp.team;
     constexpr int kMmaWarp = 4, kValueWarp = 5, kCopyWarp = 6;
     if (threadIdx.x == 0) {
         abort_s = 0;
@@ -292,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_relinquish();
         tc::tc_fence_before();
     }
-    locate<kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start, me, gridDim.x / lp.team);
+    locate<kThreads>(p, reinterpret_cast<uint32_t*>(ring), &start);
     tc::tc_fence_after();
     const uint32_t tmem = tmem_s;
     if (threadIdx.x < 2) part_head(p, blockIdx.x, threadIdx.x)->n = 0;
@@ -324,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t tiles = 0, items = 0, q_sent = 0, rope_sent = 0, sent = 0;  // sent: pairs of pieces
         const int box_keys = min(p.page_size, kSub), npg = kSub / box_keys;
         const bool wide = npg == 1;  // a copy takes both column blocks of a piece
-        const uint64_t policy = tc::policy_of(one_tile(p));
+        // keys are read once here: they leave L2 to the parts of split tiles (16 heads: 104 us, 108 without)
+        const uint64_t policy = tc::policy_of(true);
         bool more_now = more(cur);
         Item it, after;
         Pages pages, pages_after;
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) tc::mbar_arrive_expect_tx(q_full, kBlocks * p.tokens_per_tile * p.group * 128);
                     __syncwarp();
                     if (lane < kBlocks)
-                        tc::tma_load_3d(qs + lane * kN * 128, &qmap, q_full, lane * 64, block * p.group,
+                        tc::tma_load_3d(qs + lane * kN * 128, &qmap, q_full, lane * 64, 0,
                                         it.r.row0 + it.tile * p.tokens_per_tile);
                 }
             }
@@ -550,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 const int row = row0 + 8 * i;
                 const RowAt at = row_at(p, it, min(row, rows - 1));
-                const int head = block * p.group + at.head;
-                valid[i] = row < rows && head < lp.q_heads;
+                valid[i] = row < rows;
                 if (valid[i]) {
                     const int pos = it.r.kv - it.r.n + (at.token - it.r.row0);
                     hi[i] = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
@@ -559,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kTree) branch[i] = branch_of(p, it.r, at.token);
                 }
                 if (speaks) {
-                    row_off[row] = valid[i] ? at.token * p.o_ld + head * p.o_head : -1;
-                    row_lse[row] = (int64_t)at.token * lp.q_heads + head;
+                    row_off[row] = valid[i] ? at.token * p.o_ld + at.head * p.o_head : -1;
+                    row_lse[row] = (int64_t)at.token * lp.q_heads + at.head;
                 }
             }
             // every row sees keys [lo_all, hi_all): no mask there
@@ -726,9 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             if (!it.whole && threadIdx.x == 0) {
                 const Parts parts = parts_of(p, it, start);
-                *part_head(p, blockIdx.x, slot) = {parts.last - parts.first + 1, me - parts.first,
-                                                   parts.first * lp.team + block, rows,
-                                                   it.r.row0 + it.tile * p.tokens_per_tile, block};
+                *part_head(p, blockIdx.x, slot) = {parts.last - parts.first + 1, (int)blockIdx.x - parts.first, parts.first, 1,
+                                                   rows, it.r.row0 + it.tile * p.tokens_per_tile, 0};
             }
             tc::tc_fence_before();  // o has been read: the next item's first arrival on p_full says so
             sync_128();             // and the rows' places may be written again
@@ -766,7 +763,7 @@ bool make_latent_q_map(CUtensorMap* m, const LatentParams& lp) {
     cuuint64_t dims[3] = {kWidth, (cuuint64_t)q_heads, (cuuint64_t)p.T};
     cuuint64_t strides[2] = {(cuuint64_t)(q_heads > 1 ? p.q_head * 2 : kWidth * 2),
                              (cuuint64_t)(p.T > 1 ? p.q_ld * 2 : kWidth * 2)};
-    cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)p.tokens_per_tile};
+    cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)lp.cta_tokens};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -820,26 +817,27 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
     p.parts = static_cast<uint8_t*>(a.workspace) + kMaxCtas * sizeof(uint32_t);
     p.inject_ns = wait_injection_ns();
     lp.q_heads = a.num_q_heads;
-    lp.team = a.num_q_heads > 64 ? 2 : 1;
     p.heads = 1;
-    p.group = (a.num_q_heads + lp.team - 1) / lp.team;
-    // a request's rows in as few tiles as hold them, of 64 at most; a narrow tile where they are few
-    const int most = 64 / p.group;
-    p.tokens_per_tile = a.max_q < most ? a.max_q : most;
+    // Up to 64 rows a request go to one CTA, more to pairs, which take two thirds of the time for 128 rows that
+    // single CTAs take for 64 twice (128 heads: 150 us against 201).  One rule for the whole call, as in attn.cu.
+    const bool pairs = (int64_t)a.max_q * a.num_q_heads > 64;
+    lp.split_heads = a.num_q_heads > 64;
+    p.group = lp.split_heads ? (a.num_q_heads + 1) / 2 : a.num_q_heads;
+    const int most = 64 / p.group, half = a.max_q / 2 + a.max_q % 2;  // tokens
+    lp.cta_tokens = !pairs ? a.max_q : lp.split_heads ? 1 : half < most ? half : most;
+    p.tokens_per_tile = pairs && !lp.split_heads ? 2 * lp.cta_tokens : lp.cta_tokens;
     // what a query tile costs beside its key tiles (1.7 us each 64 keys) is about 4 us
     p.item_cost = 1;
     p.item_slack = 1;
     p.cta_units = 1;
     if (grid_cap > kMostParts) grid_cap = kMostParts;
-    const int teams = grid_cap / lp.team < 1 ? 1 : grid_cap / lp.team;
-    int grid = grid_for(p, teams);
-    const int fit = device_info().num_sms / lp.team;
-    if (grid > fit) grid = fit;
+    int grid = device_info().num_sms < grid_cap ? device_info().num_sms : grid_cap;
+    const int team = pairs ? 2 : 1, teams = grid / team > 0 ? grid / team : 1;
+    grid = grid_for(p, teams) * team;
     const int rows = p.tokens_per_tile * p.group;
-    grid *= lp.team;
-    const cudaError_t e = lp.team == 2 ? launch_latent_pair(c, lp, grid, st)
-                          : tree       ? launch_of<true>(c, lp, rows, grid, st)
-                                       : launch_of<false>(c, lp, rows, grid, st);
+    const cudaError_t e = pairs  ? launch_latent_pair(c, lp, grid, st)
+                          : tree ? launch_of<true>(c, lp, rows, grid, st)
+                                 : launch_of<false>(c, lp, rows, grid, st);
     if (e != cudaSuccess || p.max_kv <= kKeyTile) return e;  // a tile of one unit is never split
     return launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp);
 }

@@ -15,16 +15,14 @@ constexpr int kBlockBytes = kSub * 128;        // one of them
 constexpr int kPieceBytes = 2 * kBlockBytes;   // 128 columns, as the second product takes them
 constexpr int kPieces = kLatent / 128;
 
+// A query tile's rows are (token, head), head fastest, p.group heads of a token.  A pair of CTAs (attn_latent_pair.cu)
+// shares them out by heads where there are more than 64 (a tile is one token then), by tokens otherwise.
 struct LatentParams {
-    Params p;      // heads = 1; group = the heads of one CTA
-    int q_heads;   // of a token
-    int team;      // CTAs that share a range of keys
+    Params p;          // heads = 1
+    int q_heads;       // of a token
+    int cta_tokens;    // of a tile and CTA
+    int split_heads;   // pairs: 1 by heads, 0 by tokens
 };
-
-// Whether no request of the call has more than one query tile: then its keys are read once, and leave L2 to the
-// parts of split tiles (64 requests with 16 heads 104 us, 108 without; but two chunks of 64 tokens with 128
-// heads, whose tiles read the same keys, 173, 150 without).
-__device__ __forceinline__ bool one_tile(const Params& p) { return p.max_q <= p.tokens_per_tile; }
 
 // Key tiles of kSub keys of an item: [first, last), none for a tile that sees no key.
 struct Subs {
@@ -42,18 +40,19 @@ struct PartHead {
     int n;        // parts of the tile, 0: no part in this slot
     int rank;     // of this one among them
     int first;    // the CTA with the first one (in its slot 0; the others are in slot 1)
-    int rows;     // of the tile
+    int step;     // CTAs from one part to the next
+    int rows;     // of the tile and CTA
     int token;    // its first row of q
-    int block;    // which of the heads' blocks
+    int head;     // and that row's head
 };
 __device__ __forceinline__ PartHead* part_head(const Params& p, int cta, int slot) {
     return reinterpret_cast<PartHead*>(part_ml(p, cta, slot) + 64);
 }
 
-// attn_latent_pair.cu: 65 to 128 heads, on pairs of CTAs
+// attn_latent_pair.cu: tiles of 65 to 128 rows, on pairs of CTAs
 cudaError_t launch_latent_pair(const moe_latent_cache& c, const LatentParams& lp, int grid, cudaStream_t st);
 
-// q as (d, head, token): a box holds the rows of a query tile in (token, head) order.
+// q as (d, head, token): a box holds a CTA's rows of a query tile.
 bool make_latent_q_map(CUtensorMap* m, const LatentParams& lp);
 // The pool as (d within a block, token, column block, page): a box holds `blocks` column blocks of `tokens` tokens.
 bool make_latent_map(CUtensorMap* m, const moe_latent_cache& c, int blocks, int tokens);

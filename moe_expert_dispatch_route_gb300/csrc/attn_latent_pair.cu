@@ -1,6 +1,6 @@
-// Latent attention, absorbed form, 65 to 128 heads: a query tile is one token's heads, half of them in each CTA
-// of a pair (a cluster of two), over the same range of keys, 64 at a time.  The pair's MMAs (cta_group::2) read
-// each operand from where it lies:
+// Latent attention, absorbed form, for requests of more than 64 rows: a query tile of up to 128 rows, half of
+// them (of a token's heads, or of the tokens) in each CTA of a pair (a cluster of two), over the same range of
+// keys, 64 at a time.  The pair's MMAs (cta_group::2) read each operand from where it lies:
 //   S = Q K^T    m = 128 rows, n = 64 keys, k = 576     each CTA holds its 64 rows of Q and 32 of the keys
 //   O += P V     m = 128 rows, n = 2 x 256 columns, k = 64 keys     its rows of P and half of the columns
 // so that a CTA copies 68 KB for 64 keys where each of two single CTAs copies 72, and its tensor cores read two
@@ -197,12 +197,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             *abort = 1;
         }
     };
+    // this CTA's part of a query tile
+    const int head0 = lp.split_heads ? block * p.group : 0, token0 = lp.split_heads ? 0 : block * lp.cta_tokens;
     constexpr uint32_t kScores = 256;  // column of the score buffers, 32 each, behind the output's two of 128
 
     if (warp == kKeyCopies || warp == kValueCopies) {
         // ------------------------------------------------------------ copies
         const bool is_k = warp == kKeyCopies;
-        const uint64_t policy = tc::policy_of(one_tile(p));
+        // several query tiles read the same keys, one leaves L2 to the parts of split tiles (two chunks of 64
+        // tokens with 128 heads: 151 us, 173 if their keys gave way)
+        const uint64_t policy = tc::policy_of(p.max_q <= p.tokens_per_tile);
         const int span_keys = is_k ? kSub / 2 : kSub;             // of a tile that this CTA copies
         const int box_keys = min(p.page_size, span_keys), npg = span_keys / box_keys;
         const int blks = is_k ? kBlocks : 4;                      // column blocks
@@ -236,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 ++items;
                 if (!*abort) {
                     ++q_sent;
-                    if (first_cta && lane == 0) tc::mbar_arrive_expect_tx(q_full, 2 * kBlocks * p.group * 128);
+                    if (first_cta && lane == 0) tc::mbar_arrive_expect_tx(q_full, 2 * kBlocks * lp.cta_tokens * p.group * 128);
                     __syncwarp();
                     if (lane < kBlocks)
-                        tc::tma_load_3d_pair(qs + lane * kRows * 128, &qmap, tc::map_to_rank(q_full, 0), lane * 64,
-                                             block * p.group, it.r.row0 + it.tile);
+                        tc::tma_load_3d_pair(qs + lane * kRows * 128, &qmap, tc::map_to_rank(q_full, 0), lane * 64, head0,
+                                             it.r.row0 + it.tile * p.tokens_per_tile + token0);
                 }
             }
             for (int k = s.first; k < s.last; ++k, ++tiles) {
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // ------------------------------------------------------------ softmax and epilogue
         const uint32_t lanes = (uint32_t)warp << 21;  // this warp's quarter of the lanes
         const int row = (warp & 1) * 32 + lane, half = warp >> 1;
-        const int head = block * p.group + row;
+        const int row_token = row / p.group, head = head0 + row % p.group;
         auto any_of_both = [&](bool x) {  // of the two warps that share rows
             uint32_t r;
             asm volatile(
@@ -414,13 +418,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         while (more(cur)) {
             const Item it = take(p, cur);
             const Subs s = subs_of(it);
-            const bool valid = row < p.group && head < lp.q_heads;
-            const int token = it.r.row0 + it.tile, pos = it.r.kv - it.r.n + it.tile;
+            const int tokens = min(max(it.tokens - token0, 0), lp.cta_tokens);  // of this CTA
+            const bool valid = row_token < tokens && head < lp.q_heads;
+            const int token = it.r.row0 + it.tile * p.tokens_per_tile + token0 + row_token;
+            const int pos0 = it.r.kv - it.r.n + it.tile * p.tokens_per_tile + token0, pos = pos0 + row_token;
             const int hi = p.causal ? min(pos + 1, it.r.kv) : it.r.kv;
             const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
             Branch branch = {0, 0};
-            if (kTree) branch = branch_of(p, it.r, token);
-            const int hi_all = kTree ? max(it.r.kv - it.r.n, 0) : hi;
+            if (kTree && valid) branch = branch_of(p, it.r, token);
+            // every row sees keys [lo_all, hi_all): no mask there
+            const int hi_all = kTree ? max(it.r.kv - it.r.n, 0) : p.causal ? min(it.r.kv, pos0 + 1) : it.r.kv;
+            const int lo_all = p.window > 0 ? max(0, pos0 + tokens - p.window) : 0;
             float m = -CUDART_INF_F, l = 0.0f;  // m in powers of two, the same in both threads of a row
             for (int k = s.first; k < s.last; ++k, ++n) {
                 const int key0 = k * kSub + half * (kSub / 2);
@@ -432,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&s_free[n & 1]);
-                if (key0 < lo || key0 + kSub / 2 > hi_all) {
-                    uint32_t seen;  // the same for every row: they are one token's
+                if (key0 < lo_all || key0 + kSub / 2 > hi_all) {
+                    uint32_t seen;
                     if (kTree) {
                         seen = branch.word(key0);
                     } else {
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                        any ? o[4 * j + 3] : 0);
                 }
             }
-            if (half == 0 && row < p.group) {
+            if (half == 0 && row_token < tokens) {
                 if (!it.whole)
                     part_ml(p, blockIdx.x, slot)[row] = make_float2(m, l);
                 else if (p.lse && valid)
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (!it.whole && threadIdx.x == 0) {
                 const Parts parts = parts_of(p, it, start);
                 *part_head(p, blockIdx.x, slot) = {parts.last - parts.first + 1, me - parts.first,
-                                                   parts.first * 2 + block, p.group, token, block};
+                                                   parts.first * 2 + block, 2, tokens * p.group, token, head0};
             }
             tc::tc_fence_before();  // o has been read: the next item's first arrival on p_full says so
             sync_both();            // and the rows' sums may be written again
