@@ -575,7 +575,9 @@ MOE_API moe_status moe_latent_write(const moe_latent_cache* cache, int32_t T, co
  * num_q_heads from 1 to 128 (else MOE_ERR_UNSUPPORTED), rows, lengths, table, bounds, empty rows, err_flag and
  * workspace (of moe_attn_latent_workspace_size bytes) as there.  Scores, the softmax's maximum and sum, and o
  * are held in fp32, the probabilities rounded to bf16 for the second product (the sum takes them before), o
- * rounded once at the end.  The cached numbers are to be below about 2^100. */
+ * rounded once at the end.  The cached numbers are to be below about 2^100.
+ * A split tile's parts are joined by a second kernel.  For requests of more than 64 rows (max_q * num_q_heads),
+ * max_ctas is rounded down to pairs of CTAs, and up to one. */
 MOE_API size_t moe_attn_latent_workspace_size(const moe_latent_cache* cache, int32_t num_q_heads);
 MOE_API moe_status moe_attn_latent(const moe_latent_cache* cache, const moe_attn_args* args, const uint64_t* tree,
                                    int32_t max_ctas, moe_stream_t stream);

@@ -465,6 +465,7 @@ def _attn_args(where, q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, cau
                        _ptr(kv_len), _ptr(block_table), block_table.shape[1], T, B, max_q, max_kv, H, float(scale),
                        int(causal), window, _ptr(err_flag), _ptr(workspace), size)
     args.head_dim = D  # the C structure has no field for it: the cache's is meant
+    args.keep = (q, o, lse, cu_q, kv_len, block_table, err_flag, workspace)  # it holds their addresses
     return args
 
 
@@ -571,10 +572,12 @@ def attn_expanded_args(q, k, k_rope, v, o, cu_q, cu_kv, max_q, max_kv, scale, ca
     if lse is not None:
         _same("attn_expanded_args: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
     size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    return MoeAttnExpandedArgs(_ptr(q), _ptr(k), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), q.stride(0), q.stride(1),
+    args = MoeAttnExpandedArgs(_ptr(q), _ptr(k), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), q.stride(0), q.stride(1),
                                k.stride(0), k.stride(1), k_rope.stride(0), v.stride(0), v.stride(1), o.stride(0),
                                o.stride(1), _ptr(cu_q), _ptr(cu_kv), T, S, B, max_q, max_kv, H, float(scale),
                                int(causal), _ptr(err_flag), _ptr(workspace), size)
+    args.keep = (q, k, k_rope, v, o, lse, cu_q, cu_kv, err_flag, workspace)  # it holds their addresses
+    return args
 
 
 def moe_attn_expanded(args: MoeAttnExpandedArgs, max_ctas=0, stream=None):

@@ -94,14 +94,9 @@ __device__ __forceinline__ void sync_128() { asm volatile("bar.sync 1, 128;" :::
 // threads, whose sums are added in order.
 constexpr int kJoinThreads = 512;
 constexpr int kMostParts = 160;  // of a tile, and CTAs of a call
-__global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __grid_constant__ LatentParams lp) {
+__device__ __forceinline__ void join_share(const LatentParams& lp, const PartHead& h, float* weights, float4* sums) {
     const Params& p = lp.p;
-    __shared__ float weights[64 + 2 * kMostParts];  // [row of the share][part]
-    __shared__ float4 sums[kJoinThreads];
-    pdl_begin();
-    const int cta = blockIdx.x >> 1, slot = blockIdx.x & 1, tid = threadIdx.x;
-    const PartHead h = *part_head(p, cta, slot);
-    if (h.n == 0) return;
+    const int tid = threadIdx.x;
     constexpr int kPer = kLatent / 4;
     const int total = h.rows * kPer, e0 = (int)((int64_t)total * h.rank / h.n);
     const int count = (int)((int64_t)total * (h.rank + 1) / h.n) - e0;
@@ -118,7 +113,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
     int groups = 1;
     while (groups * 2 * count <= kJoinThreads && groups * 4 <= h.n) groups *= 2;
     // the first numbers are on their way while the weights are found: a chain of two loads in all
-    constexpr int kE = 8, kI = 2;  // elements and parts under way together
+    constexpr int kE = 4, kI = 2, kP = 8;  // elements and parts under way together, and parts of one element
     float4 x[kE][kI];
     auto fetch = [&](int at, int i0) {
 #pragma unroll
@@ -206,13 +201,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (at < count) {
         const float* w = weights + ((e0 + at) / kPer - r0) * h.n;
-        for (int i0 = g; i0 < h.n; i0 += kE * groups) {
-            float4 y[kE];
+        for (int i0 = g; i0 < h.n; i0 += kP * groups) {
+            float4 y[kP];
 #pragma unroll
-            for (int i = 0; i < kE; ++i)
+            for (int i = 0; i < kP; ++i)
                 if (i0 + i * groups < h.n) y[i] = load(i0 + i * groups, e0 + at);
 #pragma unroll
-            for (int i = 0; i < kE; ++i)
+            for (int i = 0; i < kP; ++i)
                 if (i0 + i * groups < h.n) add(o, y[i], w[i0 + i * groups]);
         }
     }
@@ -221,6 +216,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __
     if (g == 0 && at < count) {
         for (int i = 1; i < groups; ++i) add(o, sums[i * per + at], 1.0f);
         out(e0 + at, o);
+    }
+}
+
+// ctas: of the first kernel.
+__global__ void __launch_bounds__(kJoinThreads) attn_latent_join_kernel(const __grid_constant__ LatentParams lp, int ctas) {
+    __shared__ float weights[64 + 2 * kMostParts];  // [row of the share][part]
+    __shared__ float4 sums[kJoinThreads];
+    pdl_begin();
+    for (int i = blockIdx.x; i < 2 * ctas; i += gridDim.x) {
+        const PartHead h = *part_head(lp.p, i >> 1, i & 1);
+        if (h.n > 0) join_share(lp, h, weights, sums);
+        __syncthreads();
     }
 }
 
@@ -830,6 +837,7 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
     p.item_cost = 1;
     p.item_slack = 1;
     p.cta_units = 1;
+    const int max_ctas = grid_cap;
     if (grid_cap > kMostParts) grid_cap = kMostParts;
     int grid = device_info().num_sms < grid_cap ? device_info().num_sms : grid_cap;
     const int team = pairs ? 2 : 1, teams = grid / team > 0 ? grid / team : 1;
@@ -839,7 +847,8 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
                           : tree ? launch_of<true>(c, lp, rows, grid, st)
                                  : launch_of<false>(c, lp, rows, grid, st);
     if (e != cudaSuccess || p.max_kv <= kKeyTile) return e;  // a tile of one unit is never split
-    return launch_pdl(attn_latent_join_kernel, 2 * grid, kJoinThreads, 0, st, lp);
+    const int join = 2 * grid < max_ctas ? 2 * grid : max_ctas;
+    return launch_pdl(attn_latent_join_kernel, join, kJoinThreads, 0, st, lp, grid);
 }
 
 }  // namespace moe

@@ -221,3 +221,27 @@ def test_plain_attention_and_norm_against_torch():
     t = torch.tensor
     n = lambda x: torch.nn.functional.rms_norm(x, (16,), t(w), 0.1)
     assert np.allclose(r, t(y) + 1 + 2.0 * t(y) * n(t(y))) and np.allclose(out, n(t(r)))
+
+
+def test_arguments_keep_their_tensors():
+    """The structures hold addresses: tensors made for the call alone live as long as they do."""
+    import gc
+    import weakref
+
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    q, cu, ws = bf(2, 4, 576), i32(2), torch.zeros(8)
+    refs = [weakref.ref(t) for t in (q, cu, ws)]
+    args = B.attn_latent_args(q, bf(2, 4, 512), cu, i32(1), i32(1, 4), 2, 8, 0.1, workspace=ws)
+    del q, cu, ws
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del args
+    gc.collect()
+    assert all(r() is None for r in refs)
+    k = bf(3, 4, 128)
+    ref = weakref.ref(k)
+    args = B.attn_expanded_args(bf(2, 4, 192), k, bf(3, 64), bf(3, 4, 128), bf(2, 4, 128), i32(2), i32(2), 2, 3, 0.1)
+    del k
+    gc.collect()
+    assert ref() is not None and args.k == ref().data_ptr()
