@@ -4,10 +4,16 @@
 //   S = Q K^T    m = 128 rows, n = 64 keys, k = 576     each CTA holds its 64 rows of Q and 32 of the keys
 //   O += P V     m = 128 rows, n = 2 x 256 columns, k = 64 keys     its rows of P and half of the columns
 // so that a CTA copies 68 KB for 64 keys where each of two single CTAs copies 72, and its tensor cores read two
-// thirds of what theirs do: shared memory bounds those (attn_latent.cu; 64 requests of up to 16384 tokens, 128 heads:
-// 201 us there).  An accumulator of 64 rows a CTA fills all 128 lanes: lanes 0-63 hold the first half of
-// its columns, lanes 64-127 the second.  A row is thus shared by two threads, here for half of the keys' scores
-// and half of the output's columns each, and everything but the MMAs' operands stays in its CTA.
+// thirds of what theirs do: shared memory bounds those (64 requests of up to 16384 tokens with 128 heads: 201 us on
+// single CTAs side by side, 150 here; two chunks of 64 tokens over 8192 256 and 150).  An accumulator of 64 rows a CTA
+// fills all 128 lanes: lanes 0-63 hold the first half of its columns, lanes 64-127 the second.  A row is thus shared
+// by two threads, here for half of the keys' scores and half of the output's columns each, and everything but the
+// MMAs' operands stays in its CTA.
+//
+// What bounds it now: 2370 cycles for 64 keys, of which the MMAs last 1100 and a softmax 1100; the scores wait for
+// keys, which come about 3000 cycles after they are asked for, and two stages of them fill shared memory (HBM
+// alone would take 1570).  Three stages with one of values 222 us, keys in thirds 152-168, tiles fetched into L2
+// ahead of time 175.
 //
 // The running maximum is followed loosely, as in attn_tile.cuh.  Split tiles are joined by attn_latent.cu's
 // second kernel.
