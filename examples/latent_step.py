@@ -32,7 +32,7 @@ from moe_expert_dispatch_route_gb300 import synth  # noqa: E402
 from moe_expert_dispatch_route_gb300 import workloads as W  # noqa: E402
 
 DEV = "cuda"
-HEADS, PAGE, SCALE = 16, 64, (B.HEAD + B.ROPE)**-0.5
+HEADS, PAGE, SCALE = 12, 64, (B.HEAD + B.ROPE)**-0.5
 BF16 = torch.bfloat16
 
 # A tree of drafted tokens: node 0 is the token before them, node i the RANK[i]-th best guess after its parent.

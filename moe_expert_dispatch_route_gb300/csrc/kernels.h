@@ -152,7 +152,7 @@ cudaError_t launch_kv_read(const moe_kv_cache& c, int B, int T, const int32_t* t
                            const int32_t* start, const int32_t* cu, void* k_out, void* v_out, int32_t* err,
                            int grid_cap, cudaStream_t st);
 
-// attn.cu: paged attention (the kernels are in attn_rows.cu and attn_tile.cu)
+// attn.cu: paged attention (the kernels are in attn_rows.cuh and attn_tile.cuh)
 constexpr int kMaxRequests = 8192;
 constexpr int kMaxTokens = 1 << 30;  // rows, and cached tokens: positions less a window stay within 32 bits
 constexpr int kFewRows = 32;  // rows of a request and key/value head up to which attn_rows.cuh takes the call
