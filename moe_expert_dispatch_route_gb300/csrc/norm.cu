@@ -1,18 +1,20 @@
 // moe_block_norm: what stands between two blocks, in one pass over their rows.
 //   x = N(y; post) or y,   r' = resid + scale * gate * x,   out = N(r'; pre)
-// Every row is read once and kept in registers as fp32 through both norms, so HBM bounds it: y and the
-// residual in, both out.  A row is shared by kWarps warps, a thread holding kChunks times 8 consecutive
-// elements; a norm is one sum over them and one exchange through shared memory.  A CTA of 256 threads (512
-// for wide rows) takes as many rows as it has warps for, so that narrow rows fill it too.
-// 16384 rows of 7168, bf16 with an fp32 residual, both norms and a gate, 1.41 GB: 234 us (6.0 TB/s; a copy of as many
-// bytes reaches 6.8); 64 rows of 2048 2.2 us.
+// Every row is read from HBM once and taken through both norms in fp32, so HBM bounds it: y and the residual in,
+// both out.  A row is shared by kWarps warps, a thread holding kChunks times 8 consecutive elements; a norm is one
+// sum over them and one exchange through shared memory.  Two kernels with the same arithmetic and order of sums (a
+// row's result never depends on how many there are): CTAs that stay, with rows copied ahead, and, for narrow rows
+// and those of which two do not fit an SM, plain loads into registers.
+// 16384 rows of 7168, bf16 with an fp32 residual, both norms and a gate, 1.41 GB: 213 us (6.6 TB/s; 234 with plain
+// loads); bf16 throughout 144 (188); 16384 of 4096 82 (128); 4096 of 16384 83 (166); 64 rows of 2048 2.4 us.
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
-// Rows of up to 4096 elements a CTA, 256 threads; wider ones 512.
+// Narrow rows share CTAs of 256 threads; one that is too wide for the ring has 512.
 template <int kWarps>
 constexpr int kCtaThreads = kWarps > 8 ? 512 : 256;
 
@@ -58,18 +60,26 @@ __device__ __forceinline__ float inv_rms(float part, float* sums, int warp, floa
         if ((threadIdx.x & 31) == 0) sums[warp] = part;
         __syncthreads();
         part = 0.0f;
-        const int first = warp / kWarps * kWarps;
+        const float* of = sums + warp / kWarps * kWarps;
+        if (kWarps % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) part += sums[first + i];
+            for (int i = 0; i < kWarps; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(of + i);
+                part += (v.x + v.y) + (v.z + v.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) part += of[i];
+        }
     }
-    return 1.0f / sqrtf(part * inv_n + eps);
+    return rsqrtf(part * inv_n + eps);
 }
 
 template <typename T, typename R, int kWarps, int kChunks>
 __global__ void __launch_bounds__(kCtaThreads<kWarps>, kChunks <= 2 ? 3 : 1)
     block_norm_kernel(const __grid_constant__ moe_norm_args a) {
     constexpr int kThreads = kCtaThreads<kWarps>;
-    __shared__ float sums[2][kThreads / 32];
+    __shared__ __align__(16) float sums[2][kThreads / 32];
     pdl_begin();
     constexpr int kRows = kThreads / 32 / kWarps, kLanes = 32 * kWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x % kLanes, H = a.hidden, chunks = H / 8;
@@ -146,6 +156,153 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps>, kChunks <= 2 ? 3 : 1)
     }
 }
 
+// CTAs that stay take the rows in turn.  The rows to come are copied into shared memory while one is normed, so
+// the reads of HBM never wait for a norm's two exchanges, and a thread keeps its elements' weights in registers, as
+// they are stored, from the first row on (loaded again for each row, 28 KB for 14 of y, they come from L2: 167 us
+// where 144 are reached).  The row itself is read from shared memory twice: held in registers it spills (215).
+constexpr int kMostStages = 8;
+constexpr int kRingBytes = 208 * 1024;  // of an SM's CTAs together
+struct StreamParams {
+    moe_norm_args a;
+    int stages, stage_bytes;  // a stage: one row of y, residual and gate
+};
+template <typename T>
+struct Packed8;  // 8 elements as they are stored
+template <>
+struct Packed8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void shared(const float* p) {
+        a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void to(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+template <>
+struct Packed8<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void shared(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void to(float (&x)[8]) const { unpack8(v, x); }
+};
+template <typename T, typename R, int kWarps, int kChunks, int kCtas>
+__global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(const __grid_constant__ StreamParams sp) {
+    constexpr int kLanes = 32 * kWarps;
+    const moe_norm_args& a = sp.a;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(16) float sums[2][kWarps];
+    __shared__ uint64_t full[kMostStages];
+    const int tid = threadIdx.x, warp = tid >> 5, H = a.hidden, chunks = H / 8;
+    const int y_bytes = H * (int)sizeof(T), r_bytes = a.resid ? H * (int)sizeof(R) : 0;
+    const bool gates = a.gate && a.gate_rows > 1;
+    if (tid == 0) {
+        for (int i = 0; i < sp.stages; ++i) tc::mbar_init(&full[i], 1);
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_begin();
+    auto fetch = [&](int64_t t, int st) {  // one thread
+        if (t >= a.T) return;
+        uint8_t* to = ring + st * sp.stage_bytes;
+        tc::mbar_arrive_expect_tx(&full[st], sp.stage_bytes);
+        tc::bulk_load(to, static_cast<const T*>(a.y) + t * H, y_bytes, &full[st]);
+        if (r_bytes) tc::bulk_load(to + y_bytes, static_cast<const R*>(a.resid) + t * H, r_bytes, &full[st]);
+        if (gates) tc::bulk_load(to + y_bytes + r_bytes, static_cast<const T*>(a.gate) + t * H, y_bytes, &full[st]);
+    };
+    if (tid == 0)
+        for (int i = 0; i < sp.stages; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    const T *post = static_cast<const T*>(a.post_weight), *pre = static_cast<const T*>(a.pre_weight);
+    Packed8<T> wp[kChunks], wn[kChunks], g[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = tid + i * kLanes;
+        if (c >= chunks) continue;
+        if (post) wp[i].load(post + c * 8);
+        if (a.out) wn[i].load(pre + c * 8);
+        if (a.gate && !gates) g[i].load(static_cast<const T*>(a.gate) + c * 8);
+    }
+    const float inv_n = 1.0f / (float)H;
+    int st = 0, turn = 0;
+    uint32_t parity = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const bool landed = tc::mbar_wait_bounded(&full[st], parity);
+        const uint8_t* at = ring + st * sp.stage_bytes;
+        const T *y = reinterpret_cast<const T*>(at), *gate = reinterpret_cast<const T*>(at + y_bytes + r_bytes);
+        const R* resid = reinterpret_cast<const R*>(at + y_bytes);
+        const float scale = landed ? a.scale : __int_as_float(0x7fc00000);  // a wait that gave up: NaN, not an old row
+        float f = 1.0f, sum = 0.0f;
+        if (post) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = tid + i * kLanes;
+                if (c >= chunks) continue;
+                Packed8<T> y8;
+                float x[8];
+                y8.shared(y + c * 8);
+                y8.to(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+            }
+            f = inv_rms<kWarps>(sum, sums[turn], warp, inv_n, a.eps), turn ^= 1, sum = 0.0f;
+        }
+        float r[kChunks][8];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = tid + i * kLanes;
+            if (c >= chunks) continue;
+            Packed8<T> y8;
+            float x[8], w[8];
+            y8.shared(y + c * 8);
+            y8.to(x);
+            if (post) {
+                wp[i].to(w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
+            }
+            if (a.gate) {
+                if (gates) g[i].shared(gate + c * 8);
+                g[i].to(w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
+            if (r_bytes) {
+                Packed8<R> r8;
+                r8.shared(resid + c * 8);
+                r8.to(r[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                r[i][j] = fmaf(scale, x[j], r[i][j]);
+                sum = fmaf(r[i][j], r[i][j], sum);
+            }
+            if (a.resid_out) store8(static_cast<R*>(a.resid_out) + t * H + c * 8, r[i]);
+        }
+        if (a.out)
+            f = inv_rms<kWarps>(sum, sums[turn], warp, inv_n, a.eps), turn ^= 1;
+        else
+            __syncthreads();
+        // behind this barrier every thread has read its numbers: the stage takes another row
+        if (tid == 0) fetch(t + (int64_t)sp.stages * gridDim.x, st);
+        if (++st == sp.stages) st = 0, parity ^= 1u;
+        if (!a.out) continue;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = tid + i * kLanes;
+            if (c >= chunks) continue;
+            float w[8];
+            wn[i].to(w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * f * w[j];
+            store8(static_cast<T*>(a.out) + t * H + c * 8, r[i]);
+        }
+    }
+}
+
 template <typename T, typename R, int kWarps, int kChunks>
 cudaError_t launch_as(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     constexpr int kThreads = kCtaThreads<kWarps>, kRows = kThreads / 32 / kWarps;
@@ -153,18 +310,58 @@ cudaError_t launch_as(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     if (grid > grid_cap) grid = grid_cap;
     return launch_pdl(block_norm_kernel<T, R, kWarps, kChunks>, grid, kThreads, 0, st, a);
 }
-// A row goes to as few warps as hold it with 8 elements a thread, wide ones to 8 or 16 warps with more.  Three CTAs
-// an SM keep enough loads under way: the rows above with 8 warps and 32 elements a thread take 242 us, 299 where the
-// registers leave two CTAs; 32 warps 264.
+// How far ahead rows are copied: HBM needs some 45 KB an SM under way, and slows down to 86 % when reads press
+// on the writes (32768 rows of 4096, one norm: 161 us with 32 KB ahead, 181 with 64; 16384 of 7168 with an fp32
+// residual and a gate a token, two norms: 250 with 57 KB, 281 with 115; 16384 of 4096, two norms: 82 with 64, 86
+// with 32).  Two norms take longer, so a little more of it waits.
+template <typename T, typename R, int kWarps, int kChunks, int kCtas>
+cudaError_t launch_stream(const moe_norm_args& a, int stage_bytes, int grid_cap, cudaStream_t st) {
+    constexpr int kRing = kRingBytes / kCtas;
+    auto kern = block_norm_stream_kernel<T, R, kWarps, kChunks, kCtas>;
+    const cudaError_t e = ensure_max_dynamic_smem(kern, kRing);
+    if (e != cudaSuccess) return e;
+    const int ahead = (a.post_weight && a.out ? 48 : 40) * 1024 / kCtas;
+    int stages = 1 + (ahead + stage_bytes / 2) / stage_bytes;
+    if (stages < 2) stages = 2;
+    if (stages > kMostStages) stages = kMostStages;
+    if (stages > kRing / stage_bytes) stages = kRing / stage_bytes;
+    int grid = device_info().num_sms * kCtas;
+    if (grid > a.T) grid = a.T;
+    if (grid > grid_cap) grid = grid_cap;
+    return launch_pdl(kern, grid, kWarps * 32, stages * stage_bytes, st, StreamParams{a, stages, stage_bytes});
+}
+// Few warps a row keep a norm's exchange short, and a fitting count of chunks wastes few threads (fp32 weights take
+// twice the registers: twice the warps there).  A row of 7168 takes its CTA some 1.9 us: with bf16 throughout two
+// CTAs an SM hide one another's exchanges (144 us for 16384 rows, 202 with one; two of 16 warps 175, one of 32 204);
+// wide rows with more bytes an element fill HBM with one, and two slow it down (fp32 residual: 213 against 239; 5120
+// elements 154, 171; 4096 with a gate a token 140, 157; but of 4104, 25 KB, one takes 157 and two 132).
 template <typename T, typename R>
 cudaError_t launch_of(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     const int n = (a.hidden / 8 + 31) / 32;  // warps' worth of chunks
+    const int row = a.hidden * (int)(sizeof(T) + (a.resid ? sizeof(R) : 0) + (a.gate && a.gate_rows > 1 ? sizeof(T) : 0));
+    constexpr bool kHalf = sizeof(T) == 2;
+    const bool one = row > 28 * 1024 && row > 5 * a.hidden;
     if (n <= 1) return launch_as<T, R, 1, 1>(a, grid_cap, st);
     if (n <= 2) return launch_as<T, R, 2, 1>(a, grid_cap, st);
-    if (n <= 4) return launch_as<T, R, 4, 1>(a, grid_cap, st);
-    if (n <= 8) return launch_as<T, R, 8, 1>(a, grid_cap, st);
-    if (n <= 16) return launch_as<T, R, 8, 2>(a, grid_cap, st);
-    if (n <= 32) return launch_as<T, R, 16, 2>(a, grid_cap, st);
+    // up to 1024 elements plain loads do as well until rows come in tens an SM (4096 rows of 1024: 7.7 us, staying
+    // CTAs 8.3; 16384: 31 and 26)
+    if (n <= 4 && a.T < 32 * device_info().num_sms) return launch_as<T, R, 4, 1>(a, grid_cap, st);
+    if (n <= 4) return launch_stream<T, R, 4, 1, 8>(a, row, grid_cap, st);
+    if (n <= 8) return launch_stream<T, R, 8, 1, 4>(a, row, grid_cap, st);
+    if (kHalf && n <= 12 && row <= kRingBytes / 8) return launch_stream<T, R, 4, 3, 4>(a, row, grid_cap, st);
+    if (n <= 16)
+        return one ? launch_stream<T, R, 8, 2, 1>(a, row, grid_cap, st) : launch_stream<T, R, 8, 2, 2>(a, row, grid_cap, st);
+    if constexpr (kHalf) {
+        if (n <= 24)
+            return one ? launch_stream<T, R, 8, 3, 1>(a, row, grid_cap, st)
+                       : launch_stream<T, R, 8, 3, 2>(a, row, grid_cap, st);
+        if (n <= 32)
+            return one ? launch_stream<T, R, 8, 4, 1>(a, row, grid_cap, st)
+                       : launch_stream<T, R, 8, 4, 2>(a, row, grid_cap, st);
+        if (row <= kRingBytes / 2) return launch_stream<T, R, 16, 4, 1>(a, row, grid_cap, st);
+    } else if (n <= 32) {
+        return launch_stream<T, R, 16, 2, 1>(a, row, grid_cap, st);
+    }
     return launch_as<T, R, 16, 4>(a, grid_cap, st);
 }
 

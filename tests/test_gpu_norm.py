@@ -76,6 +76,32 @@ def test_in_place_and_ranges():
     run(9, 512, "f32", "f32", std=1e15, post=True)
 
 
+@pytest.mark.parametrize("dtype,resid", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("H", [768, 1024, 1032, 2048, 2056, 4104, 6152, 8192, 16384])
+def test_rows_in_turn(H, dtype, resid):
+    """More rows than a CTA's ring holds, several times over, in place too, and one norm of the two."""
+    run(29, H, dtype, resid, post=True, gate=2, seed=H, max_ctas=2)
+    run(29, H, dtype, resid, post=True, gate=1, seed=H + 1, max_ctas=1, inplace=True)
+    run(29, H, dtype, resid, seed=H + 2, max_ctas=2, inplace=True)
+    run(29, H, dtype, resid, post=True, normed=False, seed=H + 3, max_ctas=1)
+    run(29, H, dtype, None, keep=False, seed=H + 4, max_ctas=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [256, 520, 1024, 2048, 2304, 4096, 5000, 7168, 16384])
+def test_a_row_does_not_depend_on_the_others(H, dtype):
+    T = 5003 if H <= 1024 else 701
+    y, r = torch.randn(T, H, device=DEV).to(TYPES[dtype]), torch.randn(T, H, device=DEV)
+    w, gate = torch.randn(H, device=DEV).to(TYPES[dtype]), torch.randn(T, H, device=DEV).to(TYPES[dtype])
+    out, ro = torch.empty_like(y), torch.empty_like(r)
+    B.moe_block_norm(y, out, w, resid=r, resid_out=ro, post_weight=w, gate=gate)
+    for t in (0, 333, T - 3):
+        some = slice(t, t + 3)
+        o, q = torch.empty_like(y[some]), torch.empty_like(r[some])
+        B.moe_block_norm(y[some], o, w, resid=r[some], resid_out=q, post_weight=w, gate=gate[some])
+        assert torch.equal(o, out[some]) and torch.equal(q, ro[some])
+
+
 def test_many_tokens_and_rows_behind_them():
     T, H = 40001, 256
     y = torch.randn(T, H, device=DEV).to(torch.bfloat16)
