@@ -627,6 +627,7 @@ MOE_API moe_status moe_attn_expanded(const moe_attn_expanded_args* args, int32_t
  *   r' = resid + scale * gate * x           (no resid: 0; no gate: 1)
  *   out = N(r'; pre_weight)
  * in fp32 from end to end, with one rounding each of r' and out (out is normed from r' before its rounding).
+ * A row's result does not depend on the other rows or on max_ctas.  A row of zeros normed with eps 0 is NaN.
  * resid_out may be resid, and out may be y; no other two buffers overlap. */
 typedef struct {
     const void* y;           /* device [T][hidden] of `dtype` */

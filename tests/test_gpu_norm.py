@@ -113,6 +113,28 @@ def test_many_tokens_and_rows_behind_them():
     near(out[:T], want, 40 * U_F32 * np.abs(want), "out")
 
 
+@pytest.mark.parametrize("H", [1024, 8192])
+def test_offsets_past_31_bits(H):
+    T = (1 << 31) // H + 300
+    y, w = torch.full((T, H), 0.5, dtype=torch.bfloat16, device=DEV), torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    tail = torch.randn(300, H, device=DEV).to(torch.bfloat16)
+    y[-300:] = tail
+    B.moe_block_norm(y, y, w)
+    out = torch.empty_like(tail)
+    B.moe_block_norm(tail, out, w)
+    assert torch.equal(y[-300:], out) and torch.all(y[:-300] == 1.0)
+
+
+def test_a_row_of_zeros():
+    y, w = torch.zeros(3, 2048, dtype=torch.bfloat16, device=DEV), torch.ones(2048, dtype=torch.bfloat16, device=DEV)
+    y[1] = 1.0
+    out = torch.empty_like(y)
+    B.moe_block_norm(y, out, w, eps=1e-6)
+    assert torch.all(out[[0, 2]] == 0.0) and torch.all(out[1] == 1.0)
+    B.moe_block_norm(y, out, w, eps=0.0)
+    assert torch.all(out[[0, 2]].isnan()) and torch.all(out[1] == 1.0)
+
+
 def test_stream_and_graph():
     y, r = torch.randn(64, 2048, device=DEV).to(torch.bfloat16), torch.randn(64, 2048, device=DEV)
     w, out, ro = torch.ones(2048, dtype=torch.bfloat16, device=DEV), torch.empty_like(y), torch.empty_like(r)
