@@ -628,7 +628,9 @@ MOE_API moe_status moe_attn_expanded(const moe_attn_expanded_args* args, int32_t
  *   out = N(r'; pre_weight)
  * in fp32 from end to end, with one rounding each of r' and out (out is normed from r' before its rounding).
  * A row's result does not depend on the other rows or on max_ctas.  A row of zeros normed with eps 0 is NaN.
- * resid_out may be resid, and out may be y; no other two buffers overlap. */
+ * resid_out may be resid, and out may be y; no other two buffers overlap.
+ * Rows of more than 512 numbers are copied ahead, with bounded waits.  One that runs out makes its CTA's rows from there
+ * on NaN, in out and resid_out, and is told by moe_comm_error. */
 typedef struct {
     const void* y;           /* device [T][hidden] of `dtype` */
     const void* post_weight; /* device [hidden] of `dtype` or NULL: y is taken as it is */
@@ -696,14 +698,14 @@ MOE_API moe_status moe_draft_verify_ex(int32_t B, int32_t N, int32_t vocab, int3
  * skips its work, frees its tensor memory and returns normally, so the context stays
  * usable.  So does the first CTA (pair) of an attention kernel, while the others do their work.  The staged combine kernel takes the same
  * path (its error goes to the layer's err_flag, or, called on its own, to the word
- * moe_comm_error reads).
+ * moe_comm_error reads), and so does the first CTA of moe_block_norm's kernel for wide rows, with copies in flight.
  * enable = 0 (the default) turns it off.  Process-wide, host-side only;
  * enable != 0 with timeout_ns <= 0 is MOE_ERR_INVALID_ARG. */
 MOE_API moe_status moe_debug_inject_wait(int32_t enable, int64_t timeout_ns);
 
 /* ---------------------------------------------------------------------------
- * moe_comm_error -- the library's sticky error word for moe_combine, whose signature
- * carries no error flag: MOE_ERR_TIMEOUT once a bounded wait of its staged kernel ran
+ * moe_comm_error -- the library's sticky error word for moe_combine and moe_block_norm, whose
+ * arguments carry no error flag: MOE_ERR_TIMEOUT once a bounded wait of one of their kernels ran
  * out on the current device (never on a healthy GPU; see moe_debug_inject_wait), else
  * 0.  (moe_dispatch has no waits.)  Synchronises the current device, writes the word to
  * *code (host), and resets it to 0 when clear != 0.  code NULL: MOE_ERR_INVALID_ARG. */

@@ -173,12 +173,18 @@ moe_status moe_debug_inject_wait(int32_t enable, int64_t timeout_ns) {
 
 moe_status moe_comm_error(int32_t* code, int32_t clear) {
     if (!code) return MOE_ERR_INVALID_ARG;
-    int32_t* word = comm_error_word();
-    if (!word) return MOE_ERR_CUDA;
+    int32_t* words[] = {comm_error_word(), norm_error_word()};
     cudaError_t e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) e = cudaMemcpy(code, word, sizeof(int32_t), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && clear) e = cudaMemset(word, 0, sizeof(int32_t));
+    int32_t first = 0;
+    for (int32_t* word : words) {
+        if (!word) return MOE_ERR_CUDA;
+        int32_t one = 0;
+        if (e == cudaSuccess) e = cudaMemcpy(&one, word, sizeof(int32_t), cudaMemcpyDeviceToHost);
+        if (e == cudaSuccess && clear) e = cudaMemset(word, 0, sizeof(int32_t));
+        if (first == 0) first = one;
+    }
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) *code = first;
     return cuda_status(e);
 }
 

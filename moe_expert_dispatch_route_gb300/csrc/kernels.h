@@ -35,6 +35,9 @@ int64_t wait_injection_ns();
 // word: the staged combine kernel called on its own (no caller flag) stores
 // MOE_ERR_TIMEOUT there when a bounded wait runs out.  NULL if it cannot be looked up.
 int32_t* comm_error_word();
+// norm.cu: the same for moe_block_norm, whose kernel knows its word's address by itself (no lookup on
+// the way of a call, which may be captured).
+int32_t* norm_error_word();
 // Raises the dynamic shared memory limit of a kernel to `bytes`, once per context
 // (thread-safe); later calls in the same context return at once.
 cudaError_t ensure_max_dynamic_smem(const void* func, int bytes);

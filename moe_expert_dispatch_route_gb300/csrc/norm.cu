@@ -165,7 +165,9 @@ constexpr int kRingBytes = 208 * 1024;  // of an SM's CTAs together
 struct StreamParams {
     moe_norm_args a;
     int stages, stage_bytes;  // a stage: one row of y, residual and gate
+    int64_t inject_ns;
 };
+__device__ int32_t g_norm_error;  // read by moe_comm_error: MOE_ERR_TIMEOUT once a wait has run out
 template <typename T>
 struct Packed8;  // 8 elements as they are stored
 template <>
@@ -188,18 +190,41 @@ struct Packed8<__nv_bfloat16> {
     __device__ __forceinline__ void shared(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void to(float (&x)[8]) const { unpack8(v, x); }
 };
+// A CTA whose wait for its row-th row ran out: no row is copied any more, those under way land (or a bounded wait
+// gives up) before the CTA ends, and its rows from that one on are void: NaN.
+template <typename T, typename R, int kLanes>
+__device__ __noinline__ void leave(const StreamParams& sp, uint64_t* full, uint64_t* never, int row) {
+    const moe_norm_args& a = sp.a;
+    const int64_t first = blockIdx.x + (int64_t)row * gridDim.x;
+    if (threadIdx.x == 0) {
+        if (sp.inject_ns > 0) tc::wait_on_nothing(never, (uint64_t)sp.inject_ns);
+        set_err(&g_norm_error, MOE_ERR_TIMEOUT);
+        for (int i = 0; i < sp.stages && first + (int64_t)i * gridDim.x < a.T; ++i)
+            tc::mbar_wait_bounded(&full[(row + i) % sp.stages], (row + i) / sp.stages & 1);
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    const float none[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+    for (int64_t t = first; t < a.T; t += gridDim.x)
+        for (int c = threadIdx.x; c < a.hidden / 8; c += kLanes) {
+            if (a.resid_out) store8(static_cast<R*>(a.resid_out) + t * a.hidden + c * 8, none);
+            if (a.out) store8(static_cast<T*>(a.out) + t * a.hidden + c * 8, none);
+        }
+}
 template <typename T, typename R, int kWarps, int kChunks, int kCtas>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(const __grid_constant__ StreamParams sp) {
     constexpr int kLanes = 32 * kWarps;
     const moe_norm_args& a = sp.a;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(16) float sums[2][kWarps];
-    __shared__ uint64_t full[kMostStages];
+    __shared__ uint64_t full[kMostStages], never;
+    __shared__ int gave_up;  // the CTA's row whose wait ran out first
     const int tid = threadIdx.x, warp = tid >> 5, H = a.hidden, chunks = H / 8;
     const int y_bytes = H * (int)sizeof(T), r_bytes = a.resid ? H * (int)sizeof(R) : 0;
     const bool gates = a.gate && a.gate_rows > 1;
     if (tid == 0) {
         for (int i = 0; i < sp.stages; ++i) tc::mbar_init(&full[i], 1);
+        tc::mbar_init(&never, 1);
+        gave_up = INT32_MAX;
         tc::fence_barrier_init();
     }
     __syncthreads();
@@ -225,15 +250,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(c
         if (a.gate && !gates) g[i].load(static_cast<const T*>(a.gate) + c * 8);
     }
     const float inv_n = 1.0f / (float)H;
-    int st = 0, turn = 0;
+    volatile int* left = &gave_up;
+    const bool hook = sp.inject_ns > 0 && blockIdx.x == 0;  // test hook: as if the first row's wait had run out
+    int st = 0, turn = 0, row = 0;
     uint32_t parity = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const bool landed = tc::mbar_wait_bounded(&full[st], parity);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, ++row) {
+        const bool landed = tc::mbar_wait_bounded(&full[st], parity) && !hook;
+        if (!landed) atomicMin(&gave_up, row);
         const uint8_t* at = ring + st * sp.stage_bytes;
         const T *y = reinterpret_cast<const T*>(at), *gate = reinterpret_cast<const T*>(at + y_bytes + r_bytes);
         const R* resid = reinterpret_cast<const R*>(at + y_bytes);
-        const float scale = landed ? a.scale : __int_as_float(0x7fc00000);  // a wait that gave up: NaN, not an old row
-        float f = 1.0f, sum = 0.0f;
+        const float start = landed ? 0.0f : __int_as_float(0x7fc00000);  // of a sum: a wait that gave up makes it NaN
+        float f = 1.0f, sum = start;
         if (post) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
@@ -246,7 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(c
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
             }
-            f = inv_rms<kWarps>(sum, sums[turn], warp, inv_n, a.eps), turn ^= 1, sum = 0.0f;
+            f = inv_rms<kWarps>(sum, sums[turn], warp, inv_n, a.eps), turn ^= 1, sum = start;
         }
         float r[kChunks][8];
 #pragma unroll
@@ -277,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(c
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                r[i][j] = fmaf(scale, x[j], r[i][j]);
+                r[i][j] = fmaf(a.scale, x[j], r[i][j]);
                 sum = fmaf(r[i][j], r[i][j], sum);
             }
             if (a.resid_out) store8(static_cast<R*>(a.resid_out) + t * H + c * 8, r[i]);
@@ -286,7 +314,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(c
             f = inv_rms<kWarps>(sum, sums[turn], warp, inv_n, a.eps), turn ^= 1;
         else
             __syncthreads();
-        // behind this barrier every thread has read its numbers: the stage takes another row
+        // behind this barrier a wait of this row that ran out is known to all (by its number: a faster thread may tell of
+        // the next row's already), through the norm's sum where there is one: reading the word for every row costs 3 %
+        if ((!a.out || f != f) && *left <= row) break;
+        // and every thread has read its numbers: the stage takes another row
         if (tid == 0) fetch(t + (int64_t)sp.stages * gridDim.x, st);
         if (++st == sp.stages) st = 0, parity ^= 1u;
         if (!a.out) continue;
@@ -301,6 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) block_norm_stream_kernel(c
             store8(static_cast<T*>(a.out) + t * H + c * 8, r[i]);
         }
     }
+    if (*left != INT32_MAX) leave<T, R, kLanes>(sp, full, &never, *left);
 }
 
 template <typename T, typename R, int kWarps, int kChunks>
@@ -328,7 +360,7 @@ cudaError_t launch_stream(const moe_norm_args& a, int stage_bytes, int grid_cap,
     int grid = device_info().num_sms * kCtas;
     if (grid > a.T) grid = a.T;
     if (grid > grid_cap) grid = grid_cap;
-    return launch_pdl(kern, grid, kWarps * 32, stages * stage_bytes, st, StreamParams{a, stages, stage_bytes});
+    return launch_pdl(kern, grid, kWarps * 32, stages * stage_bytes, st, StreamParams{a, stages, stage_bytes, wait_injection_ns()});
 }
 // Few warps a row keep a norm's exchange short, and a fitting count of chunks wastes few threads (fp32 weights take
 // twice the registers: twice the warps there).  A row of 7168 takes its CTA some 1.9 us: with bf16 throughout two
@@ -366,6 +398,11 @@ cudaError_t launch_of(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
 }
 
 }  // namespace
+
+int32_t* norm_error_word() {
+    void* p = nullptr;
+    return cudaGetSymbolAddress(&p, g_norm_error) == cudaSuccess ? static_cast<int32_t*>(p) : nullptr;
+}
 
 cudaError_t launch_block_norm(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     const bool f = a.dtype == MOE_F32, rf = a.resid_dtype == MOE_F32;
