@@ -850,7 +850,9 @@ cudaError_t launch_attn_latent(const moe_latent_cache& c, const moe_attn_args& a
     const cudaError_t e = pairs  ? launch_latent_pair(c, lp, grid, st)
                           : tree ? launch_of<true>(c, lp, rows, grid, st)
                                  : launch_of<false>(c, lp, rows, grid, st);
-    if (e != cudaSuccess || p.max_kv <= kKeyTile) return e;  // a tile of one unit is never split
+    // a boundary that locate() leaves inside a tile lies behind its item_cost and the first key tile, and before the
+    // item_slack last ones: tiles of fewer key tiles than that, and those of a single team, are never split
+    if (e != cudaSuccess || p.max_kv <= (p.item_slack + 1) * kKeyTile || grid == team) return e;
     const int join = 2 * grid < max_ctas ? 2 * grid : max_ctas;
     return launch_pdl(attn_latent_join_kernel, join, kJoinThreads, 0, st, lp, grid);
 }
