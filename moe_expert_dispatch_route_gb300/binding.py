@@ -436,6 +436,14 @@ def _table_ok(where, t, B):
         raise ValueError(f"{where}: the block table is packed int32 [{B}][pages], got {t.dtype} {tuple(t.shape)}")
 
 
+def _strides(t):
+    """Row and head strides of t [rows][heads][width].  That of an index with one value is not used, and may be any
+    number: the packed one is passed on."""
+    rows, heads, width = t.shape
+    head = t.stride(1) if heads > 1 else width
+    return t.stride(0) if rows > 1 else heads * head, head
+
+
 def moe_attn_workspace_size(cache: MoeKvCache, num_q_heads: int) -> int:
     return int(lib().moe_attn_workspace_size(ctypes.byref(cache), num_q_heads))
 
@@ -461,9 +469,9 @@ def _attn_args(where, q, o, cu_q, kv_len, block_table, max_q, max_kv, scale, cau
     if lse is not None:
         _same(f"{where}: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
     size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    args = MoeAttnArgs(_ptr(q), _ptr(o), _ptr(lse), q.stride(0), q.stride(1), o.stride(0), o.stride(1), _ptr(cu_q),
-                       _ptr(kv_len), _ptr(block_table), block_table.shape[1], T, B, max_q, max_kv, H, float(scale),
-                       int(causal), window, _ptr(err_flag), _ptr(workspace), size)
+    args = MoeAttnArgs(_ptr(q), _ptr(o), _ptr(lse), *_strides(q), *_strides(o), _ptr(cu_q), _ptr(kv_len),
+                       _ptr(block_table), block_table.shape[1], T, B, max_q, max_kv, H, float(scale), int(causal), window,
+                       _ptr(err_flag), _ptr(workspace), size)
     args.head_dim = D  # the C structure has no field for it: the cache's is meant
     args.keep = (q, o, lse, cu_q, kv_len, block_table, err_flag, workspace)  # it holds their addresses
     return args
@@ -572,10 +580,10 @@ def attn_expanded_args(q, k, k_rope, v, o, cu_q, cu_kv, max_q, max_kv, scale, ca
     if lse is not None:
         _same("attn_expanded_args: lse", (lse.shape, (T, H)), (lse.dtype, torch.float32), (lse.is_contiguous(), True))
     size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    args = MoeAttnExpandedArgs(_ptr(q), _ptr(k), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), q.stride(0), q.stride(1),
-                               k.stride(0), k.stride(1), k_rope.stride(0), v.stride(0), v.stride(1), o.stride(0),
-                               o.stride(1), _ptr(cu_q), _ptr(cu_kv), T, S, B, max_q, max_kv, H, float(scale),
-                               int(causal), _ptr(err_flag), _ptr(workspace), size)
+    args = MoeAttnExpandedArgs(_ptr(q), _ptr(k), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), *_strides(q), *_strides(k),
+                               k_rope.stride(0) if S > 1 else ROPE, *_strides(v), *_strides(o), _ptr(cu_q), _ptr(cu_kv),
+                               T, S, B, max_q, max_kv, H, float(scale), int(causal), _ptr(err_flag), _ptr(workspace),
+                               size)
     args.keep = (q, k, k_rope, v, o, lse, cu_q, cu_kv, err_flag, workspace)  # it holds their addresses
     return args
 
