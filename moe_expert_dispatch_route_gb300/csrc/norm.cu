@@ -366,7 +366,8 @@ cudaError_t launch_stream(const moe_norm_args& a, int stage_bytes, int grid_cap,
 // twice the registers: twice the warps there).  A row of 7168 takes its CTA some 1.9 us: with bf16 throughout two
 // CTAs an SM hide one another's exchanges (144 us for 16384 rows, 202 with one; two of 16 warps 175, one of 32 204);
 // wide rows with more bytes an element fill HBM with one, and two slow it down (fp32 residual: 213 against 239; 5120
-// elements 154, 171; 4096 with a gate a token 140, 157; but of 4104, 25 KB, one takes 157 and two 132).
+// elements 154, 171; 4096 with a gate a token 140, 157; but of 4104, 25 KB, one takes 157 and two 132).  `one` says
+// that: more than five bytes an element are an fp32 residual, a gate a token beside a residual, or fp32 rows with either.
 template <typename T, typename R>
 cudaError_t launch_of(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     const int n = (a.hidden / 8 + 31) / 32;  // warps' worth of chunks
@@ -379,8 +380,14 @@ cudaError_t launch_of(const moe_norm_args& a, int grid_cap, cudaStream_t st) {
     // CTAs 8.3; 16384: 31 and 26)
     if (n <= 4 && a.T < 32 * device_info().num_sms) return launch_as<T, R, 4, 1>(a, grid_cap, st);
     if (n <= 4) return launch_stream<T, R, 4, 1, 8>(a, row, grid_cap, st);
+    // up to 2048: a chunk a thread, four CTAs an SM (16384 rows of 2048, bf16: 45 us; two CTAs 57, plain loads 53, four
+    // warps of two chunks 46; 4096 of 1536: 11.4, 15.8, 13.5, 12.2; of 2048 with an fp32 residual two CTAs would take
+    // 64 of these 70, and 86 of 95 in fp32 throughout)
     if (n <= 8) return launch_stream<T, R, 8, 1, 4>(a, row, grid_cap, st);
-    if (kHalf && n <= 12 && row <= kRingBytes / 8) return launch_stream<T, R, 4, 3, 4>(a, row, grid_cap, st);
+    // a little above, three chunks a thread of four warps waste fewer threads than two of eight (16384 rows of 2560,
+    // bf16: 53 us, 74; 4096: 16.5, 22.1; with an fp32 residual 85, 79 and 23.0, 22.5)
+    if constexpr (kHalf)
+        if (n <= 12) return launch_stream<T, R, 4, 3, 4>(a, row, grid_cap, st);
     if (n <= 16)
         return one ? launch_stream<T, R, 8, 2, 1>(a, row, grid_cap, st) : launch_stream<T, R, 8, 2, 2>(a, row, grid_cap, st);
     if constexpr (kHalf) {
