@@ -1,8 +1,9 @@
 // Latent attention, expanded form, for prompts: every head has its own keys (128 numbers, and 64 that all heads
 // share) and values (128).  Bound by the tensor cores; the pipeline is attn_tile.cuh's: a query tile is two
 // halves of 128 rows (here tokens of one head) over the same key tiles, and while the softmax of one half
-// runs, the tensor cores work on the other.  A prompt of 8192 tokens with 128 heads takes 2.00-2.11 ms from box to box,
-// 1300-1370 TFLOP/s; ragged prompts of up to 1100 new tokens with 16 heads 85 us.
+// runs, the tensor cores work on the other.  A prompt of 8192 tokens with 128 heads takes 1.87-2.11 ms from box to box,
+// 1300-1470 TFLOP/s, and 2.20 once a busy GPU is at its power cap; ragged prompts of up to 1100 new tokens with 16 heads
+// 85 us.
 //   S = Q K^T    k = 192: 12 instructions of 128 rows x 128 keys      O += P V    8 of 128 rows x 128 columns
 // Scores, probabilities and output fill tensor memory as there (S0 | S1 | O0 | O1, P over S).
 //

@@ -11,8 +11,8 @@
 // MMAs' operands stays in its CTA.
 //
 // What bounds it now: 2370 cycles for 64 keys, of which the MMAs last 1100 and a softmax 1100; the scores wait for
-// keys, which come about 3000 cycles after they are asked for, and two stages of them fill shared memory (HBM
-// alone would take 1570).  Three stages with one of values 222 us, keys in thirds 152-168, tiles fetched into L2
+// keys, which come about 3000 cycles after they are asked for, and with Q beside them two stages fill shared memory (HBM
+// alone would take 1570; tensor memory has 192 columns left, which are not used).  Three stages with one of values 222 us, keys in thirds 152-168, tiles fetched into L2
 // ahead of time 175.
 //
 // The running maximum is followed loosely, as in attn_tile.cuh.  Split tiles are joined by attn_latent.cu's
@@ -48,8 +48,11 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
 }
 // Arrives on an mbarrier of another CTA of the cluster, ordered after what this CTA has done, at its own scope: what
 // is told is that this SM's tensor core may read this CTA's shared memory (its writers' proxy fences come
-// before), or write its tensor memory.  No thread of the other CTA reads any of it.  (Released at cluster scope, an
-// arrival took 1900 cycles to be seen, on the chain that bounds the kernel.)
+// before), or write its tensor memory.  No thread of the other CTA reads any of it.  PTX's memory model does not
+// cover that: a release at this scope orders nothing for a thread of the other CTA, the one that issues the MMA.  That the
+// reader is the writers' own SM, whose shared memory holds what they have fenced, is a property of this chip (sm_103a),
+// which is all this file is compiled for.  (Released at cluster scope, an arrival took 1900 cycles to be seen, on the
+// chain that bounds the kernel: 210 us where this takes 150.)
 __device__ __forceinline__ void mbar_tell_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

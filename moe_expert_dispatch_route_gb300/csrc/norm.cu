@@ -6,7 +6,7 @@
 // row's result never depends on how many there are): CTAs that stay, with rows copied ahead, and, for narrow rows
 // and those of which two do not fit an SM, plain loads into registers.
 // 16384 rows of 7168, bf16 with an fp32 residual, both norms and a gate, 1.41 GB: 213 us (6.6 TB/s; 234 with plain
-// loads); bf16 throughout 144 (188); 16384 of 4096 82 (128); 4096 of 16384 83 (166); 64 rows of 2048 2.4 us.
+// loads); bf16 throughout 146 (188); 16384 of 4096 82 (128); 4096 of 16384 86 (166); 64 rows of 2048 2.5 us.
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kCtaThreads<kWarps>, kChunks <= 2 ? 3 : 1)
 // CTAs that stay take the rows in turn.  The rows to come are copied into shared memory while one is normed, so
 // the reads of HBM never wait for a norm's two exchanges, and a thread keeps its elements' weights in registers, as
 // they are stored, from the first row on (loaded again for each row, 28 KB for 14 of y, they come from L2: 167 us
-// where 144 are reached).  The row itself is read from shared memory twice: held in registers it spills (215).
+// where 146 are reached).  The row itself is read from shared memory twice: held in registers it spills (215).
 constexpr int kMostStages = 8;
 constexpr int kRingBytes = 208 * 1024;  // of an SM's CTAs together
 struct StreamParams {
@@ -364,7 +364,7 @@ cudaError_t launch_stream(const moe_norm_args& a, int stage_bytes, int grid_cap,
 }
 // Few warps a row keep a norm's exchange short, and a fitting count of chunks wastes few threads (fp32 weights take
 // twice the registers: twice the warps there).  A row of 7168 takes its CTA some 1.9 us: with bf16 throughout two
-// CTAs an SM hide one another's exchanges (144 us for 16384 rows, 202 with one; two of 16 warps 175, one of 32 204);
+// CTAs an SM hide one another's exchanges (146 us for 16384 rows, 202 with one; two of 16 warps 175, one of 32 204);
 // wide rows with more bytes an element fill HBM with one, and two slow it down (fp32 residual: 213 against 239; 5120
 // elements 154, 171; 4096 with a gate a token 140, 157; but of 4104, 25 KB, one takes 157 and two 132).  `one` says
 // that: more than five bytes an element are an fp32 residual, a gate a token beside a residual, or fp32 rows with either.
